@@ -56,7 +56,8 @@ extern "C" {
 #define GMM_ERR_UNSUPPORTED    -2  /* valid request outside what the kernels implement (e.g. too many groups) */
 #define GMM_ERR_CUDA           -3  /* a CUDA runtime/driver call failed (allocation, launch, copy) */
 #define GMM_ERR_DEVICE_TIMEOUT -4  /* a kernel gave up waiting on its own pipeline (reported by gmm_query_status) */
-#define GMM_ERR_BAD_INPUT      -5  /* decreasing a_offsets or an expert id >= num_experts (gmm_query_status) */
+#define GMM_ERR_BAD_INPUT      -5  /* decreasing a_offsets, or an expert id, slot or row index past its range
+                                      (gmm_query_status) */
 #define GMM_ERR_NO_DEVICE      -6  /* the device is not an sm_103 GPU, or none is present */
 
 typedef struct gmm_ctx *gmm_handle_t;
@@ -208,6 +209,133 @@ int gmm_run_planes(gmm_handle_t h, void *c, const void *a, const uint32_t *a_off
 int gmm_run_fp8(gmm_handle_t h, void *c, const void *a, const uint32_t *a_offsets, const void *b,
                 const int32_t *expert_ids, uint32_t *expert_usage_stats, int num_groups, int N, int K,
                 const float *input_scale, const float *weight_scale, const int *scales_granularity_mnk,
+                const gmm_epilogue *epilogue, cudaStream_t stream);
+
+/*
+ * Tokens sorted by expert and back.  A router gives token t its top_k experts; slot
+ * s = t * top_k + j is its j-th.  Rows (the grouped calls' A and C) hold one slot each, all
+ * slots of expert 0 first, then expert 1, ..., each expert's in ascending slot order.
+ * The calls below are asynchronous on `stream`, allocate nothing, can be captured in a CUDA
+ * graph, and give the same bits every time.  Element types of the moved rows:
+ */
+#define GMM_DTYPE_BF16 0
+#define GMM_DTYPE_FP16 1
+#define GMM_DTYPE_FP32 2
+
+/*
+ * Sort the slots by expert and copy the tokens to their rows.
+ *   slot_experts : int32 [num_tokens, top_k]; a negative id drops the slot, an id
+ *                  >= num_experts (the handle's) drops it and is reported as
+ *                  GMM_ERR_BAD_INPUT by gmm_query_status.  A token may name an expert twice.
+ *   a_offsets    : uint32 [num_experts + 1], written: the prefix sum of rows per expert, for
+ *                  grouped calls with num_groups = num_experts and expert_ids = 0, 1, ....
+ *   slot_rows    : int32 [num_tokens, top_k], written: each slot's row, -1 for a dropped one.
+ *   row_slots    : int32 [num_tokens * top_k], written: each row's slot, -1 for the rows at
+ *                  and past a_offsets[num_experts].
+ *   rows         : [num_tokens * top_k, width], contiguous, written below
+ *                  a_offsets[num_experts]: rows[r, :] = tokens[row_slots[r] / top_k, :].
+ *   tokens       : [num_tokens, width] of `dtype`, rows tokens_stride elements apart (0: one
+ *                  row for all).  rows and tokens both NULL: only the sort.
+ * The gradient of the copy, d_tokens[t, :] = sum_j d_rows[slot_rows[t, j], :], is
+ * gmm_combine without weights.
+ * num_tokens == 0 writes a_offsets only.
+ * Errors (nothing is launched): GMM_ERR_INVALID_ARG (NULL or misaligned for its element
+ * type, negative size, unknown dtype, only one of rows and tokens), GMM_ERR_UNSUPPORTED
+ * (top_k > 32, more than 2^30 slots, more than 4096 experts), GMM_ERR_CUDA.
+ */
+int gmm_dispatch(gmm_handle_t h, uint32_t *a_offsets, int32_t *slot_rows, int32_t *row_slots, void *rows,
+                 const int32_t *slot_experts, const void *tokens, long long tokens_stride, int num_tokens, int top_k,
+                 int width, int dtype, cudaStream_t stream);
+
+/*
+ * Rows back to tokens, weighted:
+ *     out[t, :] = sum_j weights[t, j] * rows[slot_rows[t, j], :]
+ * summed in fp32 in ascending j and rounded once; a negative slot_rows entry adds nothing
+ * (a token with none gets zeros), one >= num_rows adds nothing and is reported as
+ * GMM_ERR_BAD_INPUT.
+ *   out: [num_tokens, width] of `dtype`, rows out_stride (>= width) elements apart;
+ *   rows: [num_rows, width], contiguous; slot_rows: int32 [num_tokens, top_k];
+ *   weights: fp32 [num_tokens, top_k], or NULL for ones.
+ * Errors: as gmm_dispatch (the number of experts does not matter).
+ */
+int gmm_combine(gmm_handle_t h, void *out, long long out_stride, const void *rows, int num_rows, const int32_t *slot_rows,
+                const float *weights, int num_tokens, int top_k, int width, int dtype, cudaStream_t stream);
+
+/*
+ * The gradient of gmm_combine:
+ *     d_rows[slot_rows[t, j], :] = weights[t, j] * d_out[t, :]
+ *     d_weights[t, j] = sum_n d_out[t, n] * rows[slot_rows[t, j], n]     (0 for a dropped slot)
+ *   d_rows: [num_rows, width], contiguous; rows that no slot names stay untouched;
+ *   d_weights: fp32 [num_tokens, top_k], or NULL (rows may then be NULL too);
+ *   d_out: [num_tokens, width], rows d_out_stride elements apart (0: one row for all);
+ *   rows, slot_rows, weights: as gmm_combine took them.
+ * Products and sums in fp32 (each element of d_rows rounded once).  Errors: as gmm_combine.
+ */
+int gmm_combine_grad(gmm_handle_t h, void *d_rows, float *d_weights, const void *d_out, long long d_out_stride,
+                     const void *rows, int num_rows, const int32_t *slot_rows, const float *weights, int num_tokens,
+                     int top_k, int width, int dtype, cudaStream_t stream);
+
+/*
+ * Microscaled 4-bit floating point.  A value is e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives) times its block's scale; blocks run along K.
+ *   GMM_FP4_NV (nvfp4): blocks of 16, e4m3 scales, and an optional fp32 scale of the whole
+ *                       tensor (of each expert's weights).
+ *   GMM_FP4_MX (mxfp4): blocks of 32, e8m0 scales (powers of two: 2^(code - 127)).
+ * packed: uint8 [rows, K / 2], element k in nibble k % 2 of byte k / 2, low nibble first.
+ * scales: uint8 [rows, GMM_FP4_SCALE_PITCH(K, block)]: one byte per block, each row padded to
+ * a multiple of 16 bytes.
+ */
+#define GMM_FP4_NV 0
+#define GMM_FP4_MX 1
+#define GMM_FP4_SCALE_PITCH(K, block) ((((K) / (block)) + 15) / 16 * 16)
+
+/*
+ * Quantise rows of x, optionally gathered:
+ *     source row of r: row_slots ? row_slots[r] / top_k : r
+ *   nvfp4: s = e4m3(amax / (6 g)), q = e2m1(x / (s g)), g = *global_scale (1 when NULL; it
+ *          must be finite and above zero);
+ *   mxfp4: s = 2^(floor(log2 amax) - 2), q = e2m1(x / s); global_scale must be NULL;
+ * with amax the block's largest magnitude, every step rounded to nearest even in fp32, and
+ * saturation at 448 and 6.  s = 0 gives q = 0.  A block that holds an infinity or a NaN gets
+ * a NaN scale and zero codes.
+ *   packed, scales: as above, 16-byte aligned; padding bytes of a scale row are zeroed;
+ *   x: [src_rows, K] of `dtype`, rows x_stride elements apart (0: one row for all);
+ *   row_slots: int32 [rows] (gmm_dispatch's row_slots) or NULL; a row with a negative entry
+ *   stays untouched, one whose source row is past src_rows too and is reported as
+ *   GMM_ERR_BAD_INPUT.
+ * Requirements: K a multiple of 32.  rows == 0 launches nothing.
+ * Errors (nothing is launched): GMM_ERR_INVALID_ARG, GMM_ERR_UNSUPPORTED (K > 2^24),
+ * GMM_ERR_CUDA.
+ */
+int gmm_quantize_fp4(gmm_handle_t h, void *packed, void *scales, const void *x, long long x_stride, int src_rows,
+                     const int32_t *row_slots, int top_k, const float *global_scale, int rows, int K, int dtype,
+                     int format, cudaStream_t stream);
+
+/*
+ * The values that packed and scales stand for: y[r, k] = q * (s * g), of `dtype`, rows
+ * y_stride (>= K) elements apart.  The other arguments and the errors are those of
+ * gmm_quantize_fp4.
+ */
+int gmm_dequantize_fp4(gmm_handle_t h, void *y, long long y_stride, const void *packed, const void *scales,
+                       const float *global_scale, int rows, int K, int dtype, int format, cudaStream_t stream);
+
+/*
+ * The grouped GEMM on microscaled 4-bit operands:
+ *     C[r, n] = bf16( ga * gb[e] * sum_k sa[r, k / block] * qa[r, k] * sb[e, n, k / block] * qb[e, n, k] )
+ * for the rows and groups of gmm_run, then the optional epilogue; the sums are fp32 on the
+ * tensor cores.
+ *   a: packed [rows, K / 2]; a_scales [rows, pitch]; b: packed [num_experts, N, K / 2];
+ *   b_scales [num_experts, N, pitch] with pitch = GMM_FP4_SCALE_PITCH(K, block), all 16-byte
+ *   aligned, both operands of `format`; a_global: fp32, one value, b_global: fp32
+ *   [num_experts], each NULL for ones; c and the rest as gmm_run.
+ * Requirements: those of gmm_run with K a multiple of 32.  Padding bytes of the scales are
+ * not used.  With num_groups == 0, c, a and a_scales may be NULL.
+ * Errors: as gmm_run_ex, plus GMM_ERR_INVALID_ARG for an unknown format and NULL or
+ * misaligned scales, GMM_ERR_UNSUPPORTED where the device cannot run the CTA-pair kernel.
+ */
+int gmm_run_fp4(gmm_handle_t h, void *c, const void *a, const uint32_t *a_offsets, const void *b,
+                const int32_t *expert_ids, uint32_t *expert_usage_stats, int num_groups, int N, int K,
+                const void *a_scales, const void *b_scales, int format, const float *a_global, const float *b_global,
                 const gmm_epilogue *epilogue, cudaStream_t stream);
 
 /*

@@ -32,7 +32,8 @@ GMM_ERR_BAD_INPUT = -5
 GMM_ERR_NO_DEVICE = -6
 
 EXPORTED = ("gmm_create", "gmm_run", "gmm_run_ex", "gmm_run_int4", "gmm_run_int4_ex", "gmm_matmul_int4",
-            "gmm_run_fp8", "gmm_run_planes", "gmm_run_noalloc", "gmm_query_status", "gmm_error_string", "gmm_destroy")
+            "gmm_run_fp8", "gmm_run_planes", "gmm_run_noalloc", "gmm_query_status", "gmm_error_string", "gmm_destroy",
+            "gmm_dispatch", "gmm_combine", "gmm_combine_grad", "gmm_quantize_fp4", "gmm_dequantize_fp4", "gmm_run_fp4")
 
 # Activations of the optional epilogue (GMM_ACT_* in gmm.h).
 GMM_ACT_NONE = 0
@@ -40,6 +41,15 @@ GMM_ACT_RELU = 1
 GMM_ACT_SILU = 2
 GMM_ACT_GELU_TANH = 3
 ACTIVATIONS = {"none": GMM_ACT_NONE, "relu": GMM_ACT_RELU, "silu": GMM_ACT_SILU, "gelu_tanh": GMM_ACT_GELU_TANH}
+
+# Element types of the moved rows (GMM_DTYPE_*) and 4-bit formats (GMM_FP4_*) in gmm.h.
+GMM_DTYPE_BF16 = 0
+GMM_DTYPE_FP16 = 1
+GMM_DTYPE_FP32 = 2
+GMM_FP4_NV = 0
+GMM_FP4_MX = 1
+FP4_FORMATS = {"nvfp4": GMM_FP4_NV, "mxfp4": GMM_FP4_MX}
+FP4_BLOCKS = {GMM_FP4_NV: 16, GMM_FP4_MX: 32}
 
 
 class GmmEpilogue(ctypes.Structure):
@@ -88,6 +98,19 @@ def load_library(path: str | None = None):
     lib.gmm_matmul_int4.restype = I
     lib.gmm_run_noalloc.argtypes = [P, P, P, P, P, P, I, I, I, I, P]
     lib.gmm_run_noalloc.restype = I
+    L = ctypes.c_longlong
+    lib.gmm_dispatch.argtypes = [P, P, P, P, P, P, P, L, I, I, I, I, P]
+    lib.gmm_dispatch.restype = I
+    lib.gmm_combine.argtypes = [P, P, L, P, I, P, P, I, I, I, I, P]
+    lib.gmm_combine.restype = I
+    lib.gmm_combine_grad.argtypes = [P, P, P, P, L, P, I, P, P, I, I, I, I, P]
+    lib.gmm_combine_grad.restype = I
+    lib.gmm_quantize_fp4.argtypes = [P, P, P, P, L, I, P, I, P, I, I, I, I, P]
+    lib.gmm_quantize_fp4.restype = I
+    lib.gmm_dequantize_fp4.argtypes = [P, P, L, P, P, P, I, I, I, I, P]
+    lib.gmm_dequantize_fp4.restype = I
+    lib.gmm_run_fp4.argtypes = [P, P, P, P, P, P, P, I, I, I, P, P, I, P, P, EP, P]
+    lib.gmm_run_fp4.restype = I
     lib.gmm_query_status.argtypes = [P, P]
     lib.gmm_query_status.restype = I
     lib.gmm_error_string.argtypes = [I]
@@ -371,6 +394,237 @@ def gmm_matmul_int4(h: Handle, c, a, b_packed, b_scales, group_size: int = 128, 
                                         stream_handle(h.device, stream))
     if check and rc != GMM_OK:
         raise GmmError(rc, "gmm_matmul_int4")
+    return rc
+
+
+# ---------------------------------------------------------------- tokens sorted by expert and back
+
+_ROW_TYPES = None
+
+
+def _row_types():
+    """torch dtype -> GMM_DTYPE_*"""
+    global _ROW_TYPES
+    if _ROW_TYPES is None:
+        import torch
+        _ROW_TYPES = {torch.bfloat16: GMM_DTYPE_BF16, torch.float16: GMM_DTYPE_FP16, torch.float32: GMM_DTYPE_FP32}
+    return _ROW_TYPES
+
+
+def _check_strided(t, name, dtypes, device, out=False):
+    """A 2-D tensor of contiguous rows, any distance apart (an output's must not overlap):
+    its pointer and row stride in elements."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda" or t.device.index != device:
+        raise ValueError(f"{name} must live on cuda:{device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got {t.dim()}-D")
+    rows, width = t.shape
+    stride = t.stride(0) if rows > 1 else width
+    if (width > 1 and t.stride(1) != 1) or (out and stride < width):
+        raise ValueError(f"{name} must have contiguous rows{' that do not overlap' if out else ''}, got strides {t.stride()}")
+    return ctypes.c_void_p(t.data_ptr()), stride
+
+
+def _slots(t, name, device):
+    import torch
+    p = _check(t, name, (torch.int32,), device)
+    if t.dim() != 2 or t.shape[1] < 1:
+        raise ValueError(f"{name} must be [tokens, top_k]")
+    return p, t.shape[0], t.shape[1]
+
+
+def _slot_weights(t, name, shape, device):
+    import torch
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be [tokens, top_k] = {tuple(shape)}, got {tuple(t.shape)}")
+    return _check(t, name, (torch.float32,), device)
+
+
+def gmm_dispatch(h: Handle, a_offsets, slot_rows, row_slots, slot_experts, rows=None, tokens=None, stream=None,
+                 check: bool = True) -> int:
+    """Sort the slots of slot_experts [tokens, top_k] (int32; negative: dropped) by expert, stably:
+    writes a_offsets [E + 1], slot_rows [tokens, top_k] and row_slots [tokens * top_k], and, when
+    `rows` [tokens * top_k, width] and `tokens` [tokens, width] are given, copies each token to its
+    rows (asynchronous).  The gradient of the copy is gmm_combine without weights."""
+    import torch
+    pe, T, k = _slots(slot_experts, "slot_experts", h.device)
+    po = _check(a_offsets, "a_offsets", _i32_types(), h.device, h.num_experts + 1)
+    psr, T2, k2 = _slots(slot_rows, "slot_rows", h.device)
+    prs = _check(row_slots, "row_slots", (torch.int32,), h.device)
+    if (T2, k2) != (T, k) or row_slots.numel() != T * k:
+        raise ValueError(f"slot_rows must be [{T}, {k}] and row_slots [{T * k}]")
+    if (rows is None) != (tokens is None):
+        raise ValueError("rows and tokens go together")
+    pr = pt = None
+    stride, width, dtype = 0, 1, GMM_DTYPE_BF16
+    if tokens is not None:
+        types = _row_types()
+        pt, stride = _check_strided(tokens, "tokens", types, h.device)
+        width, dtype = tokens.shape[1], types[tokens.dtype]
+        pr = _check(rows, "rows", (tokens.dtype,), h.device)
+        if tokens.shape[0] != T or tuple(rows.shape) != (T * k, width):
+            raise ValueError(f"tokens must be [{T}, width] and rows [{T * k}, width], got {tuple(tokens.shape)} and "
+                             f"{tuple(rows.shape)}")
+    rc = load_library().gmm_dispatch(h.ptr, po, psr, prs, pr, pe, pt, stride, T, k, width, dtype,
+                                     stream_handle(h.device, stream))
+    if check and rc != GMM_OK:
+        raise GmmError(rc, "gmm_dispatch")
+    return rc
+
+
+def gmm_combine(h: Handle, out, rows, slot_rows, weights=None, stream=None, check: bool = True) -> int:
+    """out[t] = sum_j weights[t, j] * rows[slot_rows[t, j]] (negative slot_rows: nothing); weights fp32
+    [tokens, top_k], None: ones.  out [tokens, width] and rows [num_rows, width] of one dtype."""
+    types = _row_types()
+    psr, T, k = _slots(slot_rows, "slot_rows", h.device)
+    po, stride = _check_strided(out, "out", types, h.device, out=True)
+    pr = _check(rows, "rows", (out.dtype,), h.device)
+    if rows.dim() != 2 or out.shape[0] != T or out.shape[1] != rows.shape[1]:
+        raise ValueError(f"out must be [{T}, width] and rows [num_rows, width], got {tuple(out.shape)} and "
+                         f"{tuple(rows.shape)}")
+    pw = _slot_weights(weights, "weights", (T, k), h.device)
+    rc = load_library().gmm_combine(h.ptr, po, stride, pr, rows.shape[0], psr, pw, T, k, out.shape[1],
+                                    types[out.dtype], stream_handle(h.device, stream))
+    if check and rc != GMM_OK:
+        raise GmmError(rc, "gmm_combine")
+    return rc
+
+
+def gmm_combine_grad(h: Handle, d_rows, d_weights, d_out, rows, slot_rows, weights=None, stream=None,
+                     check: bool = True) -> int:
+    """The gradient of gmm_combine: d_rows[slot_rows[t, j]] = weights[t, j] * d_out[t] (rows that no slot
+    names stay untouched) and d_weights[t, j] = <d_out[t], rows[slot_rows[t, j]]> in fp32 (None: not
+    computed, and `rows` may be None)."""
+    types = _row_types()
+    psr, T, k = _slots(slot_rows, "slot_rows", h.device)
+    pg, stride = _check_strided(d_out, "d_out", types, h.device)
+    pd = _check(d_rows, "d_rows", (d_out.dtype,), h.device)
+    if d_rows.dim() != 2 or d_out.shape[0] != T or d_out.shape[1] != d_rows.shape[1]:
+        raise ValueError(f"d_out must be [{T}, width] and d_rows [num_rows, width], got {tuple(d_out.shape)} and "
+                         f"{tuple(d_rows.shape)}")
+    pr = None
+    if rows is not None:
+        pr = _check(rows, "rows", (d_out.dtype,), h.device)
+        if tuple(rows.shape) != tuple(d_rows.shape):
+            raise ValueError("rows and d_rows must have the same shape")
+    elif d_weights is not None:
+        raise ValueError("d_weights needs rows")
+    pw = _slot_weights(weights, "weights", (T, k), h.device)
+    pdw = _slot_weights(d_weights, "d_weights", (T, k), h.device)
+    rc = load_library().gmm_combine_grad(h.ptr, pd, pdw, pg, stride, pr, d_rows.shape[0], psr, pw, T, k,
+                                         d_out.shape[1], types[d_out.dtype], stream_handle(h.device, stream))
+    if check and rc != GMM_OK:
+        raise GmmError(rc, "gmm_combine_grad")
+    return rc
+
+
+# ---------------------------------------------------------------- 4-bit floating point
+
+def _fp4_format(fmt) -> int:
+    f = FP4_FORMATS.get(fmt, fmt)
+    if f not in FP4_BLOCKS:
+        raise ValueError(f"unknown 4-bit format {fmt!r}: one of {tuple(FP4_FORMATS)}")
+    return f
+
+
+def fp4_scale_pitch(K: int, fmt="nvfp4") -> int:
+    """Bytes of a row of block scales (one per 16 or 32 of K, padded to a multiple of 16)."""
+    return (K // FP4_BLOCKS[_fp4_format(fmt)] + 15) // 16 * 16
+
+
+def _check_fp4(packed, scales, names, fmt, lead, K, device):
+    import torch
+    if tuple(packed.shape) != (*lead, K // 2):
+        raise ValueError(f"{names[0]} must be {(*lead, K // 2)}, got {tuple(packed.shape)}")
+    if tuple(scales.shape) != (*lead, fp4_scale_pitch(K, fmt)):
+        raise ValueError(f"{names[1]} must be {(*lead, fp4_scale_pitch(K, fmt))}, got {tuple(scales.shape)}")
+    return (_check(packed, names[0], (torch.uint8,), device), _check(scales, names[1], (torch.uint8,), device))
+
+
+def _check_global(t, name, device, numel=1):
+    import torch
+    if t is None:
+        return None
+    if t.numel() != numel:
+        raise ValueError(f"{name} must hold {numel} value(s), got {t.numel()}")
+    return _check(t, name, (torch.float32,), device)
+
+
+def gmm_quantize_fp4(h: Handle, packed, scales, x, fmt="nvfp4", row_slots=None, top_k: int = 1, global_scale=None,
+                     stream=None, check: bool = True) -> int:
+    """Quantise x [src_rows, K] to e2m1 with block scales: packed uint8 [rows, K / 2], scales uint8
+    [rows, fp4_scale_pitch(K, fmt)].  With row_slots (int32 [rows], gmm_dispatch's) row r is quantised
+    from x[row_slots[r] // top_k]; a negative entry leaves it untouched."""
+    import torch
+    f = _fp4_format(fmt)
+    types = _row_types()
+    px, stride = _check_strided(x, "x", types, h.device)
+    K = x.shape[1]
+    ps = None
+    rows = x.shape[0]
+    if row_slots is not None:
+        ps = _check(row_slots, "row_slots", (torch.int32,), h.device)
+        rows = row_slots.numel()
+    pp, psc = _check_fp4(packed, scales, ("packed", "scales"), f, (rows,), K, h.device)
+    pg = _check_global(global_scale, "global_scale", h.device)
+    rc = load_library().gmm_quantize_fp4(h.ptr, pp, psc, px, stride, x.shape[0], ps, int(top_k), pg, rows, K,
+                                         types[x.dtype], f, stream_handle(h.device, stream))
+    if check and rc != GMM_OK:
+        raise GmmError(rc, "gmm_quantize_fp4")
+    return rc
+
+
+def gmm_dequantize_fp4(h: Handle, y, packed, scales, fmt="nvfp4", global_scale=None, stream=None,
+                       check: bool = True) -> int:
+    """y [rows, K] (bf16, fp16 or fp32) = the values that packed and scales stand for."""
+    f = _fp4_format(fmt)
+    types = _row_types()
+    py, stride = _check_strided(y, "y", types, h.device, out=True)
+    rows, K = y.shape
+    pp, psc = _check_fp4(packed, scales, ("packed", "scales"), f, (rows,), K, h.device)
+    pg = _check_global(global_scale, "global_scale", h.device)
+    rc = load_library().gmm_dequantize_fp4(h.ptr, py, stride, pp, psc, pg, rows, K, types[y.dtype], f,
+                                           stream_handle(h.device, stream))
+    if check and rc != GMM_OK:
+        raise GmmError(rc, "gmm_dequantize_fp4")
+    return rc
+
+
+def gmm_run_fp4(h: Handle, c, a, a_offsets, b, expert_ids, expert_usage_stats, a_scales, b_scales, fmt="nvfp4",
+                a_global=None, b_global=None, bias=None, row_scale=None, activation=GMM_ACT_NONE, stream=None,
+                check: bool = True) -> int:
+    """Grouped GEMM on microscaled 4-bit operands: a uint8 [rows, K / 2] with a_scales [rows, pitch],
+    b uint8 [E, N, K / 2] with b_scales [E, N, pitch] (pitch = fp4_scale_pitch(K, fmt)); a_global one
+    fp32 value, b_global fp32 [E]; then the optional epilogue."""
+    import torch
+    f = _fp4_format(fmt)
+    if a.dim() != 2 or b.dim() != 3 or c.dim() != 2:
+        raise ValueError("a must be [rows, K / 2], b [E, N, K / 2], c [rows, N]")
+    E, N, KB = b.shape
+    rows, K = a.shape[0], 2 * KB
+    if a.shape[1] != KB or c.shape[1] != N or c.shape[0] != rows or E != h.num_experts:
+        raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, c {tuple(c.shape)}, "
+                         f"handle E={h.num_experts}")
+    pc = _check(c, "c", (torch.bfloat16,), h.device)
+    pa, pas = _check_fp4(a, a_scales, ("a", "a_scales"), f, (rows,), K, h.device)
+    pb, pbs = _check_fp4(b, b_scales, ("b", "b_scales"), f, (E, N), K, h.device)
+    pga = _check_global(a_global, "a_global", h.device)
+    pgb = _check_global(b_global, "b_global", h.device, E)
+    po, pi, ps, G = _routing_args(h, a_offsets, expert_ids, expert_usage_stats)
+    epi = None
+    if bias is not None or row_scale is not None or activation:
+        epi = ctypes.byref(_epilogue(h, rows, N, bias, row_scale, activation))
+    rc = load_library().gmm_run_fp4(h.ptr, pc, pa, po, pb, pi, ps, G, N, K, pas, pbs, f, pga, pgb, epi,
+                                    stream_handle(h.device, stream))
+    if check and rc != GMM_OK:
+        raise GmmError(rc, "gmm_run_fp4")
     return rc
 
 

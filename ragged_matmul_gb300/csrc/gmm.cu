@@ -17,6 +17,9 @@
 #include "gmm.h"
 #include "gmm_kernel.cuh"
 #include "gmm_fp8_block.cuh"
+#include "gmm_route.cuh"
+#include "gmm_fp4_quant.cuh"
+#include "gmm_fp4.cuh"
 
 namespace {
 
@@ -78,12 +81,14 @@ struct gmm_ctx {
   gmm_variant var[2][2];          // [4-bit][pair]
   gmm_variant var_fp8[2];         // e4m3 kernels, [pair]
   gmm_variant var_fp8_block;      // e4m3 with per-K-block scales (one CTA per tile)
+  gmm_variant var_fp4[2];         // 4-bit floating point, [mxfp4], CTA pairs; grid 0: does not fit
   int smem_per_sm = 0;            // shared memory of one SM (a launch reserves more than half: one CTA per SM)
   bool debug = false;             // GMM_DEBUG was set when the handle was created
   int use_pairs = 1;              // bf16 path: 1 = CTA-pair kernels (cta_group::2), 0 = one CTA per tile
   int use_pairs_int4 = 1;         // 4-bit path: the same
-  uint8_t *ws = nullptr;          // [status word | per-CTA tensor-map slots]
+  uint8_t *ws = nullptr;          // [status word | per-CTA tensor-map slots | chunk counts]
   size_t ws_bytes = 0;
+  uint32_t *route_counts = nullptr;   // in ws; null with more experts than gmm_dispatch takes
   PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   PFN_cuMemsetD32Async_v3020 memset32 = nullptr;   // value writes that a captured CUDA graph replays as such
 };
@@ -325,6 +330,76 @@ int launch_fp8_block(gmm_ctx *h, GmmParams &p, cudaStream_t stream) {
   return GMM_OK;
 }
 
+// The 4-bit floating point kernel: as many stages as fit, two CTAs per tile.  A device or
+// budget that cannot run it leaves grid 0 (gmm_run_fp4 then returns GMM_ERR_UNSUPPORTED).
+template <bool kMx>
+void configure_fp4(gmm_variant *v, int optin, int sm_smem, int device_optin, int num_sms) {
+  auto kernel = gmm::gmm_fp4_kernel<kMx>;
+  v->grid = 0;
+  cudaFuncAttributes attr;
+  if (cudaFuncGetAttributes(&attr, reinterpret_cast<const void *>(kernel)) != cudaSuccess) return;
+  const long avail = static_cast<long>(optin) - static_cast<long>(attr.sharedSizeBytes);
+  if (avail <= 0 || num_sms < 2) return;
+  v->budget = static_cast<size_t>(avail);
+  v->stage_bytes = gmm::F4Geom<kMx>::kStageBytes;
+  v->fixed[0] = gmm::kF4FixedBytes;
+  v->stages = stages_for(*v, 1, 0);
+  if (v->stages < v->min_stages) return;
+  const long reserve = static_cast<long>(sm_smem) / 2 + 1024;   // more than half an SM: one CTA per SM
+  const long cap = static_cast<long>(device_optin) - static_cast<long>(attr.sharedSizeBytes);
+  v->smem = static_cast<size_t>(std::min(cap, std::max(avail, reserve)));
+  if (cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(v->smem)) != cudaSuccess)
+    return;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cudaLaunchAttribute la[1];
+  la[0].id = cudaLaunchAttributeClusterDimension;
+  la[0].val.clusterDim.x = 2;
+  la[0].val.clusterDim.y = 1;
+  la[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(num_sms & ~1));
+  cfg.blockDim = dim3(gmm::kF4Threads);
+  cfg.dynamicSmemBytes = v->smem;
+  cfg.attrs = la;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess || clusters < 1) return;
+  v->grid = std::min(2 * clusters, num_sms & ~1);
+}
+
+template <bool kMx>
+int launch_fp4(gmm_ctx *h, gmm::F4Params &p, cudaStream_t stream) {
+  DeviceGuard guard(h->device);
+  const gmm_variant &v = h->var_fp4[kMx];
+  if (v.grid == 0) return GMM_ERR_UNSUPPORTED;
+  p.num_stages = stages_for(v, p.num_groups, 0);
+  if (p.num_stages < v.min_stages) return GMM_ERR_UNSUPPORTED;   // the prefix leaves no room for the ring
+  if (h->debug)
+    fprintf(stderr, "gmm: launch %s pair, %d groups: stages %d packed slots 0\n", kMx ? "mxfp4" : "nvfp4", p.num_groups,
+            p.num_stages);
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(v.grid));
+  cfg.blockDim = dim3(gmm::kF4Threads);
+  cfg.dynamicSmemBytes = v.smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, gmm::gmm_fp4_kernel<kMx>, p);
+  if (err != cudaSuccess) {
+    debug_report("launch of the 4-bit floating point kernel", static_cast<int>(err), cudaGetErrorString(err));
+    cudaGetLastError();
+    return GMM_ERR_CUDA;
+  }
+  return GMM_OK;
+}
+
 template <bool kInt4, bool kFp8 = false>
 int launch(gmm_ctx *h, GmmParams &p, cudaStream_t stream) {
   DeviceGuard guard(h->device);
@@ -367,6 +442,153 @@ int launch(gmm_ctx *h, GmmParams &p, cudaStream_t stream) {
   return GMM_OK;
 }
 
+// Dynamic shared memory of the dispatch kernels.
+size_t small_dispatch_smem(int E, int slots) {
+  return (static_cast<size_t>(gmm::kRouteWarps) * E + E + 1 + slots) * 4;
+}
+constexpr size_t kCountSmem = 96 * 1024;   // gmm_dispatch_count_kernel's counters, at most
+
+int configure_route() {
+  const int small = static_cast<int>(small_dispatch_smem(gmm::kRouteSmallExperts, gmm::kRouteSmallSlots));
+  const void *kernels[3] = {reinterpret_cast<const void *>(gmm::gmm_dispatch_small_kernel<16>),
+                            reinterpret_cast<const void *>(gmm::gmm_dispatch_small_kernel<4>),
+                            reinterpret_cast<const void *>(gmm::gmm_dispatch_small_kernel<2>)};
+  for (const void *k : kernels)
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, small) != cudaSuccess) return GMM_ERR_CUDA;
+  if (cudaFuncSetAttribute(reinterpret_cast<const void *>(gmm::gmm_dispatch_count_kernel),
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kCountSmem)) != cudaSuccess)
+    return GMM_ERR_CUDA;
+  return GMM_OK;
+}
+
+int dtype_bytes(int dtype) {
+  switch (dtype) {
+    case GMM_DTYPE_BF16:
+    case GMM_DTYPE_FP16: return 2;
+    case GMM_DTYPE_FP32: return 4;
+    default: return 0;
+  }
+}
+
+bool aligned_to(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+// Argument checks shared by the calls that move rows of tokens.
+int check_rows(gmm_ctx *h, int num_tokens, int top_k, int width, int dtype, long long stride) {
+  if (!h || num_tokens < 0 || top_k < 1 || width < 1 || !dtype_bytes(dtype)) return GMM_ERR_INVALID_ARG;
+  if (stride < 0) return GMM_ERR_INVALID_ARG;
+  if (top_k > gmm::kRouteMaxTopK || static_cast<long long>(num_tokens) * top_k > (1ll << 30)) return GMM_ERR_UNSUPPORTED;
+  return GMM_OK;
+}
+
+int launch_status(const char *what) {
+  const cudaError_t err = cudaGetLastError();
+  if (err == cudaSuccess) return GMM_OK;
+  debug_report(what, static_cast<int>(err), cudaGetErrorString(err));
+  return GMM_ERR_CUDA;
+}
+
+template <int VB>
+int launch_dispatch(gmm_ctx *h, gmm::DispatchParams &p, cudaStream_t stream) {
+  const int E = p.num_experts, S = p.num_tokens * p.top_k;
+  if (S <= gmm::kRouteSmallSlots && E <= gmm::kRouteSmallExperts) {
+    const long long units = p.tokens ? p.num_tokens * ((p.row_bytes / VB + 127) / 128) : 0;
+    const long long want = (units + gmm::kRouteWarps - 1) / gmm::kRouteWarps;
+    const int grid = static_cast<int>(std::max(1ll, std::min<long long>(want, h->num_sms)));
+    gmm::gmm_dispatch_small_kernel<VB><<<grid, gmm::kRouteThreads, small_dispatch_smem(E, S), stream>>>(p);
+    return launch_status("launch of the dispatch kernel");
+  }
+  int chunks = std::min(gmm::kRouteMaxChunks, std::max(1, gmm::kRouteMaxCounts / E));
+  chunks = std::min(chunks, p.num_tokens);
+  p.chunk_tokens = (p.num_tokens + chunks - 1) / chunks;
+  p.chunks = (p.num_tokens + p.chunk_tokens - 1) / p.chunk_tokens;
+  p.subs = std::max(1, std::min(4 * h->num_sms / p.chunks, p.chunk_tokens));
+  const int warps = static_cast<int>(std::min<size_t>(gmm::kRouteWarps, kCountSmem / (4u * static_cast<unsigned>(E))));
+  gmm::gmm_dispatch_count_kernel<<<p.chunks, gmm::kRouteThreads, static_cast<size_t>(warps) * E * 4, stream>>>(p, warps);
+  const int rc = launch_status("launch of the count kernel");
+  if (rc) return rc;
+  const size_t smem = (2 * static_cast<size_t>(E) + 1 + static_cast<size_t>(gmm::kRouteBatch) * p.top_k) * 4;
+  gmm::gmm_dispatch_place_kernel<VB><<<p.chunks * p.subs, gmm::kRouteThreads, smem, stream>>>(p);
+  return launch_status("launch of the place kernel");
+}
+
+template <class T, int VN>
+int launch_combine(gmm_ctx *, gmm::CombineParams &p, bool grad, cudaStream_t stream) {
+  const long long nvec = p.row_bytes / static_cast<long long>(sizeof(T) * VN);
+  const long long pieces = (nvec + 31) / 32;
+  if (!grad) {
+    const long long ctas = (p.num_tokens * pieces + gmm::kCombineWarps - 1) / gmm::kCombineWarps;
+    if (ctas > 0x7fffffffll) return GMM_ERR_UNSUPPORTED;
+    gmm::gmm_combine_kernel<T, VN><<<static_cast<unsigned>(ctas), 32 * gmm::kCombineWarps, 0, stream>>>(p);
+    return launch_status("launch of the combine kernel");
+  }
+  int wpt = 1;
+  while (wpt < gmm::kCombineWarps && wpt < pieces && static_cast<long long>(p.num_tokens) * wpt < 152 * 32) wpt *= 2;
+  p.warps_per_token = wpt;
+  const int tpc = gmm::kCombineWarps / wpt;
+  gmm::gmm_combine_grad_kernel<T, VN>
+      <<<static_cast<unsigned>((p.num_tokens + tpc - 1) / tpc), 32 * gmm::kCombineWarps, 0, stream>>>(p);
+  return launch_status("launch of the combine gradient kernel");
+}
+
+// 16-byte vectors where every row starts on a 16-byte boundary, else single elements.
+int run_combine(gmm_ctx *h, gmm::CombineParams &p, int dtype, bool vec, bool grad, cudaStream_t stream) {
+  DeviceGuard guard(h->device);
+  switch (dtype) {
+    case GMM_DTYPE_BF16:
+      return vec ? launch_combine<__nv_bfloat16, 8>(h, p, grad, stream) : launch_combine<__nv_bfloat16, 1>(h, p, grad, stream);
+    case GMM_DTYPE_FP16:
+      return vec ? launch_combine<__half, 8>(h, p, grad, stream) : launch_combine<__half, 1>(h, p, grad, stream);
+    default:
+      return vec ? launch_combine<float, 4>(h, p, grad, stream) : launch_combine<float, 1>(h, p, grad, stream);
+  }
+}
+
+template <class T, bool kMx>
+void launch_quant(const gmm::QuantParams &p, bool quantise, bool vec, unsigned grid, cudaStream_t stream) {
+  if (quantise) {
+    if (vec) gmm::gmm_quantize_fp4_kernel<T, kMx, true><<<grid, gmm::kQuantThreads, 0, stream>>>(p);
+    else gmm::gmm_quantize_fp4_kernel<T, kMx, false><<<grid, gmm::kQuantThreads, 0, stream>>>(p);
+  } else {
+    if (vec) gmm::gmm_dequantize_fp4_kernel<T, kMx, true><<<grid, gmm::kQuantThreads, 0, stream>>>(p);
+    else gmm::gmm_dequantize_fp4_kernel<T, kMx, false><<<grid, gmm::kQuantThreads, 0, stream>>>(p);
+  }
+}
+
+template <class T>
+void launch_quant_fmt(const gmm::QuantParams &p, int format, bool quantise, bool vec, unsigned grid, cudaStream_t stream) {
+  if (format == GMM_FP4_MX) launch_quant<T, true>(p, quantise, vec, grid, stream);
+  else launch_quant<T, false>(p, quantise, vec, grid, stream);
+}
+
+int fp4_block(int format) { return format == GMM_FP4_MX ? 32 : 16; }
+int fp4_scale_pitch(int K, int format) { return (K / fp4_block(format) + 15) / 16 * 16; }
+
+int run_quant(gmm_ctx *h, gmm::QuantParams &p, int dtype, int format, long long stride, bool quantise, cudaStream_t stream) {
+  if (!h || !dtype_bytes(dtype) || (format != GMM_FP4_NV && format != GMM_FP4_MX)) return GMM_ERR_INVALID_ARG;
+  if (p.rows < 0 || p.K < 32 || p.K % 32 || stride < 0) return GMM_ERR_INVALID_ARG;
+  if (p.K > (1 << 24)) return GMM_ERR_UNSUPPORTED;
+  if (p.rows == 0) return GMM_OK;
+  const int es = dtype_bytes(dtype);
+  if (!p.x || !p.packed || !p.scales || !aligned_to(p.x, es) || !aligned16(p.packed) || !aligned16(p.scales) ||
+      !aligned_to(p.global_scale, 4) || !aligned_to(p.row_slots, 4) || (format == GMM_FP4_MX && p.global_scale))
+    return GMM_ERR_INVALID_ARG;
+  if (!quantise && stride < p.K && p.rows > 1) return GMM_ERR_INVALID_ARG;   // rows of the output overlap
+  p.x_pitch = stride * es;
+  p.scale_pitch = fp4_scale_pitch(p.K, format);
+  p.status = reinterpret_cast<uint32_t *>(h->ws);
+  const long long threads = static_cast<long long>(p.rows) * (p.K / 16);
+  const long long grid = (threads + gmm::kQuantThreads - 1) / gmm::kQuantThreads;
+  if (grid > 0x7fffffffll) return GMM_ERR_UNSUPPORTED;
+  const bool vec = aligned16(p.x) && p.x_pitch % 16 == 0;
+  DeviceGuard guard(h->device);
+  switch (dtype) {
+    case GMM_DTYPE_BF16: launch_quant_fmt<__nv_bfloat16>(p, format, quantise, vec, static_cast<unsigned>(grid), stream); break;
+    case GMM_DTYPE_FP16: launch_quant_fmt<__half>(p, format, quantise, vec, static_cast<unsigned>(grid), stream); break;
+    default: launch_quant_fmt<float>(p, format, quantise, vec, static_cast<unsigned>(grid), stream); break;
+  }
+  return launch_status(quantise ? "launch of the quantisation kernel" : "launch of the dequantisation kernel");
+}
+
 uint32_t max_tok(const gmm_ctx *h, bool int4) {
   if (int4) return h->use_pairs_int4 ? gmm::Geom<true, true>::kMaxTok : gmm::Geom<true, false>::kMaxTok;
   return h->use_pairs ? gmm::Geom<false, true>::kMaxTok : gmm::Geom<false, false>::kMaxTok;
@@ -383,7 +605,7 @@ const char *gmm_error_string(int code) {
     case GMM_ERR_UNSUPPORTED: return "unsupported shape or option";
     case GMM_ERR_CUDA: return "CUDA runtime or driver call failed";
     case GMM_ERR_DEVICE_TIMEOUT: return "kernel pipeline wait timed out";
-    case GMM_ERR_BAD_INPUT: return "decreasing a_offsets or expert id out of range";
+    case GMM_ERR_BAD_INPUT: return "decreasing a_offsets or expert id out of range, or a slot or row index out of range";
     case GMM_ERR_NO_DEVICE: return "no sm_103 device";
     default: return "unknown error code";
   }
@@ -460,6 +682,14 @@ int gmm_create(gmm_handle_t *out, int num_experts, int device) {
     delete h;
     return GMM_ERR_CUDA;
   }
+  configure_fp4<false>(&h->var_fp4[0], optin, sm_smem, device_optin, sms);
+  configure_fp4<true>(&h->var_fp4[1], optin, sm_smem, device_optin, sms);
+  if (configure_route() != GMM_OK) {
+    cudaGetLastError();
+    delete h;
+    return GMM_ERR_CUDA;
+  }
+  cudaGetLastError();   // a 4-bit configuration that does not fit is not an error of this call
 
   h->debug = getenv("GMM_DEBUG") != nullptr;
   if (h->debug) {
@@ -469,7 +699,8 @@ int gmm_create(gmm_handle_t *out, int num_experts, int device) {
     for (int i = 0; i < 7; ++i)
       fprintf(stderr, "gmm: %-16s stages %d smem %zu grid %d\n", names[i], vs[i]->stages, vs[i]->smem, vs[i]->grid);
   }
-  h->ws_bytes = kStatusBytes + static_cast<size_t>(sms) * gmm::kMapSlotBytes;
+  const size_t counts_at = kStatusBytes + static_cast<size_t>(sms) * gmm::kMapSlotBytes;
+  h->ws_bytes = counts_at + (num_experts <= gmm::kRouteMaxExperts ? gmm::kRouteMaxCounts * sizeof(uint32_t) : 0);
   if (cudaMalloc(&h->ws, h->ws_bytes) != cudaSuccess ||
       cudaMemset(h->ws, 0, h->ws_bytes) != cudaSuccess) {
     cudaGetLastError();
@@ -477,6 +708,7 @@ int gmm_create(gmm_handle_t *out, int num_experts, int device) {
     delete h;
     return GMM_ERR_CUDA;
   }
+  if (num_experts <= gmm::kRouteMaxExperts) h->route_counts = reinterpret_cast<uint32_t *>(h->ws + counts_at);
   *out = h;
   return GMM_OK;
 }
@@ -693,6 +925,181 @@ int gmm_run_int4(gmm_handle_t h, void *c, const void *a, const uint32_t *a_offse
                  cudaStream_t stream) {
   return gmm_run_int4_ex(h, c, a, a_offsets, b_packed, b_scales, expert_ids, expert_usage_stats, num_groups, N,
                          K, group_size, nullptr, stream);
+}
+
+int gmm_dispatch(gmm_handle_t h, uint32_t *a_offsets, int32_t *slot_rows, int32_t *row_slots, void *rows,
+                 const int32_t *slot_experts, const void *tokens, long long tokens_stride, int num_tokens, int top_k,
+                 int width, int dtype, cudaStream_t stream) {
+  if (!rows != !tokens) return GMM_ERR_INVALID_ARG;
+  const bool copy = tokens != nullptr;
+  int rc = check_rows(h, num_tokens, top_k, copy ? width : 1, copy ? dtype : GMM_DTYPE_BF16, copy ? tokens_stride : 0);
+  if (rc) return rc;
+  if (!a_offsets || !aligned_to(a_offsets, 4)) return GMM_ERR_INVALID_ARG;
+  if (num_tokens > 0 && (!slot_rows || !row_slots || !slot_experts || !aligned_to(slot_rows, 4) ||
+                         !aligned_to(row_slots, 4) || !aligned_to(slot_experts, 4)))
+    return GMM_ERR_INVALID_ARG;
+  if (h->num_experts > gmm::kRouteMaxExperts) return GMM_ERR_UNSUPPORTED;
+  gmm::DispatchParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.slot_experts = slot_experts;
+  p.a_offsets = a_offsets;
+  p.slot_rows = slot_rows;
+  p.row_slots = row_slots;
+  p.num_tokens = num_tokens;
+  p.top_k = top_k;
+  p.num_experts = h->num_experts;
+  p.counts = h->route_counts;
+  p.status = reinterpret_cast<uint32_t *>(h->ws);
+  int vb = 16;
+  if (copy) {
+    const int es = dtype_bytes(dtype);
+    if (!aligned_to(rows, es) || !aligned_to(tokens, es)) return GMM_ERR_INVALID_ARG;
+    p.tokens = static_cast<const uint8_t *>(tokens);
+    p.rows = static_cast<uint8_t *>(rows);
+    p.token_pitch = tokens_stride * es;
+    p.row_bytes = static_cast<long long>(width) * es;
+    const unsigned long long all = reinterpret_cast<uintptr_t>(tokens) | reinterpret_cast<uintptr_t>(rows) |
+                                   static_cast<unsigned long long>(p.token_pitch | p.row_bytes);
+    vb = all % 16 == 0 ? 16 : (all % 4 == 0 ? 4 : 2);
+  }
+  DeviceGuard guard(h->device);
+  return vb == 16 ? launch_dispatch<16>(h, p, stream)
+                  : (vb == 4 ? launch_dispatch<4>(h, p, stream) : launch_dispatch<2>(h, p, stream));
+}
+
+int gmm_combine(gmm_handle_t h, void *out, long long out_stride, const void *rows, int num_rows, const int32_t *slot_rows,
+                const float *weights, int num_tokens, int top_k, int width, int dtype, cudaStream_t stream) {
+  int rc = check_rows(h, num_tokens, top_k, width, dtype, out_stride);
+  if (rc) return rc;
+  if (num_rows < 0) return GMM_ERR_INVALID_ARG;
+  if (num_tokens == 0) return GMM_OK;
+  const int es = dtype_bytes(dtype);
+  if (!out || (!rows && num_rows > 0) || !slot_rows || !aligned_to(out, es) || !aligned_to(rows, es) ||
+      !aligned_to(slot_rows, 4) || !aligned_to(weights, 4))
+    return GMM_ERR_INVALID_ARG;
+  if (out_stride < width && num_tokens > 1) return GMM_ERR_INVALID_ARG;   // rows of the output overlap
+  gmm::CombineParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.out = static_cast<uint8_t *>(out);
+  p.rows = static_cast<const uint8_t *>(rows);
+  p.slot_rows = slot_rows;
+  p.weights = weights;
+  p.out_pitch = out_stride * es;
+  p.row_bytes = static_cast<long long>(width) * es;
+  p.num_tokens = num_tokens;
+  p.top_k = top_k;
+  p.num_rows = num_rows;
+  p.status = reinterpret_cast<uint32_t *>(h->ws);
+  const bool vec = aligned16(out) && aligned16(rows) && p.out_pitch % 16 == 0 && p.row_bytes % 16 == 0;
+  return run_combine(h, p, dtype, vec, false, stream);
+}
+
+int gmm_combine_grad(gmm_handle_t h, void *d_rows, float *d_weights, const void *d_out, long long d_out_stride,
+                     const void *rows, int num_rows, const int32_t *slot_rows, const float *weights, int num_tokens,
+                     int top_k, int width, int dtype, cudaStream_t stream) {
+  int rc = check_rows(h, num_tokens, top_k, width, dtype, d_out_stride);
+  if (rc) return rc;
+  if (num_rows < 0) return GMM_ERR_INVALID_ARG;
+  if (num_tokens == 0) return GMM_OK;
+  const int es = dtype_bytes(dtype);
+  if ((!d_rows && num_rows > 0) || !d_out || (d_weights && !rows && num_rows > 0) || !slot_rows ||
+      !aligned_to(d_rows, es) || !aligned_to(d_out, es) || !aligned_to(rows, es) || !aligned_to(slot_rows, 4) ||
+      !aligned_to(weights, 4) || !aligned_to(d_weights, 4))
+    return GMM_ERR_INVALID_ARG;
+  gmm::CombineParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.rows = static_cast<const uint8_t *>(rows);
+  p.slot_rows = slot_rows;
+  p.weights = weights;
+  p.d_out = static_cast<const uint8_t *>(d_out);
+  p.d_rows = static_cast<uint8_t *>(d_rows);
+  p.d_weights = d_weights;
+  p.out_pitch = d_out_stride * es;
+  p.row_bytes = static_cast<long long>(width) * es;
+  p.num_tokens = num_tokens;
+  p.top_k = top_k;
+  p.num_rows = num_rows;
+  p.status = reinterpret_cast<uint32_t *>(h->ws);
+  const bool vec = aligned16(d_out) && aligned16(d_rows) && (!d_weights || aligned16(rows)) && p.out_pitch % 16 == 0 &&
+                   p.row_bytes % 16 == 0;
+  return run_combine(h, p, dtype, vec, true, stream);
+}
+
+int gmm_quantize_fp4(gmm_handle_t h, void *packed, void *scales, const void *x, long long x_stride, int src_rows,
+                     const int32_t *row_slots, int top_k, const float *global_scale, int rows, int K, int dtype,
+                     int format, cudaStream_t stream) {
+  if (top_k < 1 || src_rows < 0) return GMM_ERR_INVALID_ARG;
+  if (!row_slots && src_rows < rows) return GMM_ERR_INVALID_ARG;
+  gmm::QuantParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.x = static_cast<const uint8_t *>(x);
+  p.packed = static_cast<uint8_t *>(packed);
+  p.scales = static_cast<uint8_t *>(scales);
+  p.row_slots = row_slots;
+  p.global_scale = global_scale;
+  p.rows = rows;
+  p.src_rows = src_rows;
+  p.K = K;
+  p.top_k = top_k;
+  return run_quant(h, p, dtype, format, x_stride, true, stream);
+}
+
+int gmm_dequantize_fp4(gmm_handle_t h, void *y, long long y_stride, const void *packed, const void *scales,
+                       const float *global_scale, int rows, int K, int dtype, int format, cudaStream_t stream) {
+  gmm::QuantParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.x = static_cast<const uint8_t *>(y);
+  p.packed = static_cast<uint8_t *>(const_cast<void *>(packed));
+  p.scales = static_cast<uint8_t *>(const_cast<void *>(scales));
+  p.global_scale = global_scale;
+  p.rows = rows;
+  p.K = K;
+  p.top_k = 1;
+  return run_quant(h, p, dtype, format, y_stride, false, stream);
+}
+
+// The packed values go through the bf16 kernel's tensor maps over their bytes: a row of K
+// e2m1 values is K / 2 bytes, K / 4 two-byte units.
+int gmm_run_fp4(gmm_handle_t h, void *c, const void *a, const uint32_t *a_offsets, const void *b,
+                const int32_t *expert_ids, uint32_t *expert_usage_stats, int num_groups, int N, int K,
+                const void *a_scales, const void *b_scales, int format, const float *a_global, const float *b_global,
+                const gmm_epilogue *epilogue, cudaStream_t stream) {
+  if (format != GMM_FP4_NV && format != GMM_FP4_MX) return GMM_ERR_INVALID_ARG;
+  if (K < 32 || K % 32) return GMM_ERR_INVALID_ARG;
+  const int KU = K / 4;
+  if (h && num_groups == 0) {   // no rows: c, a and a_scales may be NULL (an empty tensor's), nothing is read or written
+    if (!c) c = h->ws;
+    if (!a) a = h->ws;
+    if (!a_scales) a_scales = h->ws;
+  }
+  int rc = check_common(h, c, a, a_offsets, expert_ids, expert_usage_stats, num_groups, N, KU);
+  if (rc) return rc;
+  rc = check_epilogue(epilogue);
+  if (rc) return rc;
+  if (!b || !aligned16(b) || !a_scales || !b_scales || !aligned16(a_scales) || !aligned16(b_scales) ||
+      !aligned_to(a_global, 4) || !aligned_to(b_global, 4))
+    return GMM_ERR_INVALID_ARG;
+  gmm::F4Params p;
+  std::memset(&p, 0, sizeof(p));
+  {
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(KU), static_cast<cuuint64_t>(N),
+                          static_cast<cuuint64_t>(h->num_experts)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(KU) * 2, static_cast<cuuint64_t>(N) * KU * 2};
+    cuuint32_t box[3] = {gmm::kBK, gmm::kBlockN, 1};
+    rc = encode_map(h, &p.w_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, b, dims, strides, box,
+                    CU_TENSOR_MAP_SWIZZLE_128B);
+    if (rc) return rc;
+  }
+  rc = encode_token_maps(h, p, a, KU, 1);
+  if (rc) return rc;
+  fill_common(h, p, c, a_offsets, expert_ids, expert_usage_stats, num_groups, N, KU, gmm::kF4MaxTok);
+  set_epilogue(p, epilogue);
+  p.sf_a = static_cast<const uint8_t *>(a_scales);
+  p.sf_w = static_cast<const uint8_t *>(b_scales);
+  p.g_a = a_global;
+  p.g_w = b_global;
+  p.sf_pitch = fp4_scale_pitch(K, format);
+  return format == GMM_FP4_MX ? launch_fp4<true>(h, p, stream) : launch_fp4<false>(h, p, stream);
 }
 
 int gmm_query_status(gmm_handle_t h, cudaStream_t stream) {

@@ -1,0 +1,461 @@
+// 4-bit block-scaled grouped GEMM (e2m1 operands, e4m3 or e8m0 block scales), for sm_103a.
+//
+// Operation, for each active group g with expert e and rows r of the group (b = 16 for
+// nvfp4, 32 for mxfp4):
+//   C[r, n] = bf16( epi( ga * gb[e] * sum_k sa[r, k / b] qa[r, k] sb[e, n, k / b] qb[e, n, k] ) )
+// The scales enter in the tensor core (tcgen05.mma kind::mxf4nvf4), fp32 accumulation.
+//
+// Orientation and pairs are the grouped kernel's: weights are the MMA's M (256 rows over a
+// CTA pair), tokens its N (a multiple of 32 up to 224).  A stage is 256 of K: 128-byte rows
+// of packed values, so the value operands go through the bf16 kernel's tensor maps, swizzle
+// and descriptors unchanged.
+//
+// Scales.  The MMA takes them from tensor memory, 4 scales (one 32-bit word) per operand
+// row, row m in lane m % 32 and column m / 32, the same in all four lane quadrants.  In
+// global memory a row's scales follow one another (16 bytes per stage for nvfp4, 8 for
+// mxfp4), rows may start anywhere, and a tensor copy cannot transpose 4-byte words.  So
+// warps load them: lane l takes rows l, l + 32, l + 64, l + 96 of a 128-row block, and the
+// four rows' word j are 16 bytes of a 512-byte atom (one per block and word) in the stage's
+// shared memory, from where tcgen05.cp spreads it over the quadrants.  The copies run in
+// order with the MMAs of the issuing thread, so one set of scale columns serves all stages.
+// Both CTAs of a pair hold the scales of all the tile's tokens (each computes its own 128
+// weight rows against all of them), and of their own 128 weight rows.
+//
+// Tensor memory: two accumulators of 224 columns and 48 columns of scales.
+//
+// Roles (416 threads per CTA):
+//   warp 0        TMA producer of the stage's weight and token values.
+//   warp 1        TMEM allocation; in the pair's leader the scale copies and MMAs.
+//   warps 2..9    epilogue, two per TMEM lane quadrant taking every second 32-row chunk.
+//   warps 10..12  scales: the weight rows' block, and the tokens' two.
+//
+// Tiles are the static share of each pair (tile t, t + pairs, ...); a group's rows are cut
+// into equal token blocks (to the granule of 32).  Every wait is bounded as in the grouped
+// kernel.
+#pragma once
+
+#include "gmm_kernel.cuh"
+
+namespace gmm {
+
+constexpr uint32_t kF4EpiWarps = 8;
+constexpr uint32_t kF4ScaleWarps = 3;
+constexpr uint32_t kF4FirstScaleWarp = 2 + kF4EpiWarps;
+constexpr int kF4Threads = 32 * static_cast<int>(2 + kF4EpiWarps + kF4ScaleWarps);
+constexpr uint32_t kF4MaxTok = 224;
+constexpr uint32_t kF4TokAlign = 32;
+constexpr uint32_t kF4StageK = 256;
+constexpr uint32_t kF4WBytes = kBlockN * 128;               // 128 weight rows x 128 bytes
+constexpr uint32_t kF4TBytes = kF4MaxTok / 2 * 128;         // a CTA's half of the tokens
+constexpr uint32_t kF4Atom = 512;                           // one scale word of 128 rows
+constexpr uint32_t kF4AccCols = kF4MaxTok;
+constexpr uint32_t kF4ScaleCol = 2 * kF4AccCols;            // scale columns follow the accumulators
+constexpr uint32_t kF4StgBytes = kEpiRows * kEpiRowBytes;   // one epilogue staging buffer
+constexpr uint32_t kF4StgBufs = 2;                          // per epilogue warp
+
+// Scale words per row and stage, and the instructions of K = 64 that share one.
+template <bool kMx>
+struct F4Scale {
+  static constexpr uint32_t kWords = kMx ? 2 : 4;
+  static constexpr uint32_t kStepsPerWord = kMx ? 2 : 1;
+  static constexpr uint32_t kBlock = kMx ? 32 : 16;
+  static constexpr uint32_t kBytes = 3 * kWords * kF4Atom;   // a stage's atoms: weights, then tokens
+  static_assert(kF4ScaleCol + 12 * kWords <= kTmemCols, "scales beside the accumulators");
+};
+
+template <bool kMx>
+struct F4Geom {
+  static constexpr uint32_t kRows = 2 * kBlockN;
+  static constexpr uint32_t kMaxTok = kF4MaxTok;
+  static constexpr uint32_t kTokAlign = kF4TokAlign;
+  static constexpr uint32_t kStageBytes = kF4WBytes + kF4TBytes + F4Scale<kMx>::kBytes;
+};
+constexpr size_t kF4FixedBytes = 1024 + kF4EpiWarps * kF4StgBufs * kF4StgBytes;
+
+struct alignas(128) F4Params : GmmParams {   // K counts two-byte units: 4 elements each
+  const uint8_t *sf_a;     // [rows, sf_pitch]
+  const uint8_t *sf_w;     // [E, N, sf_pitch]
+  const float *g_a;        // one value or null
+  const float *g_w;        // [E] or null
+  int sf_pitch;            // bytes, a multiple of 16
+};
+
+// Tile t with the group's rows cut into equal blocks: as many as kF4MaxTok asks for, each
+// the same multiple of 32 rows (the last one less).
+template <bool kMx>
+__device__ __forceinline__ Tile f4_decode_tile(uint32_t t, const uint32_t *prefix, const GmmParams &p) {
+  Tile x = decode_tile<F4Geom<kMx>>(t, prefix, p);
+  return x;
+}
+
+template <bool kMx>
+__global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_constant__ F4Params p) {
+  using G = F4Geom<kMx>;
+  using S = F4Scale<kMx>;
+  constexpr uint32_t kFullArrivals = 1 + 2 * kF4ScaleWarps;
+  constexpr uint32_t kEpiArrivals = 2 * kF4EpiWarps;
+  __shared__ Ctrl ctl;
+  extern __shared__ uint8_t dyn_smem[];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t ST = static_cast<uint32_t>(p.num_stages);
+  const int KB = (p.K + kBK - 1) / kBK;   // stages per tile: 64 two-byte units = 256 of K
+  const uint32_t rank = cluster_ctarank();
+
+  const uint32_t dyn_base = smem_addr(dyn_smem);
+  const uint32_t w_ring = (dyn_base + 1023u) & ~1023u;
+  const uint32_t t_ring = w_ring + ST * kF4WBytes;
+  const uint32_t s_ring = t_ring + ST * kF4TBytes;
+  const uint32_t epi_ring = s_ring + ST * S::kBytes;
+  uint32_t *prefix = reinterpret_cast<uint32_t *>(dyn_smem + (epi_ring + kF4EpiWarps * kF4StgBufs * kF4StgBytes - dyn_base));
+
+  if (tid == 0) {
+    set_wait_limit(p.wait_limit_ns);
+    for (uint32_t s = 0; s < ST; ++s) {
+      mbar_init(smem_addr(&ctl.full[s]), kFullArrivals);
+      mbar_init(smem_addr(&ctl.empty[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_addr(&ctl.acc_full[a]), 1);
+      mbar_init(smem_addr(&ctl.acc_empty[a]), kEpiArrivals);
+    }
+    mbar_init(smem_addr(&ctl.maps_ready), 1);
+    ctl.abort = 0;
+    ctl.active = 0;
+    ctl.flags = 0;
+    ctl.max_group_tiles = 0;
+    ctl.min_group_tiles = 0xffffffffu;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_addr(&ctl.tmem_base), kTmemCols);
+    tmem_relinquish_pair();
+    tc_fence_before_sync();
+  }
+  __syncthreads();
+  build_schedule<G>(p, ctl, prefix, kF4Threads);
+  cluster_sync();   // the peer's barriers are initialised before anyone signals them
+
+  if (blockIdx.x == 0 && tid == 0) {
+    p.stats[1] = ctl.active;
+    const uint32_t f = ctl.flags & (kStatusBadOffsets | kStatusBadExpert | kStatusTooLarge);
+    if (f) atomicOr(p.status, f);
+  }
+  tc_fence_after_sync();
+  const uint32_t tmem_base = ctl.tmem_base;
+  const uint32_t total = ctl.total_tiles;
+  volatile int *abort = &ctl.abort;
+  const uint32_t unit0 = cluster_id_x(), units = cluster_count_x();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ value producer
+    uint8_t *slot = p.map_slots + static_cast<size_t>(blockIdx.x) * kMapSlotBytes;
+    if (lane == 0 && unit0 < total) {
+      const CUtensorMap *tok_maps = reinterpret_cast<const CUtensorMap *>(slot);
+      prefetch_tensormap(&p.w_map);
+      const uint64_t pol_first = l2_policy_evict_first();
+      const uint64_t pol_last = l2_policy_evict_last();
+      const uint64_t pol_normal = l2_policy_evict_normal();
+      Ring rt;
+      uint32_t pending = 0, pend_phase = 0;
+      bool ok = true, maps_acquired = false;
+      for (uint32_t t = unit0; t < total && ok; t += units) {
+        const Tile ti = f4_decode_tile<kMx>(t, prefix, p);
+        const uint32_t my_tok = ti.ntok / 2;
+        const uint32_t tx = 2u * (kF4WBytes + my_tok * 128u);
+        const int32_t w_row = static_cast<int32_t>(ti.n0 + rank * kBlockN);
+        const int32_t t_row = static_cast<int32_t>(ti.row0 + rank * my_tok);
+        const uint64_t w_pol = (p.cache_hints && ti.single_block) ? pol_first : pol_normal;
+        const uint64_t t_pol = p.cache_hints ? pol_last : pol_normal;
+        if (!maps_acquired) {
+          if (!wait_phase(smem_addr(&ctl.maps_ready), 0, abort)) { ok = false; break; }
+          for (uint32_t i = 0; i < kF4MaxTok / 32; ++i) tensormap_acquire(slot + i * 128);
+          maps_acquired = true;
+        }
+        const CUtensorMap *tok = tok_maps + (my_tok / 16u - 1u);
+        for (int kb = 0; kb < KB; ++kb) {
+          const uint32_t full_local = smem_addr(&ctl.full[rt.slot]);
+          if (!wait_phase(smem_addr(&ctl.empty[rt.slot]), rt.phase ^ 1u, abort)) { ok = false; break; }
+          if (rank == 0) mbar_arrive_expect_tx(full_local, tx);
+          const uint32_t full_leader = map_to_rank(full_local, 0);
+          tma_load_3d_pair(w_ring + rt.slot * kF4WBytes, &p.w_map, full_leader, kb * kBK, w_row, ti.e, w_pol);
+          tma_load_2d_pair(t_ring + rt.slot * kF4TBytes, tok, full_leader, kb * kBK, t_row, t_pol);
+          pending |= 1u << rt.slot;
+          pend_phase = (pend_phase & ~(1u << rt.slot)) | (rt.phase << rt.slot);
+          rt.next(ST);
+        }
+      }
+      if (!ok) {
+        // As in the grouped kernel: the leader lets the copies already issued land (its
+        // barriers count both CTAs' bytes), the peer is held at the final cluster barrier.
+        for (uint32_t s = 0; s < ST; ++s)
+          if ((pending & (1u << s)) && rank == 0)
+            wait_phase_for(smem_addr(&ctl.full[s]), (pend_phase >> s) & 1u, kDrainLimitNs);
+        atomicOr(p.status, kStatusTimeout);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ scale copies and MMAs (leader)
+    if (rank == 0 && unit0 < total) {
+      Ring rt;
+      uint32_t acc = 0, acc_phase = 0;
+      bool ok = true;
+      const uint64_t w_desc0 = smem_desc_k_sw128(w_ring), t_desc0 = smem_desc_k_sw128(t_ring);
+      const uint64_t s_desc0 = smem_desc_scales(s_ring);
+      const uint32_t sfa = tmem_base + kF4ScaleCol, sfb = sfa + 4u * S::kWords;
+      for (uint32_t t = unit0; t < total && ok; t += units) {
+        const Tile ti = f4_decode_tile<kMx>(t, prefix, p);
+        const bool acc_free = __all_sync(
+            0xffffffffu, wait_phase_cluster<true>(smem_addr(&ctl.acc_empty[acc]), acc_phase ^ 1u, abort));
+        if (!acc_free) { ok = false; break; }
+        tc_fence_after_sync();
+        const uint32_t d_tmem = tmem_base + acc * kF4AccCols;
+        for (int kb = 0; kb < KB; ++kb) {
+          // Acquire at cluster scope: the peer's scale warps wrote its shared memory.
+          const bool staged =
+              __all_sync(0xffffffffu, wait_phase_cluster(smem_addr(&ctl.full[rt.slot]), rt.phase, abort));
+          if (!staged) { ok = false; break; }
+          tc_fence_after_sync();
+          const uint64_t a_desc = w_desc0 + ((rt.slot * kF4WBytes) >> 4);
+          const uint64_t b_desc = t_desc0 + ((rt.slot * kF4TBytes) >> 4);
+          const uint64_t s_desc = s_desc0 + ((rt.slot * S::kBytes) >> 4);
+#pragma unroll
+          for (uint32_t j = 0; j < S::kWords; ++j) {
+            tmem_copy_scales_pair(sfa + 4u * j, s_desc + ((j * kF4Atom) >> 4));
+            tmem_copy_scales_pair(sfb + 8u * j, s_desc + (((S::kWords + 2u * j) * kF4Atom) >> 4));
+            if (ti.ntok > 128u)
+              tmem_copy_scales_pair(sfb + 8u * j + 4u, s_desc + (((S::kWords + 2u * j + 1u) * kF4Atom) >> 4));
+          }
+#pragma unroll
+          for (uint32_t k = 0; k < 4; ++k) {   // 64 of K each: +32 bytes, +2 in the >>4 address field
+            const uint32_t j = k / S::kStepsPerWord;
+            mma_e2m1_pair<!kMx>(d_tmem, a_desc + 2u * k, b_desc + 2u * k,
+                                idesc_e2m1_f32(G::kRows, ti.ntok, kMx, kMx ? 2u * (k & 1u) : 0u), sfa + 4u * j,
+                                sfb + 8u * j, (kb | static_cast<int>(k)) != 0);
+          }
+          mma_commit_pair(smem_addr(&ctl.empty[rt.slot]), 0x3);
+          rt.next(ST);
+        }
+        if (!ok) break;
+        mma_commit_pair(smem_addr(&ctl.acc_full[acc]), 0x3);
+        acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      if (!ok && lane == 0) atomicOr(p.status, kStatusTimeout);
+    }
+  } else if (warp < static_cast<int>(kF4FirstScaleWarp)) {
+    // ------------------------------------------------------------ epilogue
+    if (warp == 2) {   // the producer's token maps, as in the grouped kernel
+      uint8_t *slot = p.map_slots + static_cast<size_t>(blockIdx.x) * kMapSlotBytes;
+      if (total > 0 && lane < static_cast<int>(kF4MaxTok / 32)) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(&p.tok_map);
+        uint4 *dst = reinterpret_cast<uint4 *>(slot + lane * 128);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dst[i] = src[i];
+        tensormap_set_dim1(dst, __ldg(p.a_offsets + p.num_groups));
+        tensormap_set_box1(dst, 16u * static_cast<uint32_t>(lane + 1));
+        tensormap_release();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&ctl.maps_ready));
+    }
+    const uint32_t quad = static_cast<uint32_t>(warp & 3);
+    const uint32_t ew = static_cast<uint32_t>(warp - 2), esub = ew >> 2;
+    constexpr uint32_t kSub = kF4EpiWarps / 4;   // warps per quadrant
+    const uint32_t stg0 = epi_ring + ew * kF4StgBufs * kF4StgBytes;
+    const uint32_t acc_empty0 = map_to_rank(smem_addr(&ctl.acc_empty[0]), 0);
+    const uint32_t acc_empty1 = map_to_rank(smem_addr(&ctl.acc_empty[1]), 0);
+    const float ga = p.g_a != nullptr ? __ldg(p.g_a) : 1.0f;
+    const bool fused = p.epi_bias != nullptr || p.epi_row_scale != nullptr || p.epi_act != kActNone;
+    uint32_t acc = 0, acc_phase = 0, buf = 0, outstanding = 0;
+    for (uint32_t t = unit0; t < total; t += units) {
+      const Tile ti = f4_decode_tile<kMx>(t, prefix, p);
+      const uint32_t seg = static_cast<uint32_t>(lane) & 3u, rsub = static_cast<uint32_t>(lane) >> 2;
+      const uint32_t ncta = ti.n0 + rank * kBlockN + quad * 32u;   // this warp's first C column
+      const uint32_t n8 = ncta + seg * 8u;
+      const bool cols_ok = n8 < static_cast<uint32_t>(p.N);
+      __nv_bfloat16 *crow = p.c + static_cast<size_t>(ti.row0) * p.N + n8;
+      const uint32_t taddr = tmem_base + ((quad * 32u) << 16) + acc * kF4AccCols;
+      const float gs = ga * (p.g_w != nullptr ? __ldg(p.g_w + ti.e) : 1.0f);
+      // Operands of the fused epilogue, loaded before the accumulator wait: the bias of the
+      // thread's 4 fragment columns, the row scales of this warp's chunks (lane l: row l).
+      constexpr int kRowRegs = static_cast<int>((kF4MaxTok / 32 + kSub - 1) / kSub);
+      float rs[kRowRegs], bias4[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t n = ncta + 8u * i + rsub;
+        bias4[i] = p.epi_bias != nullptr && n < static_cast<uint32_t>(p.N)
+                       ? __bfloat162float(p.epi_bias[static_cast<size_t>(ti.e) * p.N + n])
+                       : 0.0f;
+      }
+#pragma unroll
+      for (int q = 0; q < kRowRegs; ++q) {
+        const uint32_t r = (static_cast<uint32_t>(q) * kSub + esub) * 32u + static_cast<uint32_t>(lane);
+        rs[q] = p.epi_row_scale != nullptr && r < ti.nrows ? __ldg(p.epi_row_scale + ti.row0 + r) : 1.0f;
+      }
+      int ok = 1;
+      if (lane == 0) ok = wait_phase(smem_addr(&ctl.acc_full[acc]), acc_phase, abort);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) {
+        if (lane == 0) atomicOr(p.status, kStatusTimeout);
+        break;
+      }
+      tc_fence_after_sync();
+      const uint32_t st_row = static_cast<uint32_t>(lane) & 7u, st_blk = static_cast<uint32_t>(lane) >> 3;
+      for (uint32_t c0 = esub * 32u; c0 < ti.ntok; c0 += 32u * kSub) {
+        uint32_t va[16], vb[16];
+        tmem_ld_16x256b_x4(taddr + c0, va);
+        tmem_ld_16x256b_x4(taddr + (16u << 16) + c0, vb);
+        // The two staging buffers in turn: of the stores in flight, all but the newest must
+        // have read theirs.
+        const uint32_t stg = stg0 + buf * kF4StgBytes;
+        if (lane == 0 && ((outstanding >> buf) & 1u)) {
+          if (outstanding == 3u) bulk_wait_read<1>(); else bulk_wait_read<0>();
+        }
+        outstanding &= ~(1u << buf);
+        tmem_ld_wait();
+        __syncwarp();
+#pragma unroll
+        for (uint32_t g = 0; g < 4; ++g) {
+          float s0 = 1.0f, s1 = 1.0f;
+          if (fused) {
+            s0 = __shfl_sync(0xffffffffu, rs[0], static_cast<int>(8 * g + 2 * seg));
+            s1 = __shfl_sync(0xffffffffu, rs[0], static_cast<int>(8 * g + 2 * seg + 1));
+          }
+          uint32_t w[4];
+#pragma unroll
+          for (uint32_t i = 0; i < 4; ++i) {
+            const uint32_t *v = (i >> 1) ? vb : va;
+            float y0 = __uint_as_float(v[4 * g + 2 * (i & 1)]) * gs;
+            float y1 = __uint_as_float(v[4 * g + 2 * (i & 1) + 1]) * gs;
+            if (fused) {
+              y0 = epilogue_op(y0, bias4[i], p.epi_act, s0);
+              y1 = epilogue_op(y1, bias4[i], p.epi_act, s1);
+            }
+            w[i] = pack_bf16x2(y0, y1);
+          }
+          const uint32_t row = 8 * g + st_row;
+          stmatrix_x4_trans(stg + row * kEpiRowBytes + ((st_blk ^ ((row >> 1) & 3u)) << 4), w[0], w[1], w[2], w[3]);
+        }
+        if (p.c_tma && c0 + 32u <= ti.nrows && ncta < static_cast<uint32_t>(p.N)) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&p.c_map, stg, static_cast<int32_t>(ncta), static_cast<int32_t>(ti.row0 + c0));
+            bulk_commit();
+          }
+          outstanding |= 1u << buf;
+        } else {   // 16-byte stores masked to the group's rows
+          __syncwarp();
+          const uint8_t *stg_ptr = dyn_smem + (stg - dyn_base);
+#pragma unroll
+          for (uint32_t pass = 0; pass < 4; ++pass) {
+            const uint32_t rl = pass * 8u + rsub, row = c0 + rl;
+            const uint4 out =
+                *reinterpret_cast<const uint4 *>(stg_ptr + rl * kEpiRowBytes + ((seg ^ ((rl >> 1) & 3u)) << 4));
+            if (cols_ok && row < ti.nrows) *reinterpret_cast<uint4 *>(crow + static_cast<size_t>(row) * p.N) = out;
+          }
+        }
+        buf ^= 1u;
+#pragma unroll
+        for (int q = 0; q + 1 < kRowRegs; ++q) rs[q] = rs[q + 1];
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(acc ? acc_empty1 : acc_empty0);
+      acc ^= 1u;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+    if (lane == 0) bulk_wait_all();
+  } else {
+    // ------------------------------------------------------------ scales
+    // Warp role 0: the CTA's 128 weight rows; 1 and 2: token rows 0 .. 127 and 128 .. 223.
+    // Rows past the matrix or the group repeat the last one (their results are not stored);
+    // scale bytes past K are zeroed, as the values there are.  Loads run kAhead stages ahead
+    // of their use in registers.
+    constexpr int kAhead = 4;
+    constexpr uint32_t kRowStage = kF4StageK / S::kBlock;   // scale bytes per row and stage
+    const uint32_t role = static_cast<uint32_t>(warp) - kF4FirstScaleWarp;
+    const uint32_t full0 = map_to_rank(smem_addr(&ctl.full[0]), 0);
+    const int row_bytes = 4 * p.K / static_cast<int>(S::kBlock);
+    Ring rt;
+    bool ok = true;
+    for (uint32_t t = unit0; t < total && ok; t += units) {
+      const Tile ti = f4_decode_tile<kMx>(t, prefix, p);
+      const uint8_t *src[4];
+#pragma unroll
+      for (uint32_t c = 0; c < 4; ++c) {
+        const uint32_t m = 32u * c + static_cast<uint32_t>(lane);
+        if (role == 0) {
+          const uint32_t n = min(ti.n0 + rank * kBlockN + m, static_cast<uint32_t>(p.N) - 1u);
+          src[c] = p.sf_w + (static_cast<size_t>(ti.e) * p.N + n) * p.sf_pitch;
+        } else {
+          const uint32_t r = min((role - 1u) * 128u + m, ti.nrows - 1u);
+          src[c] = p.sf_a + (static_cast<size_t>(ti.row0) + r) * p.sf_pitch;
+        }
+      }
+      const bool work = role < 2 || ti.ntok > 128u;
+      uint32_t v[kAhead][4][S::kWords];
+      auto load = [&](uint32_t (&x)[4][S::kWords], int kb) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if constexpr (kMx) {
+            const uint2 y = __ldg(reinterpret_cast<const uint2 *>(src[c] + kb * kRowStage));
+            x[c][0] = y.x;
+            x[c][1] = y.y;
+          } else {
+            const uint4 y = __ldg(reinterpret_cast<const uint4 *>(src[c] + kb * kRowStage));
+            x[c][0] = y.x;
+            x[c][1] = y.y;
+            x[c][2] = y.z;
+            x[c][3] = y.w;
+          }
+        }
+      };
+      if (work) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+          if (i < KB) load(v[i], i);
+      }
+      for (int kb0 = 0; kb0 < KB && ok; kb0 += kAhead) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int kb = kb0 + i;
+          if (kb < KB && ok) {
+            if (!__all_sync(0xffffffffu, wait_phase(smem_addr(&ctl.empty[rt.slot]), rt.phase ^ 1u, abort))) {
+              ok = false;
+            } else {
+              if (work) {
+                const uint32_t dst = s_ring + rt.slot * S::kBytes + static_cast<uint32_t>(lane) * 16u +
+                                     (role == 0 ? 0u : (S::kWords + role - 1u) * kF4Atom);
+                const int left = row_bytes - kb * static_cast<int>(kRowStage);   // scale bytes before K's end
+#pragma unroll
+                for (uint32_t j = 0; j < S::kWords; ++j) {
+                  const int nb = left - 4 * static_cast<int>(j);
+                  const uint32_t mask = nb >= 4 ? 0xffffffffu : (nb <= 0 ? 0u : (1u << (8 * nb)) - 1u);
+                  st_shared_v4(dst + j * (role == 0 ? kF4Atom : 2u * kF4Atom), v[i][0][j] & mask, v[i][1][j] & mask,
+                               v[i][2][j] & mask, v[i][3][j] & mask);
+                }
+                if (kb + kAhead < KB) load(v[i], kb + kAhead);
+                fence_async_smem();   // these writes, before the tensor-memory copies read them
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(full0 + rt.slot * 8u);
+              rt.next(ST);
+            }
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) atomicOr(p.status, kStatusTimeout);
+  }
+
+  __syncthreads();
+  cluster_sync();   // no CTA leaves while its peer may still signal it
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+}  // namespace gmm

@@ -1,0 +1,496 @@
+// Tokens sorted by expert and back, for sm_103a.
+//
+// A router gives every token t its top_k experts: slot s = t * top_k + j holds expert
+// id e_s.  With E experts and S = tokens * top_k slots:
+//   dispatch      a stable counting sort of the slots by expert:
+//                   a_offsets[e] = #{ s : 0 <= e_s < e },  a_offsets[E] = the rows in use,
+//                   row(s) = a_offsets[e_s] + #{ s' < s : e_s' = e_s },
+//                 slot_rows[s] = row(s) (-1 for a dropped slot), row_slots its inverse (-1
+//                 past the rows in use), and rows[row(s), :] = tokens[s / top_k, :].
+//   combine       out[t, :] = sum_j w[t, j] * rows[slot_rows[t, j], :]
+//                 (w = 1: the gradient of dispatch's copy).
+//   combine_grad  d_rows[slot_rows[t, j], :] = w[t, j] * d_out[t, :],
+//                 d_w[t, j] = < d_out[t, :], rows[slot_rows[t, j], :] >.
+// Every sum has a fixed order (j ascending; a dot product per lane, then a fixed tree),
+// no result depends on the order of atomics.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstdint>
+
+#include "gmm_kernel.cuh"
+
+namespace gmm {
+
+constexpr uint32_t kStatusBadSlot = 16u;   // a slot_rows / row_slots value outside its range
+
+constexpr int kRouteThreads = 512;
+constexpr int kRouteWarps = kRouteThreads / 32;
+constexpr int kRouteMaxTopK = 32;          // a token's slots are held one per lane
+constexpr int kRouteSmallSlots = 4096;     // up to here (and kRouteSmallExperts) one launch sorts and copies
+constexpr int kRouteSmallExperts = 1024;
+constexpr int kRouteMaxExperts = 4096;     // one group per expert: the grouped kernels' limit
+constexpr int kRouteMaxCounts = 32768;     // chunk counts (chunks x experts) in the workspace
+constexpr int kRouteMaxChunks = 152;
+constexpr int kRouteBatch = 64;            // tokens whose rows a CTA holds in shared memory at a time
+
+struct DispatchParams {
+  const int32_t *slot_experts;   // [tokens, top_k]
+  uint32_t *a_offsets;           // [E + 1]
+  int32_t *slot_rows;            // [tokens, top_k]
+  int32_t *row_slots;            // [tokens * top_k]
+  const uint8_t *tokens;         // [tokens, width] with a row pitch, or null (no copy)
+  uint8_t *rows;                 // [tokens * top_k, width] contiguous
+  long long token_pitch;         // bytes
+  long long row_bytes;
+  int num_tokens;
+  int top_k;
+  int num_experts;
+  int chunks;                    // two-launch form: chunks of chunk_tokens tokens
+  int chunk_tokens;
+  int subs;                      // two-launch form: CTAs of the copy per chunk
+  uint32_t *counts;              // workspace [chunks, E]
+  uint32_t *status;
+};
+
+// Stable ranks of the slots [begin, end) (one warp's contiguous share) among the slots of
+// the same expert in that share; cnt[e] ends as the share's count of expert e.  Thirty-two
+// slots a step: lanes with the same expert find one another with a warp match, the lowest
+// of them advances the count.  `emit(s, e, rank)` is called for every slot (rank -1 when
+// its expert id is out of range).
+template <class Emit>
+__device__ __forceinline__ uint32_t route_rank_share(const int32_t *ids, int begin, int end, int E, uint32_t *cnt,
+                                                     Emit emit) {
+  const uint32_t lane = threadIdx.x & 31u;
+  uint32_t flags = 0;
+  for (int s0 = begin; s0 < end; s0 += 32) {
+    const int s = s0 + static_cast<int>(lane);
+    const int e = s < end ? __ldg(ids + s) : -1;
+    const bool ok = e >= 0 && e < E;
+    if (e >= E) flags = kStatusBadExpert;
+    const uint32_t peers = __match_any_sync(0xffffffffu, ok ? e : -1);
+    const uint32_t below = __popc(peers & ((1u << lane) - 1u));
+    uint32_t first = 0;
+    if (ok) first = cnt[e];
+    __syncwarp();
+    if (ok && below == 0) cnt[e] = first + __popc(peers);
+    __syncwarp();
+    if (s < end) emit(s, e, ok ? static_cast<int>(first + below) : -1);
+  }
+  return flags;
+}
+
+// Exclusive scan of v[0 .. n) in shared memory by the whole CTA; v[n] receives the total.
+// `warp_sums` holds kRouteWarps words.
+__device__ __forceinline__ void route_scan(uint32_t *v, int n, uint32_t *warp_sums) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (n + kRouteThreads - 1) / kRouteThreads;
+  const int b = min(n, tid * per), e = min(n, b + per);
+  uint32_t mine = 0;
+  for (int i = b; i < e; ++i) mine += v[i];
+  uint32_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  uint32_t run = incl - mine;
+  for (int w = 0; w < warp; ++w) run += warp_sums[w];
+  for (int i = b; i < e; ++i) {
+    const uint32_t x = v[i];
+    v[i] = run;
+    run += x;
+  }
+  if (tid == kRouteThreads - 1) v[n] = run;
+  __syncthreads();
+}
+
+template <int VB>
+struct RouteVec;
+template <>
+struct RouteVec<16> { using type = uint4; };
+template <>
+struct RouteVec<4> { using type = uint32_t; };
+template <>
+struct RouteVec<2> { using type = unsigned short; };
+
+// Copies of tokens [t0, t0 + n) to their rows; rows_s[i * top_k + j] is the row of slot j
+// of token t0 + i (-1: dropped).  A unit is up to 4 vectors a lane of one token: read once,
+// written to each of its rows.  Units go to the CTA's warps in turn, `part` of `parts` CTAs.
+template <int VB>
+__device__ __forceinline__ void route_copy(const DispatchParams &p, const int *rows_s, int t0, int n, int part,
+                                           int parts) {
+  using V = typename RouteVec<VB>::type;
+  constexpr int kU = 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int nvec = static_cast<int>(p.row_bytes / VB);
+  const int pieces = (nvec + 32 * kU - 1) / (32 * kU);
+  const int units = n * pieces;
+  for (int u = part * kRouteWarps + warp; u < units; u += parts * kRouteWarps) {
+    const int i = u / pieces, v0 = (u - i * pieces) * 32 * kU + lane;
+    const V *src = reinterpret_cast<const V *>(p.tokens + (t0 + i) * p.token_pitch);
+    V x[kU];
+#pragma unroll
+    for (int q = 0; q < kU; ++q)
+      if (v0 + 32 * q < nvec) x[q] = __ldg(src + v0 + 32 * q);
+    for (int j = 0; j < p.top_k; ++j) {
+      const int r = rows_s[i * p.top_k + j];
+      if (r < 0) continue;
+      V *dst = reinterpret_cast<V *>(p.rows + r * p.row_bytes);
+#pragma unroll
+      for (int q = 0; q < kU; ++q)
+        if (v0 + 32 * q < nvec) dst[v0 + 32 * q] = x[q];
+    }
+  }
+}
+
+// One launch for few slots: every CTA sorts all of them (a read of at most 16 KB that sits
+// in L2, about a microsecond) and copies its share, which saves the second launch that a
+// count before the copy would need.  CTA 0 writes the maps.
+template <int VB>
+__global__ void __launch_bounds__(kRouteThreads) gmm_dispatch_small_kernel(const __grid_constant__ DispatchParams p) {
+  extern __shared__ uint32_t route_smem[];
+  __shared__ uint32_t warp_sums[kRouteWarps];
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int E = p.num_experts, S = p.num_tokens * p.top_k;
+  uint32_t *cnt = route_smem;                                       // [kRouteWarps][E]
+  uint32_t *off = cnt + kRouteWarps * E;                            // [E + 1]
+  int *row_s = reinterpret_cast<int *>(off + E + 1);                // [S]
+  for (int i = tid; i < kRouteWarps * E; i += kRouteThreads) cnt[i] = 0;
+  __syncthreads();
+  const int share = ((S + kRouteWarps - 1) / kRouteWarps + 31) & ~31;
+  const int begin = min(S, warp * share), end = min(S, begin + share);
+  const uint32_t flags = route_rank_share(p.slot_experts, begin, end, E, cnt + warp * E,
+                                          [&](int s, int, int rank) { row_s[s] = rank; });
+  __syncthreads();
+  for (int e = tid; e < E; e += kRouteThreads) {
+    uint32_t run = 0;
+#pragma unroll
+    for (int w = 0; w < kRouteWarps; ++w) {
+      const uint32_t c = cnt[w * E + e];
+      cnt[w * E + e] = run;
+      run += c;
+    }
+    off[e] = run;
+  }
+  __syncthreads();
+  route_scan(off, E, warp_sums);
+  for (int s = begin + (tid & 31); s < end; s += 32) {
+    const int rank = row_s[s];
+    int row = -1;
+    if (rank >= 0) {
+      const int e = __ldg(p.slot_experts + s);
+      row = static_cast<int>(off[e] + cnt[warp * E + e]) + rank;
+    }
+    row_s[s] = row;
+    if (blockIdx.x == 0) {
+      p.slot_rows[s] = row;
+      if (row >= 0) p.row_slots[row] = s;
+    }
+  }
+  if (blockIdx.x == 0) {
+    for (int e = tid; e <= E; e += kRouteThreads) p.a_offsets[e] = off[e];
+    for (int r = static_cast<int>(off[E]) + tid; r < S; r += kRouteThreads) p.row_slots[r] = -1;
+    if (flags) atomicOr(p.status, flags);
+  }
+  if (p.tokens == nullptr) return;
+  __syncthreads();
+  route_copy<VB>(p, row_s, 0, p.num_tokens, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
+}
+
+// Many slots, first launch: CTA c counts the experts of its chunk of tokens and leaves every
+// slot's rank among the chunk's slots of the same expert in slot_rows.
+__global__ void __launch_bounds__(kRouteThreads) gmm_dispatch_count_kernel(const __grid_constant__ DispatchParams p,
+                                                                           int warps) {
+  extern __shared__ uint32_t route_smem[];
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int E = p.num_experts;
+  const long long t0 = static_cast<long long>(blockIdx.x) * p.chunk_tokens;
+  const int first = static_cast<int>(min(t0, static_cast<long long>(p.num_tokens))) * p.top_k;
+  const int last = static_cast<int>(min(t0 + p.chunk_tokens, static_cast<long long>(p.num_tokens))) * p.top_k;
+  uint32_t *cnt = route_smem;   // [warps][E]
+  for (int i = tid; i < warps * E; i += kRouteThreads) cnt[i] = 0;
+  __syncthreads();
+  const int share = ((last - first + warps - 1) / warps + 31) & ~31;
+  const int begin = min(last, first + warp * share), end = warp < warps ? min(last, begin + share) : begin;
+  if (warp < warps) {
+    const uint32_t flags = route_rank_share(p.slot_experts, begin, end, E, cnt + warp * E,
+                                            [&](int s, int, int rank) { p.slot_rows[s] = rank; });
+    if (flags) atomicOr(p.status, flags);
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += kRouteThreads) {
+    uint32_t run = 0;
+    for (int w = 0; w < warps; ++w) {
+      const uint32_t c = cnt[w * E + e];
+      cnt[w * E + e] = run;
+      run += c;
+    }
+    p.counts[static_cast<size_t>(blockIdx.x) * E + e] = run;
+  }
+  __syncthreads();
+  for (int s = begin + (tid & 31); s < end; s += 32) {   // the same thread wrote slot_rows[s] above
+    const int e = __ldg(p.slot_experts + s);
+    if (e >= 0 && e < E) p.slot_rows[s] += static_cast<int>(cnt[warp * E + e]);
+  }
+}
+
+// Second launch: a CTA sums the chunk counts (at most 128 KB, from L2) into the first row of
+// every expert's slots in its chunk, then places and copies its tokens, kRouteBatch at a time.
+template <int VB>
+__global__ void __launch_bounds__(kRouteThreads) gmm_dispatch_place_kernel(const __grid_constant__ DispatchParams p) {
+  extern __shared__ uint32_t route_smem[];
+  __shared__ uint32_t warp_sums[kRouteWarps];
+  const int tid = threadIdx.x;
+  const int E = p.num_experts, S = p.num_tokens * p.top_k;
+  uint32_t *off = route_smem;                                // [E + 1]: totals, then their exclusive scan
+  uint32_t *bef = off + E + 1;                               // [E]: counts of the chunks before this one
+  int *row_s = reinterpret_cast<int *>(bef + E);             // [kRouteBatch * top_k]
+  const int chunk = static_cast<int>(blockIdx.x) / p.subs, sub = static_cast<int>(blockIdx.x) % p.subs;
+  for (int e = tid; e < E; e += kRouteThreads) {
+    off[e] = 0;
+    bef[e] = 0;
+  }
+  __syncthreads();
+  // Threads in groups of E (one expert a thread) take the chunks in turn.
+  const int groups = max(1, kRouteThreads / E);
+  const int g = E <= kRouteThreads ? tid / E : 0;
+  if (g < groups) {
+    for (int e = E <= kRouteThreads ? tid - g * E : tid; e < E; e += kRouteThreads) {
+      uint32_t total = 0, before = 0;
+#pragma unroll 4
+      for (int c = g; c < p.chunks; c += groups) {
+        const uint32_t n = __ldg(p.counts + static_cast<size_t>(c) * E + e);
+        total += n;
+        before += c < chunk ? n : 0u;
+      }
+      atomicAdd(&off[e], total);
+      atomicAdd(&bef[e], before);
+    }
+  }
+  __syncthreads();
+  route_scan(off, E, warp_sums);
+  if (blockIdx.x == 0)
+    for (int e = tid; e <= E; e += kRouteThreads) p.a_offsets[e] = off[e];
+  for (int r = static_cast<int>(off[E]) + static_cast<int>(blockIdx.x) * kRouteThreads + tid; r < S;
+       r += static_cast<int>(gridDim.x) * kRouteThreads)
+    p.row_slots[r] = -1;
+  const long long c0 = static_cast<long long>(chunk) * p.chunk_tokens;
+  const int per = (p.chunk_tokens + p.subs - 1) / p.subs;
+  const int lim = static_cast<int>(min(c0 + p.chunk_tokens, static_cast<long long>(p.num_tokens)));
+  const int t_begin = static_cast<int>(min(c0 + static_cast<long long>(sub) * per, static_cast<long long>(lim)));
+  const int t_end = min(lim, t_begin + per);
+  for (int t = t_begin; t < t_end; t += kRouteBatch) {
+    const int n = min(kRouteBatch, t_end - t);
+    __syncthreads();   // the previous batch's copies have read row_s
+    for (int i = tid; i < n * p.top_k; i += kRouteThreads) {
+      const int s = t * p.top_k + i;
+      const int e = __ldg(p.slot_experts + s);
+      int row = -1;
+      if (e >= 0 && e < E) {
+        row = static_cast<int>(off[e] + bef[e]) + p.slot_rows[s];
+        p.row_slots[row] = s;
+        p.slot_rows[s] = row;
+      }
+      row_s[i] = row;
+    }
+    __syncthreads();
+    if (p.tokens != nullptr) route_copy<VB>(p, row_s, t, n, 0, 1);
+  }
+}
+
+// ---------------------------------------------------------------- combine and its gradient
+
+struct CombineParams {
+  uint8_t *out;                // combine: [tokens, width], row pitch out_pitch
+  const uint8_t *rows;         // [num_rows, width] contiguous
+  const int32_t *slot_rows;    // [tokens, top_k]
+  const float *weights;        // [tokens, top_k] or null (ones)
+  const uint8_t *d_out;        // gradient: [tokens, width], row pitch out_pitch
+  uint8_t *d_rows;             // gradient: [num_rows, width]
+  float *d_weights;            // gradient: [tokens, top_k] or null
+  long long out_pitch;         // bytes
+  long long row_bytes;
+  int num_tokens;
+  int top_k;
+  int num_rows;
+  int warps_per_token;         // gradient
+  uint32_t *status;
+};
+
+// VN consecutive elements of type T in one load or store.
+template <class T>
+__device__ __forceinline__ float route_to_float(T x);
+template <>
+__device__ __forceinline__ float route_to_float(float x) { return x; }
+template <>
+__device__ __forceinline__ float route_to_float(__half x) { return __half2float(x); }
+template <>
+__device__ __forceinline__ float route_to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <class T>
+__device__ __forceinline__ T route_from_float(float x);
+template <>
+__device__ __forceinline__ float route_from_float(float x) { return x; }
+template <>
+__device__ __forceinline__ __half route_from_float(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 route_from_float(float x) { return __float2bfloat16_rn(x); }
+
+template <class T, int VN>
+struct RoutePack {
+  alignas(sizeof(T) * VN) T v[VN];
+};
+
+template <class T, int VN>
+__device__ __forceinline__ RoutePack<T, VN> route_load(const uint8_t *row, int i) {
+  if constexpr (sizeof(T) * VN == 16) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(row) + i);
+    return *reinterpret_cast<const RoutePack<T, VN> *>(&x);
+  } else {
+    RoutePack<T, VN> r;
+    r.v[0] = reinterpret_cast<const T *>(row)[i];
+    return r;
+  }
+}
+
+template <class T, int VN>
+__device__ __forceinline__ void route_store(uint8_t *row, int i, const RoutePack<T, VN> &x) {
+  if constexpr (sizeof(T) * VN == 16)
+    reinterpret_cast<uint4 *>(row)[i] = *reinterpret_cast<const uint4 *>(&x);
+  else
+    reinterpret_cast<T *>(row)[i] = x.v[0];
+}
+
+// This lane's slot of token t: its row (-1: none) and weight.
+__device__ __forceinline__ int route_slot(const CombineParams &p, int t, int lane, float *w) {
+  int r = -1;
+  *w = 0.0f;
+  if (lane < p.top_k) {
+    const size_t s = static_cast<size_t>(t) * p.top_k + lane;
+    r = __ldg(p.slot_rows + s);
+    if (r >= p.num_rows) {
+      atomicOr(p.status, kStatusBadSlot);
+      r = -1;
+    }
+    if (r >= 0) *w = p.weights != nullptr ? __ldg(p.weights + s) : 1.0f;
+  }
+  return r;
+}
+
+constexpr int kCombineWarps = 8;
+constexpr int kCombineBatch = 8;   // rows of a token whose loads are in flight together
+
+// A warp per (token, 32 vectors).
+template <class T, int VN>
+__global__ void __launch_bounds__(32 * kCombineWarps) gmm_combine_kernel(const __grid_constant__ CombineParams p) {
+  const int lane = threadIdx.x & 31;
+  const int nvec = static_cast<int>(p.row_bytes / (sizeof(T) * VN));
+  const int pieces = (nvec + 31) / 32;
+  const long long u = static_cast<long long>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5);
+  if (u >= static_cast<long long>(p.num_tokens) * pieces) return;
+  const int t = static_cast<int>(u / pieces);
+  const int v = static_cast<int>(u - static_cast<long long>(t) * pieces) * 32 + lane;
+  float w;
+  const int r = route_slot(p, t, lane, &w);
+  float acc[VN];
+#pragma unroll
+  for (int i = 0; i < VN; ++i) acc[i] = 0.0f;
+  for (int j0 = 0; j0 < p.top_k; j0 += kCombineBatch) {
+    RoutePack<T, VN> x[kCombineBatch];
+    float wj[kCombineBatch];
+    bool has[kCombineBatch];
+#pragma unroll
+    for (int q = 0; q < kCombineBatch; ++q) {
+      const int rj = __shfl_sync(0xffffffffu, r, (j0 + q) & 31);
+      wj[q] = __shfl_sync(0xffffffffu, w, (j0 + q) & 31);
+      has[q] = j0 + q < p.top_k && rj >= 0 && v < nvec;
+      if (has[q]) x[q] = route_load<T, VN>(p.rows + rj * p.row_bytes, v);
+    }
+#pragma unroll
+    for (int q = 0; q < kCombineBatch; ++q)
+      if (has[q]) {
+#pragma unroll
+        for (int i = 0; i < VN; ++i) acc[i] = fmaf(wj[q], route_to_float<T>(x[q].v[i]), acc[i]);
+      }
+  }
+  if (v < nvec) {
+    RoutePack<T, VN> y;
+#pragma unroll
+    for (int i = 0; i < VN; ++i) y.v[i] = route_from_float<T>(acc[i]);
+    route_store<T, VN>(p.out + t * p.out_pitch, v, y);
+  }
+}
+
+// warps_per_token warps per token (a power of two up to kCombineWarps): they take the
+// token's 32-vector pieces in turn, four rows at a time, and join their dot products
+// through shared memory in warp order.
+template <class T, int VN>
+__global__ void __launch_bounds__(32 * kCombineWarps)
+    gmm_combine_grad_kernel(const __grid_constant__ CombineParams p) {
+  constexpr int kRows = 4;
+  __shared__ float part[kCombineWarps][kRouteMaxTopK];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int nvec = static_cast<int>(p.row_bytes / (sizeof(T) * VN));
+  const int wpt = p.warps_per_token, tpc = kCombineWarps / wpt;
+  const int t = static_cast<int>(blockIdx.x) * tpc + warp / wpt, sub = warp % wpt;
+  const bool live = t < p.num_tokens;
+  float w = 0.0f;
+  int r = -1;
+  if (live) r = route_slot(p, t, lane, &w);
+  const uint8_t *g_row = p.d_out + (live ? t : 0) * p.out_pitch;
+  for (int j0 = 0; j0 < p.top_k; j0 += kRows) {
+    int rj[kRows];
+    float wj[kRows], dot[kRows];
+    bool any = false;
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) {
+      rj[q] = __shfl_sync(0xffffffffu, r, (j0 + q) & 31);
+      wj[q] = __shfl_sync(0xffffffffu, w, (j0 + q) & 31);
+      if (j0 + q >= p.top_k) rj[q] = -1;
+      any = any || rj[q] >= 0;
+      dot[q] = 0.0f;
+    }
+    if (any) {
+#pragma unroll 2
+      for (int v = sub * 32 + lane; v < nvec; v += wpt * 32) {
+        const RoutePack<T, VN> g = route_load<T, VN>(g_row, v);
+        RoutePack<T, VN> x[kRows];
+        if (p.d_weights != nullptr) {
+#pragma unroll
+          for (int q = 0; q < kRows; ++q)
+            if (rj[q] >= 0) x[q] = route_load<T, VN>(p.rows + rj[q] * p.row_bytes, v);
+        }
+#pragma unroll
+        for (int q = 0; q < kRows; ++q)
+          if (rj[q] >= 0) {
+            RoutePack<T, VN> y;
+#pragma unroll
+            for (int i = 0; i < VN; ++i) {
+              const float gi = route_to_float<T>(g.v[i]);
+              if (p.d_weights != nullptr) dot[q] = fmaf(gi, route_to_float<T>(x[q].v[i]), dot[q]);
+              y.v[i] = route_from_float<T>(wj[q] * gi);
+            }
+            route_store<T, VN>(p.d_rows + rj[q] * p.row_bytes, v, y);
+          }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) dot[q] += __shfl_xor_sync(0xffffffffu, dot[q], o);
+      if (lane == 0 && j0 + q < p.top_k) part[warp][j0 + q] = dot[q];
+    }
+  }
+  if (p.d_weights == nullptr) return;
+  __syncthreads();
+  if (live && sub == 0 && lane < p.top_k) {
+    float d = 0.0f;
+    for (int i = 0; i < wpt; ++i) d += part[warp + i][lane];
+    p.d_weights[static_cast<size_t>(t) * p.top_k + lane] = d;
+  }
+}
+
+}  // namespace gmm

@@ -105,6 +105,10 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
 // ----------------------------------------------------------------- TMA
 
 // L2 eviction-priority policies for TMA loads (.L2::cache_hint operands).
@@ -630,7 +634,60 @@ __device__ __forceinline__ void mma_stage_f8_x4(uint32_t d_tmem, uint32_t a_lo, 
       : "memory");
 }
 
+// Pair MMA of e2m1 operands with block scales (kind::mxf4nvf4, K = 64 per instruction: 32
+// bytes of each 128-byte swizzled row, so the descriptors and their step are again the
+// bf16 ones).  The scales lie in tensor memory, one 32-bit word of four scales per operand
+// row: row m at lane m % 32 (of every 32-lane quadrant) and column m / 32 from the given
+// address.  kVec4: four scales per row and instruction (block 16), else two (block 32),
+// the word's first or second half by the scale ids of the instruction descriptor.
+template <bool kVec4>
+__device__ __forceinline__ void mma_e2m1_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  if constexpr (kVec4) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b32 l;\n\t"
+        "elect.sync l|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b32 l;\n\t"
+        "elect.sync l|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+  }
+}
+
+// Copy 32 rows of 16 bytes from shared memory (in both CTAs of the pair, each its own) to
+// 4 columns of tensor memory, the same in each of the four 32-lane quadrants.  Executes in
+// order with the MMAs of the same thread.
+__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t desc) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b32 l;\n\t"
+      "elect.sync l|e, 0xffffffff;\n\t"
+      "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+      "l"(desc)
+      : "memory");
+}
+
 // ----------------------------------------------------------------- descriptors
+
+// Shared-memory descriptor of 32 rows x 16 bytes for the copy above: no swizzle, 8-row core
+// matrices of 128 bytes one after the other.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);   // [0,14)  start address >> 4
+  d |= static_cast<uint64_t>(16u >> 4) << 16;            // [16,30) leading byte offset (one column of matrices: unused)
+  d |= static_cast<uint64_t>(128u >> 4) << 32;           // [32,46) stride byte offset: 8 rows x 16 B
+  d |= static_cast<uint64_t>(1u) << 46;                  // [46,48) descriptor version
+  return d;
+}
 
 // Shared-memory matrix descriptor for a K-major operand tile written by TMA with
 // 128-byte swizzling: rows of 64 bf16 (128 B), 8-row swizzle atoms 1024 B apart.
@@ -663,6 +720,19 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
          | (0u << 10)           // B format: e4m3
          | ((N >> 3) << 17)     // N / 8
          | ((M >> 4) << 24);    // M / 16
+}
+
+// Instruction descriptor, kind::mxf4nvf4: e2m1 A and B, fp32 D, shape M x N, e8m0 or e4m3
+// block scales; `sf_id` is the first of the scale word's bytes that the instruction reads
+// (both operands; 0, or 2 with two scales per row).
+__host__ __device__ constexpr uint32_t idesc_e2m1_f32(uint32_t M, uint32_t N, bool e8m0, uint32_t sf_id) {
+  return (sf_id << 4)                    // B scale id
+         | (1u << 7)                     // A format: e2m1
+         | (1u << 10)                    // B format: e2m1
+         | ((N >> 3) << 17)              // N / 8
+         | ((e8m0 ? 1u : 0u) << 23)      // scale format
+         | ((M >> 4) << 24)              // M / 16
+         | (sf_id << 29);                // A scale id
 }
 
 }  // namespace gmm
