@@ -1094,10 +1094,10 @@ int gmm_run_fp4(gmm_handle_t h, void *c, const void *a, const uint32_t *a_offset
   if (rc) return rc;
   fill_common(h, p, c, a_offsets, expert_ids, expert_usage_stats, num_groups, N, KU, gmm::kF4MaxTok);
   set_epilogue(p, epilogue);
-  p.sf_a = static_cast<const uint8_t *>(a_scales);
-  p.sf_w = static_cast<const uint8_t *>(b_scales);
   p.g_a = a_global;
   p.g_w = b_global;
+  p.sf_a = static_cast<const uint8_t *>(a_scales);
+  p.sf_w = static_cast<const uint8_t *>(b_scales);
   p.sf_pitch = fp4_scale_pitch(K, format);
   return format == GMM_FP4_MX ? launch_fp4<true>(h, p, stream) : launch_fp4<false>(h, p, stream);
 }

@@ -17,7 +17,9 @@
 // warps load them: lane l takes rows l, l + 32, l + 64, l + 96 of a 128-row block, and the
 // four rows' word j are 16 bytes of a 512-byte atom (one per block and word) in the stage's
 // shared memory, from where tcgen05.cp spreads it over the quadrants.  The copies run in
-// order with the MMAs of the issuing thread, so one set of scale columns serves all stages.
+// order with the MMAs of the issuing thread and beside them (12 copies and 4 MMAs of 192
+// columns measured 385 cycles, the MMAs alone 385), so one set of scale columns serves all
+// stages.
 // Both CTAs of a pair hold the scales of all the tile's tokens (each computes its own 128
 // weight rows against all of them), and of their own 128 weight rows.
 //
@@ -29,10 +31,11 @@
 //   warps 2..9    epilogue, two per TMEM lane quadrant taking every second 32-row chunk.
 //   warps 10..12  scales: the weight rows' block, and the tokens' two.
 //
-// Tiles are the static share of each pair (tile t, t + pairs, ...); a group's rows are cut
-// into equal token blocks (to the granule of 32).  Every wait is bounded as in the grouped
-// kernel.
+// Tiles are the static share of each pair (tile t, t + pairs, ...).  Every wait is bounded as
+// in the grouped kernel.
 #pragma once
+
+#include <type_traits>
 
 #include "gmm_kernel.cuh"
 
@@ -75,24 +78,21 @@ constexpr size_t kF4FixedBytes = 1024 + kF4EpiWarps * kF4StgBufs * kF4StgBytes;
 struct alignas(128) F4Params : GmmParams {   // K counts two-byte units: 4 elements each
   const uint8_t *sf_a;     // [rows, sf_pitch]
   const uint8_t *sf_w;     // [E, N, sf_pitch]
+  int sf_pitch;            // bytes, a multiple of 16
   const float *g_a;        // one value or null
   const float *g_w;        // [E] or null
-  int sf_pitch;            // bytes, a multiple of 16
 };
 
-// Tile t with the group's rows cut into equal blocks: as many as kF4MaxTok asks for, each
-// the same multiple of 32 rows (the last one less).
 template <bool kMx>
 __device__ __forceinline__ Tile f4_decode_tile(uint32_t t, const uint32_t *prefix, const GmmParams &p) {
-  Tile x = decode_tile<F4Geom<kMx>>(t, prefix, p);
-  return x;
+  return decode_tile<F4Geom<kMx>>(t, prefix, p);
 }
 
 template <bool kMx>
 __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_constant__ F4Params p) {
   using G = F4Geom<kMx>;
   using S = F4Scale<kMx>;
-  constexpr uint32_t kFullArrivals = 1 + 2 * kF4ScaleWarps;
+  constexpr uint32_t kFullArrivals = 1 + 2 * kF4ScaleWarps;   // the values, both CTAs' scale warps
   constexpr uint32_t kEpiArrivals = 2 * kF4EpiWarps;
   __shared__ Ctrl ctl;
   extern __shared__ uint8_t dyn_smem[];
@@ -200,8 +200,12 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
       Ring rt;
       uint32_t acc = 0, acc_phase = 0;
       bool ok = true;
-      const uint64_t w_desc0 = smem_desc_k_sw128(w_ring), t_desc0 = smem_desc_k_sw128(t_ring);
-      const uint64_t s_desc0 = smem_desc_scales(s_ring);
+      const uint64_t w_desc = smem_desc_k_sw128(w_ring), t_desc = smem_desc_k_sw128(t_ring);
+      const uint64_t s_desc = smem_desc_scales(s_ring);
+      const uint32_t w_lo = static_cast<uint32_t>(w_desc), t_lo = static_cast<uint32_t>(t_desc);
+      const uint32_t v_hi = static_cast<uint32_t>(w_desc >> 32);   // the same for both value operands
+      const uint32_t s_lo = static_cast<uint32_t>(s_desc), s_hi = static_cast<uint32_t>(s_desc >> 32);
+      const uint32_t empty0 = smem_addr(&ctl.empty[0]);
       const uint32_t sfa = tmem_base + kF4ScaleCol, sfb = sfa + 4u * S::kWords;
       for (uint32_t t = unit0; t < total && ok; t += units) {
         const Tile ti = f4_decode_tile<kMx>(t, prefix, p);
@@ -210,30 +214,17 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
         if (!acc_free) { ok = false; break; }
         tc_fence_after_sync();
         const uint32_t d_tmem = tmem_base + acc * kF4AccCols;
+        const uint32_t idesc = idesc_e2m1_f32(G::kRows, ti.ntok, kMx, 0);
+        const uint32_t idesc2 = idesc_e2m1_f32(G::kRows, ti.ntok, kMx, 2);
+        const uint32_t two = ti.ntok > 128u;
         for (int kb = 0; kb < KB; ++kb) {
-          // Acquire at cluster scope: the peer's scale warps wrote its shared memory.
           const bool staged =
               __all_sync(0xffffffffu, wait_phase_cluster(smem_addr(&ctl.full[rt.slot]), rt.phase, abort));
           if (!staged) { ok = false; break; }
           tc_fence_after_sync();
-          const uint64_t a_desc = w_desc0 + ((rt.slot * kF4WBytes) >> 4);
-          const uint64_t b_desc = t_desc0 + ((rt.slot * kF4TBytes) >> 4);
-          const uint64_t s_desc = s_desc0 + ((rt.slot * S::kBytes) >> 4);
-#pragma unroll
-          for (uint32_t j = 0; j < S::kWords; ++j) {
-            tmem_copy_scales_pair(sfa + 4u * j, s_desc + ((j * kF4Atom) >> 4));
-            tmem_copy_scales_pair(sfb + 8u * j, s_desc + (((S::kWords + 2u * j) * kF4Atom) >> 4));
-            if (ti.ntok > 128u)
-              tmem_copy_scales_pair(sfb + 8u * j + 4u, s_desc + (((S::kWords + 2u * j + 1u) * kF4Atom) >> 4));
-          }
-#pragma unroll
-          for (uint32_t k = 0; k < 4; ++k) {   // 64 of K each: +32 bytes, +2 in the >>4 address field
-            const uint32_t j = k / S::kStepsPerWord;
-            mma_e2m1_pair<!kMx>(d_tmem, a_desc + 2u * k, b_desc + 2u * k,
-                                idesc_e2m1_f32(G::kRows, ti.ntok, kMx, kMx ? 2u * (k & 1u) : 0u), sfa + 4u * j,
-                                sfb + 8u * j, (kb | static_cast<int>(k)) != 0);
-          }
-          mma_commit_pair(smem_addr(&ctl.empty[rt.slot]), 0x3);
+          mma_stage_e2m1_pair<!kMx>(d_tmem, w_lo + rt.slot * (kF4WBytes >> 4), t_lo + rt.slot * (kF4TBytes >> 4), v_hi,
+                                    idesc, idesc2, s_lo + rt.slot * (S::kBytes >> 4), s_hi, sfa, sfb, kb != 0, two,
+                                    empty0 + rt.slot * 8u);
           rt.next(ST);
         }
         if (!ok) break;
@@ -245,7 +236,8 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
     }
   } else if (warp < static_cast<int>(kF4FirstScaleWarp)) {
     // ------------------------------------------------------------ epilogue
-    if (warp == 2) {   // the producer's token maps, as in the grouped kernel
+    if (warp == 2) {
+      // The producer's token maps, as in the grouped kernel.
       uint8_t *slot = p.map_slots + static_cast<size_t>(blockIdx.x) * kMapSlotBytes;
       if (total > 0 && lane < static_cast<int>(kF4MaxTok / 32)) {
         const uint4 *src = reinterpret_cast<const uint4 *>(&p.tok_map);
@@ -371,82 +363,104 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
     // ------------------------------------------------------------ scales
     // Warp role 0: the CTA's 128 weight rows; 1 and 2: token rows 0 .. 127 and 128 .. 223.
     // Rows past the matrix or the group repeat the last one (their results are not stored);
-    // scale bytes past K are zeroed, as the values there are.  Loads run kAhead stages ahead
-    // of their use in registers.
-    constexpr int kAhead = 4;
+    // scale bytes past K are zeroed, as the values there are.  A row is read 32 bytes (a whole
+    // L2 sector, kStages stages) at a time, one chunk ahead of its use in registers, by one
+    // load: two loads of 16 bytes fetch a sector twice when the line has left L1 in between
+    // (prefill shapes: 0.93 ms instead of 0.71).
     constexpr uint32_t kRowStage = kF4StageK / S::kBlock;   // scale bytes per row and stage
+    constexpr int kStages = static_cast<int>(32 / kRowStage);
+    constexpr int kBufs = 2;
     const uint32_t role = static_cast<uint32_t>(warp) - kF4FirstScaleWarp;
     const uint32_t full0 = map_to_rank(smem_addr(&ctl.full[0]), 0);
     const int row_bytes = 4 * p.K / static_cast<int>(S::kBlock);
-    Ring rt;
+    const uint32_t atom0 = s_ring + static_cast<uint32_t>(lane) * 16u + (role == 0 ? 0u : (S::kWords + role - 1u) * kF4Atom);
+    const uint32_t atom_step = role == 0 ? kF4Atom : 2u * kF4Atom;
+    // Every chunk is one 32-byte load when the rows are that far apart and aligned.
+    const bool whole = ((static_cast<uint32_t>(p.sf_pitch) | static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.sf_a)) |
+                         static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.sf_w))) & 31u) == 0;
     bool ok = true;
-    for (uint32_t t = unit0; t < total && ok; t += units) {
-      const Tile ti = f4_decode_tile<kMx>(t, prefix, p);
-      const uint8_t *src[4];
+    // Two copies of the loop: a choice inside it would make every load wait for its result.
+    auto run = [&](auto whole_rows) {
+      Ring rt;
+      for (uint32_t t = unit0; t < total && ok; t += units) {
+        const Tile ti = f4_decode_tile<kMx>(t, prefix, p);
+        const uint8_t *src[4];
 #pragma unroll
-      for (uint32_t c = 0; c < 4; ++c) {
-        const uint32_t m = 32u * c + static_cast<uint32_t>(lane);
-        if (role == 0) {
-          const uint32_t n = min(ti.n0 + rank * kBlockN + m, static_cast<uint32_t>(p.N) - 1u);
-          src[c] = p.sf_w + (static_cast<size_t>(ti.e) * p.N + n) * p.sf_pitch;
-        } else {
-          const uint32_t r = min((role - 1u) * 128u + m, ti.nrows - 1u);
-          src[c] = p.sf_a + (static_cast<size_t>(ti.row0) + r) * p.sf_pitch;
-        }
-      }
-      const bool work = role < 2 || ti.ntok > 128u;
-      uint32_t v[kAhead][4][S::kWords];
-      auto load = [&](uint32_t (&x)[4][S::kWords], int kb) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if constexpr (kMx) {
-            const uint2 y = __ldg(reinterpret_cast<const uint2 *>(src[c] + kb * kRowStage));
-            x[c][0] = y.x;
-            x[c][1] = y.y;
+        for (uint32_t c = 0; c < 4; ++c) {
+          const uint32_t m = 32u * c + static_cast<uint32_t>(lane);
+          if (role == 0) {
+            const uint32_t n = min(ti.n0 + rank * kBlockN + m, static_cast<uint32_t>(p.N) - 1u);
+            src[c] = p.sf_w + (static_cast<size_t>(ti.e) * p.N + n) * p.sf_pitch;
           } else {
-            const uint4 y = __ldg(reinterpret_cast<const uint4 *>(src[c] + kb * kRowStage));
-            x[c][0] = y.x;
-            x[c][1] = y.y;
-            x[c][2] = y.z;
-            x[c][3] = y.w;
+            const uint32_t r = min((role - 1u) * 128u + m, ti.nrows - 1u);
+            src[c] = p.sf_a + (static_cast<size_t>(ti.row0) + r) * p.sf_pitch;
           }
         }
-      };
-      if (work) {
+        const bool work = role < 2 || ti.ntok > 128u;
+        uint32_t v[kBufs][4][8];
+        auto load = [&](uint32_t (&x)[4][8], int chunk) {
+          const int at = chunk * 32;
+          if constexpr (decltype(whole_rows)::value) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-          if (i < KB) load(v[i], i);
-      }
-      for (int kb0 = 0; kb0 < KB && ok; kb0 += kAhead) {
+            for (int c = 0; c < 4; ++c) ld_global_nc_v8(src[c] + at, x[c]);
+          } else {   // the row pitch is an odd number of 16 bytes: two loads, the second may lie past the row
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          const int kb = kb0 + i;
-          if (kb < KB && ok) {
-            if (!__all_sync(0xffffffffu, wait_phase(smem_addr(&ctl.empty[rt.slot]), rt.phase ^ 1u, abort))) {
-              ok = false;
-            } else {
-              if (work) {
-                const uint32_t dst = s_ring + rt.slot * S::kBytes + static_cast<uint32_t>(lane) * 16u +
-                                     (role == 0 ? 0u : (S::kWords + role - 1u) * kF4Atom);
-                const int left = row_bytes - kb * static_cast<int>(kRowStage);   // scale bytes before K's end
+            for (int c = 0; c < 4; ++c) {
+              const uint4 y = __ldg(reinterpret_cast<const uint4 *>(src[c] + at));
+              const uint4 z = at + 16 < p.sf_pitch ? __ldg(reinterpret_cast<const uint4 *>(src[c] + at) + 1)
+                                                   : make_uint4(0u, 0u, 0u, 0u);
+              x[c][0] = y.x;
+              x[c][1] = y.y;
+              x[c][2] = y.z;
+              x[c][3] = y.w;
+              x[c][4] = z.x;
+              x[c][5] = z.y;
+              x[c][6] = z.z;
+              x[c][7] = z.w;
+            }
+          }
+        };
+        const int chunks = (KB + kStages - 1) / kStages;
+        if (work) {
 #pragma unroll
-                for (uint32_t j = 0; j < S::kWords; ++j) {
-                  const int nb = left - 4 * static_cast<int>(j);
-                  const uint32_t mask = nb >= 4 ? 0xffffffffu : (nb <= 0 ? 0u : (1u << (8 * nb)) - 1u);
-                  st_shared_v4(dst + j * (role == 0 ? kF4Atom : 2u * kF4Atom), v[i][0][j] & mask, v[i][1][j] & mask,
-                               v[i][2][j] & mask, v[i][3][j] & mask);
+          for (int b = 0; b + 1 < kBufs; ++b)
+            if (b < chunks) load(v[b], b);
+        }
+        for (int c0 = 0; c0 < chunks && ok; c0 += kBufs) {
+#pragma unroll
+          for (int b = 0; b < kBufs; ++b) {
+            if (work && c0 + b + kBufs - 1 < chunks) load(v[(b + kBufs - 1) % kBufs], c0 + b + kBufs - 1);
+#pragma unroll
+            for (int i = 0; i < kStages; ++i) {
+              const int kb = (c0 + b) * kStages + i;
+              if (kb < KB && ok) {
+                if (!__all_sync(0xffffffffu, wait_phase(smem_addr(&ctl.empty[rt.slot]), rt.phase ^ 1u, abort))) {
+                  ok = false;
+                } else {
+                  if (work) {
+                    const uint32_t dst = atom0 + rt.slot * S::kBytes;
+                    const int left = row_bytes - kb * static_cast<int>(kRowStage);   // scale bytes before K's end
+#pragma unroll
+                    for (uint32_t j = 0; j < S::kWords; ++j) {
+                      const int nb = left - 4 * static_cast<int>(j);
+                      const uint32_t mask = nb >= 4 ? 0xffffffffu : (nb <= 0 ? 0u : (1u << (8 * nb)) - 1u);
+                      const uint32_t w = static_cast<uint32_t>(i) * S::kWords + j;
+                      st_shared_v4(dst + j * atom_step, v[b][0][w] & mask, v[b][1][w] & mask, v[b][2][w] & mask,
+                                   v[b][3][w] & mask);
+                    }
+                  }
+                  fence_async_smem();   // these writes, before the tensor-memory copies read them
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive_remote(full0 + rt.slot * 8u);
+                  rt.next(ST);
                 }
-                if (kb + kAhead < KB) load(v[i], kb + kAhead);
-                fence_async_smem();   // these writes, before the tensor-memory copies read them
               }
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(full0 + rt.slot * 8u);
-              rt.next(ST);
             }
           }
         }
       }
-    }
+    };
+    if (whole) run(std::true_type()); else run(std::false_type());
     if (!ok && lane == 0) atomicOr(p.status, kStatusTimeout);
   }
 

@@ -109,6 +109,13 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t x, uint32_t
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
+// 32-byte load of read-only global memory (32-byte aligned), not kept in L1.
+__device__ __forceinline__ void ld_global_nc_v8(const void *ptr, uint32_t (&x)[8]) {
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7])
+               : "l"(ptr));
+}
+
 // ----------------------------------------------------------------- TMA
 
 // L2 eviction-priority policies for TMA loads (.L2::cache_hint operands).
@@ -462,6 +469,16 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// Arrive, possibly on another CTA's mbarrier, ordering this thread's earlier writes for
+// readers in its own CTA (release at CTA scope).  For data that a pair MMA or a tensor-memory
+// copy reads through the async proxy of the CTA that wrote it, after fence.proxy.async: the
+// leader's instruction makes each CTA's tensor core read its own shared memory, and no
+// generic read crosses CTAs.  A release at cluster scope waits for every memory operation of
+// the thread, about 0.7 us here.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 __device__ __forceinline__ bool mbar_test_wait_cluster(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
@@ -634,47 +651,70 @@ __device__ __forceinline__ void mma_stage_f8_x4(uint32_t d_tmem, uint32_t a_lo, 
       : "memory");
 }
 
-// Pair MMA of e2m1 operands with block scales (kind::mxf4nvf4, K = 64 per instruction: 32
-// bytes of each 128-byte swizzled row, so the descriptors and their step are again the
-// bf16 ones).  The scales lie in tensor memory, one 32-bit word of four scales per operand
-// row: row m at lane m % 32 (of every 32-lane quadrant) and column m / 32 from the given
-// address.  kVec4: four scales per row and instruction (block 16), else two (block 32),
-// the word's first or second half by the scale ids of the instruction descriptor.
+// One stage (256 of K) of the 4-bit floating point kernel: the copies of its block scales
+// from shared memory to tensor memory, four pair MMAs of e2m1 operands (kind::mxf4nvf4,
+// K = 64: 32 bytes of each 128-byte swizzled row, so the value descriptors and their step
+// are the bf16 ones) and a commit to both CTAs' `empty`.
+//
+// A scale word holds four scales of one operand row; the 128 rows' words are a 512-byte atom
+// in shared memory (32 rows of 16 bytes: rows l, l + 32, l + 64, l + 96), which tcgen05.cp
+// spreads to 4 columns of every 32-lane quadrant, in each CTA of the pair from its own shared
+// memory.  kVec4 (four scales per row and instruction): word j serves instruction j; else
+// (two) word j serves instructions 2j and 2j + 1, its first and second half by the scale ids
+// of the instruction descriptor (idesc, idesc2).  In shared memory (descriptor s_lo, s_hi) the
+// weights' atoms come first, then per word the tokens' two; tensor memory holds the weights'
+// words from column `sfa`, 4 apart, and the tokens' from `sfb`, 8 apart.  `two` = 0 leaves
+// out the second token atom (at most 128 tokens).
+// The copies run in order with the MMAs; one elected lane issues everything from operands
+// that need no further address arithmetic but adds to the low words: with an elect and
+// 64-bit descriptor arithmetic per instruction the issuing warp took twice the MMAs' time.
+#define GMM_F4_CP(T, OFF, SOFF, P)                                                                       \
+  "add.u32 x, " T ", " OFF ";\n\tadd.u32 y, %6, " SOFF ";\n\tmov.b64 s, {y, %7};\n\t"                     \
+  "@" P " tcgen05.cp.cta_group::2.32x128b.warpx4 [x], s;\n\t"
+#define GMM_F4_MMA(VEC, K2, ID, A, B, P)                                                                   \
+  "add.u32 x, %1, " K2 ";\n\tmov.b64 a, {x, %3};\n\tadd.u32 x, %2, " K2 ";\n\tmov.b64 b, {x, %3};\n\t"       \
+  "add.u32 x, %8, " A ";\n\tadd.u32 y, %9, " B ";\n\t"                                                     \
+  "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::" VEC "X [%0], a, b, " ID ", [x], [y], " P ";\n\t"
+#define GMM_F4_HEAD                                                                                        \
+  "{\n\t.reg .pred e, p, t, q;\n\t.reg .b32 l, x, y;\n\t.reg .b64 a, b, s;\n\t"                            \
+  "elect.sync l|e, 0xffffffff;\n\t"                                                                       \
+  "setp.ne.b32 p, %10, 0;\n\tsetp.eq.b32 t, %10, %10;\n\tsetp.ne.b32 q, %11, 0;\n\tand.pred q, q, e;\n\t"
+#define GMM_F4_TAIL                                                                                        \
+  "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%12], %13;\n\t}"
+
 template <bool kVec4>
-__device__ __forceinline__ void mma_e2m1_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                              uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+__device__ __forceinline__ void mma_stage_e2m1_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t ab_hi,
+                                                    uint32_t idesc, uint32_t idesc2, uint32_t s_lo, uint32_t s_hi,
+                                                    uint32_t sfa, uint32_t sfb, uint32_t accumulate, uint32_t two,
+                                                    uint32_t empty) {
   if constexpr (kVec4) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t.reg .b32 l;\n\t"
-        "elect.sync l|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-            d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
-        : "memory");
+    asm volatile(GMM_F4_HEAD
+                 GMM_F4_CP("%8", "0", "0", "e") GMM_F4_CP("%9", "0", "128", "e") GMM_F4_CP("%9", "4", "160", "q")
+                 GMM_F4_MMA("4", "0", "%4", "0", "0", "p")
+                 GMM_F4_CP("%8", "4", "32", "e") GMM_F4_CP("%9", "8", "192", "e") GMM_F4_CP("%9", "12", "224", "q")
+                 GMM_F4_MMA("4", "2", "%4", "4", "8", "t")
+                 GMM_F4_CP("%8", "8", "64", "e") GMM_F4_CP("%9", "16", "256", "e") GMM_F4_CP("%9", "20", "288", "q")
+                 GMM_F4_MMA("4", "4", "%4", "8", "16", "t")
+                 GMM_F4_CP("%8", "12", "96", "e") GMM_F4_CP("%9", "24", "320", "e") GMM_F4_CP("%9", "28", "352", "q")
+                 GMM_F4_MMA("4", "6", "%4", "12", "24", "t")
+                 GMM_F4_TAIL ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(ab_hi), "r"(idesc), "r"(idesc2), "r"(s_lo), "r"(s_hi),
+                 "r"(sfa), "r"(sfb), "r"(accumulate), "r"(two), "r"(empty), "h"(static_cast<uint16_t>(3))
+                 : "memory");
   } else {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t.reg .b32 l;\n\t"
-        "elect.sync l|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-            d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
-        : "memory");
+    asm volatile(GMM_F4_HEAD
+                 GMM_F4_CP("%8", "0", "0", "e") GMM_F4_CP("%9", "0", "64", "e") GMM_F4_CP("%9", "4", "96", "q")
+                 GMM_F4_MMA("2", "0", "%4", "0", "0", "p") GMM_F4_MMA("2", "2", "%5", "0", "0", "t")
+                 GMM_F4_CP("%8", "4", "32", "e") GMM_F4_CP("%9", "8", "128", "e") GMM_F4_CP("%9", "12", "160", "q")
+                 GMM_F4_MMA("2", "4", "%4", "4", "8", "t") GMM_F4_MMA("2", "6", "%5", "4", "8", "t")
+                 GMM_F4_TAIL ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(ab_hi), "r"(idesc), "r"(idesc2), "r"(s_lo), "r"(s_hi),
+                 "r"(sfa), "r"(sfb), "r"(accumulate), "r"(two), "r"(empty), "h"(static_cast<uint16_t>(3))
+                 : "memory");
   }
 }
-
-// Copy 32 rows of 16 bytes from shared memory (in both CTAs of the pair, each its own) to
-// 4 columns of tensor memory, the same in each of the four 32-lane quadrants.  Executes in
-// order with the MMAs of the same thread.
-__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t desc) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t.reg .b32 l;\n\t"
-      "elect.sync l|e, 0xffffffff;\n\t"
-      "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
-      "l"(desc)
-      : "memory");
-}
+#undef GMM_F4_CP
+#undef GMM_F4_MMA
+#undef GMM_F4_HEAD
+#undef GMM_F4_TAIL
 
 // ----------------------------------------------------------------- descriptors
 
