@@ -160,10 +160,19 @@ def gmm_destroy(h: Handle) -> None:
             raise GmmError(rc, "gmm_destroy")
 
 
+_raw_stream = None
+
+
 def stream_handle(device: int, stream=None) -> ctypes.c_void_p:
-    import torch
+    global _raw_stream
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        if _raw_stream is None:
+            import torch
+            # torch's current stream as an integer; the Stream object that current_stream builds
+            # costs more than a kernel launch's own marshalling.
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                  lambda d: torch.cuda.current_stream(d).cuda_stream)
+        return ctypes.c_void_p(_raw_stream(device))
     return ctypes.c_void_p(int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -171,20 +180,26 @@ def _check(t, name, dtypes, device, min_numel=0):
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda" or t.device.index != device:
+    if not t.is_cuda or t.get_device() != device:
         raise ValueError(f"{name} must live on cuda:{device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.numel() < min_numel:
+    if min_numel and t.numel() < min_numel:
         raise ValueError(f"{name} needs at least {min_numel} elements")
     return ctypes.c_void_p(t.data_ptr())
 
 
+_I32_TYPES = None
+
+
 def _i32_types():
-    import torch
-    return (torch.int32,) + ((torch.uint32,) if hasattr(torch, "uint32") else ())
+    global _I32_TYPES
+    if _I32_TYPES is None:
+        import torch
+        _I32_TYPES = (torch.int32,) + ((torch.uint32,) if hasattr(torch, "uint32") else ())
+    return _I32_TYPES
 
 
 def _routing_args(h, a_offsets, expert_ids, stats):
@@ -417,13 +432,15 @@ def _check_strided(t, name, dtypes, device, out=False):
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda" or t.device.index != device:
+    if not t.is_cuda or t.get_device() != device:
         raise ValueError(f"{name} must live on cuda:{device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D, got {t.dim()}-D")
     rows, width = t.shape
+    if t.is_contiguous():
+        return ctypes.c_void_p(t.data_ptr()), width
     stride = t.stride(0) if rows > 1 else width
     if (width > 1 and t.stride(1) != 1) or (out and stride < width):
         raise ValueError(f"{name} must have contiguous rows{' that do not overlap' if out else ''}, got strides {t.stride()}")
@@ -541,9 +558,9 @@ def fp4_scale_pitch(K: int, fmt="nvfp4") -> int:
 
 def _check_fp4(packed, scales, names, fmt, lead, K, device):
     import torch
-    if tuple(packed.shape) != (*lead, K // 2):
+    if packed.shape != (*lead, K // 2):
         raise ValueError(f"{names[0]} must be {(*lead, K // 2)}, got {tuple(packed.shape)}")
-    if tuple(scales.shape) != (*lead, fp4_scale_pitch(K, fmt)):
+    if scales.shape != (*lead, fp4_scale_pitch(K, fmt)):
         raise ValueError(f"{names[1]} must be {(*lead, fp4_scale_pitch(K, fmt))}, got {tuple(scales.shape)}")
     return (_check(packed, names[0], (torch.uint8,), device), _check(scales, names[1], (torch.uint8,), device))
 

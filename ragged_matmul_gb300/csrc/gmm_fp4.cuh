@@ -25,11 +25,12 @@
 //
 // Tensor memory: two accumulators of 224 columns and 48 columns of scales.
 //
-// Roles (416 threads per CTA):
+// Roles (448 threads per CTA):
 //   warp 0        TMA producer of the stage's weight and token values.
 //   warp 1        TMEM allocation; in the pair's leader the scale copies and MMAs.
 //   warps 2..9    epilogue, two per TMEM lane quadrant taking every second 32-row chunk.
 //   warps 10..12  scales: the weight rows' block, and the tokens' two.
+//   warp 13       scheduler: decodes the CTA's tiles into a queue that every role reads.
 //
 // Tiles are the static share of each pair (tile t, t + pairs, ...).  Every wait is bounded as
 // in the grouped kernel.
@@ -44,7 +45,7 @@ namespace gmm {
 constexpr uint32_t kF4EpiWarps = 8;
 constexpr uint32_t kF4ScaleWarps = 3;
 constexpr uint32_t kF4FirstScaleWarp = 2 + kF4EpiWarps;
-constexpr int kF4Threads = 32 * static_cast<int>(2 + kF4EpiWarps + kF4ScaleWarps);
+constexpr int kF4Threads = 32 * static_cast<int>(2 + kF4EpiWarps + kF4ScaleWarps + 1);
 constexpr uint32_t kF4MaxTok = 224;
 constexpr uint32_t kF4TokAlign = 32;
 constexpr uint32_t kF4StageK = 256;
@@ -83,10 +84,39 @@ struct alignas(128) F4Params : GmmParams {   // K counts two-byte units: 4 eleme
   const float *g_w;        // [E] or null
 };
 
-template <bool kMx>
-__device__ __forceinline__ Tile f4_decode_tile(uint32_t t, const uint32_t *prefix, const GmmParams &p) {
-  return decode_tile<F4Geom<kMx>>(t, prefix, p);
-}
+__device__ __forceinline__ uint32_t warp_uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Reader of the CTA's tile queue, which its scheduler warp fills in the order of the CTA's
+// tiles: 1 with the tile, 0 after the last one, -1 when a wait gave up.  By a whole warp or by
+// one thread of it (kWarp = false).
+struct F4Feed {
+  uint32_t pos = 0;
+  template <bool kWarp = true>
+  __device__ __forceinline__ int next(Ctrl &ctl, volatile int *abort, Tile *x) {
+    const uint32_t slot = pos % kTileQueue, parity = (pos / kTileQueue) & 1u;
+    bool ok = wait_phase(smem_addr(&ctl.tq_full[slot]), parity, abort);
+    if (kWarp) ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return -1;
+    uint4 w0 = ld_shared_v4(smem_addr(&ctl.tq_info[slot])), w1 = ld_shared_v4(smem_addr(&ctl.tq_info[slot]) + 16u);
+    if (kWarp) {
+      w0.x = warp_uniform(w0.x);
+      w0.y = warp_uniform(w0.y);
+      w0.z = warp_uniform(w0.z);
+      w0.w = warp_uniform(w0.w);
+      w1.x = warp_uniform(w1.x);
+      w1.y = warp_uniform(w1.y);
+    }
+    if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&ctl.tq_empty[slot]));
+    ++pos;
+    x->e = static_cast<int32_t>(w0.x);
+    x->single_block = w0.y;
+    x->row0 = w0.z;
+    x->nrows = w0.w;
+    x->ntok = w1.x;
+    x->n0 = w1.y;
+    return w0.w != 0u;   // no rows: the end
+  }
+};
 
 template <bool kMx>
 __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_constant__ F4Params p) {
@@ -97,10 +127,13 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
   __shared__ Ctrl ctl;
   extern __shared__ uint8_t dyn_smem[];
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // Warp-uniform values that steer the roles are broadcast from lane 0: the compiler then knows
+  // them to be uniform and keeps what the MMA warp computes from them in uniform registers,
+  // which the tcgen05 instructions read.
+  const int tid = threadIdx.x, warp = static_cast<int>(warp_uniform(static_cast<uint32_t>(tid) >> 5)), lane = tid & 31;
   const uint32_t ST = static_cast<uint32_t>(p.num_stages);
   const int KB = (p.K + kBK - 1) / kBK;   // stages per tile: 64 two-byte units = 256 of K
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t rank = warp_uniform(cluster_ctarank());
 
   const uint32_t dyn_base = smem_addr(dyn_smem);
   const uint32_t w_ring = (dyn_base + 1023u) & ~1023u;
@@ -120,6 +153,10 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
       mbar_init(smem_addr(&ctl.acc_empty[a]), kEpiArrivals);
     }
     mbar_init(smem_addr(&ctl.maps_ready), 1);
+    for (int q = 0; q < kTileQueue; ++q) {
+      mbar_init(smem_addr(&ctl.tq_full[q]), 1);
+      mbar_init(smem_addr(&ctl.tq_empty[q]), 1 + (rank == 0) + kF4EpiWarps + kF4ScaleWarps);
+    }
     ctl.abort = 0;
     ctl.active = 0;
     ctl.flags = 0;
@@ -142,7 +179,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
     if (f) atomicOr(p.status, f);
   }
   tc_fence_after_sync();
-  const uint32_t tmem_base = ctl.tmem_base;
+  const uint32_t tmem_base = warp_uniform(ctl.tmem_base);
   const uint32_t total = ctl.total_tiles;
   volatile int *abort = &ctl.abort;
   const uint32_t unit0 = cluster_id_x(), units = cluster_count_x();
@@ -150,7 +187,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
   if (warp == 0) {
     // ------------------------------------------------------------ value producer
     uint8_t *slot = p.map_slots + static_cast<size_t>(blockIdx.x) * kMapSlotBytes;
-    if (lane == 0 && unit0 < total) {
+    if (lane == 0) {
       const CUtensorMap *tok_maps = reinterpret_cast<const CUtensorMap *>(slot);
       prefetch_tensormap(&p.w_map);
       const uint64_t pol_first = l2_policy_evict_first();
@@ -159,8 +196,13 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
       Ring rt;
       uint32_t pending = 0, pend_phase = 0;
       bool ok = true, maps_acquired = false;
-      for (uint32_t t = unit0; t < total && ok; t += units) {
-        const Tile ti = f4_decode_tile<kMx>(t, prefix, p);
+      F4Feed feed;
+      for (Tile ti; ok;) {
+        const int got = feed.next<false>(ctl, abort, &ti);
+        if (got <= 0) {
+          ok = got == 0;
+          break;
+        }
         const uint32_t my_tok = ti.ntok / 2;
         const uint32_t tx = 2u * (kF4WBytes + my_tok * 128u);
         const int32_t w_row = static_cast<int32_t>(ti.n0 + rank * kBlockN);
@@ -196,7 +238,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ scale copies and MMAs (leader)
-    if (rank == 0 && unit0 < total) {
+    if (rank == 0) {
       Ring rt;
       uint32_t acc = 0, acc_phase = 0;
       bool ok = true;
@@ -205,10 +247,12 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
       const uint32_t w_lo = static_cast<uint32_t>(w_desc), t_lo = static_cast<uint32_t>(t_desc);
       const uint32_t v_hi = static_cast<uint32_t>(w_desc >> 32);   // the same for both value operands
       const uint32_t s_lo = static_cast<uint32_t>(s_desc), s_hi = static_cast<uint32_t>(s_desc >> 32);
-      const uint32_t empty0 = smem_addr(&ctl.empty[0]);
+      const uint32_t full0 = smem_addr(&ctl.full[0]), empty0 = smem_addr(&ctl.empty[0]);
       const uint32_t sfa = tmem_base + kF4ScaleCol, sfb = sfa + 4u * S::kWords;
-      for (uint32_t t = unit0; t < total && ok; t += units) {
-        const Tile ti = f4_decode_tile<kMx>(t, prefix, p);
+      F4Feed feed;
+      Tile ti, tn;
+      int got = feed.next(ctl, abort, &ti);
+      for (; got > 0; ti = tn) {
         const bool acc_free = __all_sync(
             0xffffffffu, wait_phase_cluster<true>(smem_addr(&ctl.acc_empty[acc]), acc_phase ^ 1u, abort));
         if (!acc_free) { ok = false; break; }
@@ -217,22 +261,29 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
         const uint32_t idesc = idesc_e2m1_f32(G::kRows, ti.ntok, kMx, 0);
         const uint32_t idesc2 = idesc_e2m1_f32(G::kRows, ti.ntok, kMx, 2);
         const uint32_t two = ti.ntok > 128u;
+        bool staged = false;
         for (int kb = 0; kb < KB; ++kb) {
-          const bool staged =
-              __all_sync(0xffffffffu, wait_phase_cluster(smem_addr(&ctl.full[rt.slot]), rt.phase, abort));
-          if (!staged) { ok = false; break; }
-          tc_fence_after_sync();
-          mma_stage_e2m1_pair<!kMx>(d_tmem, w_lo + rt.slot * (kF4WBytes >> 4), t_lo + rt.slot * (kF4TBytes >> 4), v_hi,
-                                    idesc, idesc2, s_lo + rt.slot * (S::kBytes >> 4), s_hi, sfa, sfb, kb != 0, two,
-                                    empty0 + rt.slot * 8u);
+          if (!staged) {
+            if (!__all_sync(0xffffffffu, wait_phase_cluster(full0 + rt.slot * 8u, rt.phase, abort))) { ok = false; break; }
+            tc_fence_after_sync();
+          }
+          const uint32_t a = w_lo + rt.slot * (kF4WBytes >> 4), b = t_lo + rt.slot * (kF4TBytes >> 4);
+          const uint32_t s = s_lo + rt.slot * (S::kBytes >> 4), empty = empty0 + rt.slot * 8u;
+          mma_half_stage_e2m1_pair<!kMx, 0>(d_tmem, a, b, v_hi, idesc, idesc2, s, s_hi, sfa, sfb, kb != 0, two, empty);
+          // The next stage's barrier, tested while these MMAs run: when it has completed, as it
+          // has unless the operands are late, the next stage follows without a gap.
           rt.next(ST);
+          staged = kb + 1 < KB && __all_sync(0xffffffffu, mbar_test_wait_cluster(full0 + rt.slot * 8u, rt.phase));
+          if (staged) tc_fence_after_sync();
+          mma_half_stage_e2m1_pair<!kMx, 1>(d_tmem, a, b, v_hi, idesc, idesc2, s, s_hi, sfa, sfb, 1u, two, empty);
+          if (kb == 0) got = feed.next(ctl, abort, &tn);   // behind the MMAs in the pipe
         }
         if (!ok) break;
         mma_commit_pair(smem_addr(&ctl.acc_full[acc]), 0x3);
         acc ^= 1u;
         if (acc == 0) acc_phase ^= 1u;
       }
-      if (!ok && lane == 0) atomicOr(p.status, kStatusTimeout);
+      if ((!ok || got < 0) && lane == 0) atomicOr(p.status, kStatusTimeout);
     }
   } else if (warp < static_cast<int>(kF4FirstScaleWarp)) {
     // ------------------------------------------------------------ epilogue
@@ -260,8 +311,11 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
     const float ga = p.g_a != nullptr ? __ldg(p.g_a) : 1.0f;
     const bool fused = p.epi_bias != nullptr || p.epi_row_scale != nullptr || p.epi_act != kActNone;
     uint32_t acc = 0, acc_phase = 0, buf = 0, outstanding = 0;
-    for (uint32_t t = unit0; t < total; t += units) {
-      const Tile ti = f4_decode_tile<kMx>(t, prefix, p);
+    F4Feed feed;
+    for (Tile ti;;) {
+      const int got = feed.next(ctl, abort, &ti);
+      if (got < 0 && lane == 0) atomicOr(p.status, kStatusTimeout);
+      if (got <= 0) break;
       const uint32_t seg = static_cast<uint32_t>(lane) & 3u, rsub = static_cast<uint32_t>(lane) >> 2;
       const uint32_t ncta = ti.n0 + rank * kBlockN + quad * 32u;   // this warp's first C column
       const uint32_t n8 = ncta + seg * 8u;
@@ -359,7 +413,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
       if (acc == 0) acc_phase ^= 1u;
     }
     if (lane == 0) bulk_wait_all();
-  } else {
+  } else if (warp < static_cast<int>(kF4FirstScaleWarp + kF4ScaleWarps)) {
     // ------------------------------------------------------------ scales
     // Warp role 0: the CTA's 128 weight rows; 1 and 2: token rows 0 .. 127 and 128 .. 223.
     // Rows past the matrix or the group repeat the last one (their results are not stored);
@@ -369,7 +423,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
     // (prefill shapes: 0.93 ms instead of 0.71).
     constexpr uint32_t kRowStage = kF4StageK / S::kBlock;   // scale bytes per row and stage
     constexpr int kStages = static_cast<int>(32 / kRowStage);
-    constexpr int kBufs = 2;
+    const int chunks = (KB + kStages - 1) / kStages;
     const uint32_t role = static_cast<uint32_t>(warp) - kF4FirstScaleWarp;
     const uint32_t full0 = map_to_rank(smem_addr(&ctl.full[0]), 0);
     const int row_bytes = 4 * p.K / static_cast<int>(S::kBlock);
@@ -382,57 +436,69 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
     // Two copies of the loop: a choice inside it would make every load wait for its result.
     auto run = [&](auto whole_rows) {
       Ring rt;
-      for (uint32_t t = unit0; t < total && ok; t += units) {
-        const Tile ti = f4_decode_tile<kMx>(t, prefix, p);
-        const uint8_t *src[4];
+      F4Feed feed;
+      const uint8_t *src[4];   // this lane's four rows of the tile whose chunks are being loaded
+      bool src_work = false;   // and whether this warp has rows of it
+      int got = 1;
+      uint32_t v[2][4][8];
+      auto next_tile = [&]() {
+        Tile x;
+        got = feed.next(ctl, abort, &x);
+        if (got <= 0) return;
+        src_work = role < 2 || x.ntok > 128u;
 #pragma unroll
         for (uint32_t c = 0; c < 4; ++c) {
           const uint32_t m = 32u * c + static_cast<uint32_t>(lane);
           if (role == 0) {
-            const uint32_t n = min(ti.n0 + rank * kBlockN + m, static_cast<uint32_t>(p.N) - 1u);
-            src[c] = p.sf_w + (static_cast<size_t>(ti.e) * p.N + n) * p.sf_pitch;
+            const uint32_t n = min(x.n0 + rank * kBlockN + m, static_cast<uint32_t>(p.N) - 1u);
+            src[c] = p.sf_w + (static_cast<size_t>(x.e) * p.N + n) * p.sf_pitch;
           } else {
-            const uint32_t r = min((role - 1u) * 128u + m, ti.nrows - 1u);
-            src[c] = p.sf_a + (static_cast<size_t>(ti.row0) + r) * p.sf_pitch;
+            const uint32_t r = min((role - 1u) * 128u + m, x.nrows - 1u);
+            src[c] = p.sf_a + (static_cast<size_t>(x.row0) + r) * p.sf_pitch;
           }
         }
-        const bool work = role < 2 || ti.ntok > 128u;
-        uint32_t v[kBufs][4][8];
-        auto load = [&](uint32_t (&x)[4][8], int chunk) {
-          const int at = chunk * 32;
-          if constexpr (decltype(whole_rows)::value) {
+      };
+      auto load = [&](uint32_t (&x)[4][8], int chunk) {
+        const int at = chunk * 32;
+        if constexpr (decltype(whole_rows)::value) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) ld_global_nc_v8(src[c] + at, x[c]);
-          } else {   // the row pitch is an odd number of 16 bytes: two loads, the second may lie past the row
+          for (int c = 0; c < 4; ++c) ld_global_nc_v8(src[c] + at, x[c]);
+        } else {   // the row pitch is an odd number of 16 bytes: two loads, the second may lie past the row
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint4 y = __ldg(reinterpret_cast<const uint4 *>(src[c] + at));
-              const uint4 z = at + 16 < p.sf_pitch ? __ldg(reinterpret_cast<const uint4 *>(src[c] + at) + 1)
-                                                   : make_uint4(0u, 0u, 0u, 0u);
-              x[c][0] = y.x;
-              x[c][1] = y.y;
-              x[c][2] = y.z;
-              x[c][3] = y.w;
-              x[c][4] = z.x;
-              x[c][5] = z.y;
-              x[c][6] = z.z;
-              x[c][7] = z.w;
+          for (int c = 0; c < 4; ++c) {
+            const uint4 y = __ldg(reinterpret_cast<const uint4 *>(src[c] + at));
+            const uint4 z = at + 16 < p.sf_pitch ? __ldg(reinterpret_cast<const uint4 *>(src[c] + at) + 1)
+                                                 : make_uint4(0u, 0u, 0u, 0u);
+            x[c][0] = y.x;
+            x[c][1] = y.y;
+            x[c][2] = y.z;
+            x[c][3] = y.w;
+            x[c][4] = z.x;
+            x[c][5] = z.y;
+            x[c][6] = z.z;
+            x[c][7] = z.w;
+          }
+        }
+      };
+      next_tile();
+      if (got > 0 && src_work) load(v[0], 0);
+      while (got > 0 && ok) {
+        const bool work = src_work;
+        bool ahead = false;   // the next tile's first chunk is on its way
+        for (int c0 = 0; c0 < chunks && ok; c0 += 2) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const int c = c0 + b;
+            if (c + 1 < chunks) {
+              if (work) load(v[b ^ 1], c + 1);
+            } else if (b == 1 && c < chunks) {   // v[0] is free
+              next_tile();
+              if (got > 0 && src_work) load(v[0], 0);
+              ahead = true;
             }
-          }
-        };
-        const int chunks = (KB + kStages - 1) / kStages;
-        if (work) {
-#pragma unroll
-          for (int b = 0; b + 1 < kBufs; ++b)
-            if (b < chunks) load(v[b], b);
-        }
-        for (int c0 = 0; c0 < chunks && ok; c0 += kBufs) {
-#pragma unroll
-          for (int b = 0; b < kBufs; ++b) {
-            if (work && c0 + b + kBufs - 1 < chunks) load(v[(b + kBufs - 1) % kBufs], c0 + b + kBufs - 1);
 #pragma unroll
             for (int i = 0; i < kStages; ++i) {
-              const int kb = (c0 + b) * kStages + i;
+              const int kb = c * kStages + i;
               if (kb < KB && ok) {
                 if (!__all_sync(0xffffffffu, wait_phase(smem_addr(&ctl.empty[rt.slot]), rt.phase ^ 1u, abort))) {
                   ok = false;
@@ -458,10 +524,33 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
             }
           }
         }
+        if (ok && !ahead) {
+          next_tile();
+          if (got > 0 && src_work) load(v[0], 0);
+        }
       }
+      if (got < 0) ok = false;
     };
     if (whole) run(std::true_type()); else run(std::false_type());
     if (!ok && lane == 0) atomicOr(p.status, kStatusTimeout);
+  } else if (lane == 0) {
+    // ------------------------------------------------------------ scheduler
+    // Decodes the CTA's tiles ahead of the roles (a search and loads of about a microsecond,
+    // which in the MMA warp left the tensor cores idle at every tile) and closes the queue
+    // with a tile of no rows.
+    bool ok = true;
+    uint32_t pos = 0;
+    for (uint32_t t = unit0;; t += units, ++pos) {
+      const uint32_t slot = pos % kTileQueue, parity = (pos / kTileQueue) & 1u;
+      Tile x{};
+      if (t < total) x = decode_tile<G>(t, prefix, p);
+      ok = wait_phase(smem_addr(&ctl.tq_empty[slot]), parity ^ 1u, abort);
+      if (!ok) break;
+      ctl.tq_info[slot] = x;
+      mbar_arrive(smem_addr(&ctl.tq_full[slot]));
+      if (t >= total) break;
+    }
+    if (!ok) atomicOr(p.status, kStatusTimeout);
   }
 
   __syncthreads();

@@ -651,10 +651,11 @@ __device__ __forceinline__ void mma_stage_f8_x4(uint32_t d_tmem, uint32_t a_lo, 
       : "memory");
 }
 
-// One stage (256 of K) of the 4-bit floating point kernel: the copies of its block scales
-// from shared memory to tensor memory, four pair MMAs of e2m1 operands (kind::mxf4nvf4,
-// K = 64: 32 bytes of each 128-byte swizzled row, so the value descriptors and their step
-// are the bf16 ones) and a commit to both CTAs' `empty`.
+// Half a stage (128 of the stage's 256 of K) of the 4-bit floating point kernel: the copies
+// of its block scales from shared memory to tensor memory, two pair MMAs of e2m1 operands
+// (kind::mxf4nvf4, K = 64: 32 bytes of each 128-byte swizzled row, so the value descriptors
+// and their step are the bf16 ones) and, after the second half (kHalf = 1), a commit to both
+// CTAs' `empty`.
 //
 // A scale word holds four scales of one operand row; the 128 rows' words are a 512-byte atom
 // in shared memory (32 rows of 16 bytes: rows l, l + 32, l + 64, l + 96), which tcgen05.cp
@@ -668,6 +669,7 @@ __device__ __forceinline__ void mma_stage_f8_x4(uint32_t d_tmem, uint32_t a_lo, 
 // The copies run in order with the MMAs; one elected lane issues everything from operands
 // that need no further address arithmetic but adds to the low words: with an elect and
 // 64-bit descriptor arithmetic per instruction the issuing warp took twice the MMAs' time.
+// The halves leave room to test the next stage's barrier while MMAs are in the pipe.
 #define GMM_F4_CP(T, OFF, SOFF, P)                                                                       \
   "add.u32 x, " T ", " OFF ";\n\tadd.u32 y, %6, " SOFF ";\n\tmov.b64 s, {y, %7};\n\t"                     \
   "@" P " tcgen05.cp.cta_group::2.32x128b.warpx4 [x], s;\n\t"
@@ -679,42 +681,49 @@ __device__ __forceinline__ void mma_stage_f8_x4(uint32_t d_tmem, uint32_t a_lo, 
   "{\n\t.reg .pred e, p, t, q;\n\t.reg .b32 l, x, y;\n\t.reg .b64 a, b, s;\n\t"                            \
   "elect.sync l|e, 0xffffffff;\n\t"                                                                       \
   "setp.ne.b32 p, %10, 0;\n\tsetp.eq.b32 t, %10, %10;\n\tsetp.ne.b32 q, %11, 0;\n\tand.pred q, q, e;\n\t"
-#define GMM_F4_TAIL                                                                                        \
-  "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%12], %13;\n\t}"
+#define GMM_F4_COMMIT                                                                                      \
+  "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%12], %13;\n\t"
+#define GMM_F4_OPERANDS                                                                                    \
+  "r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(ab_hi), "r"(idesc), "r"(idesc2), "r"(s_lo), "r"(s_hi), "r"(sfa), "r"(sfb),  \
+      "r"(accumulate), "r"(two), "r"(empty), "h"(static_cast<uint16_t>(3))
 
-template <bool kVec4>
-__device__ __forceinline__ void mma_stage_e2m1_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t ab_hi,
-                                                    uint32_t idesc, uint32_t idesc2, uint32_t s_lo, uint32_t s_hi,
-                                                    uint32_t sfa, uint32_t sfb, uint32_t accumulate, uint32_t two,
-                                                    uint32_t empty) {
-  if constexpr (kVec4) {
+template <bool kVec4, int kHalf>
+__device__ __forceinline__ void mma_half_stage_e2m1_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t ab_hi,
+                                                         uint32_t idesc, uint32_t idesc2, uint32_t s_lo, uint32_t s_hi,
+                                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate, uint32_t two,
+                                                         uint32_t empty) {
+  if constexpr (kVec4 && kHalf == 0) {
     asm volatile(GMM_F4_HEAD
                  GMM_F4_CP("%8", "0", "0", "e") GMM_F4_CP("%9", "0", "128", "e") GMM_F4_CP("%9", "4", "160", "q")
                  GMM_F4_MMA("4", "0", "%4", "0", "0", "p")
                  GMM_F4_CP("%8", "4", "32", "e") GMM_F4_CP("%9", "8", "192", "e") GMM_F4_CP("%9", "12", "224", "q")
-                 GMM_F4_MMA("4", "2", "%4", "4", "8", "t")
+                 GMM_F4_MMA("4", "2", "%4", "4", "8", "t") "}" ::GMM_F4_OPERANDS
+                 : "memory");
+  } else if constexpr (kVec4) {
+    asm volatile(GMM_F4_HEAD
                  GMM_F4_CP("%8", "8", "64", "e") GMM_F4_CP("%9", "16", "256", "e") GMM_F4_CP("%9", "20", "288", "q")
                  GMM_F4_MMA("4", "4", "%4", "8", "16", "t")
                  GMM_F4_CP("%8", "12", "96", "e") GMM_F4_CP("%9", "24", "320", "e") GMM_F4_CP("%9", "28", "352", "q")
-                 GMM_F4_MMA("4", "6", "%4", "12", "24", "t")
-                 GMM_F4_TAIL ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(ab_hi), "r"(idesc), "r"(idesc2), "r"(s_lo), "r"(s_hi),
-                 "r"(sfa), "r"(sfb), "r"(accumulate), "r"(two), "r"(empty), "h"(static_cast<uint16_t>(3))
+                 GMM_F4_MMA("4", "6", "%4", "12", "24", "t") GMM_F4_COMMIT "}" ::GMM_F4_OPERANDS
+                 : "memory");
+  } else if constexpr (kHalf == 0) {
+    asm volatile(GMM_F4_HEAD
+                 GMM_F4_CP("%8", "0", "0", "e") GMM_F4_CP("%9", "0", "64", "e") GMM_F4_CP("%9", "4", "96", "q")
+                 GMM_F4_MMA("2", "0", "%4", "0", "0", "p") GMM_F4_MMA("2", "2", "%5", "0", "0", "t") "}" ::GMM_F4_OPERANDS
                  : "memory");
   } else {
     asm volatile(GMM_F4_HEAD
-                 GMM_F4_CP("%8", "0", "0", "e") GMM_F4_CP("%9", "0", "64", "e") GMM_F4_CP("%9", "4", "96", "q")
-                 GMM_F4_MMA("2", "0", "%4", "0", "0", "p") GMM_F4_MMA("2", "2", "%5", "0", "0", "t")
                  GMM_F4_CP("%8", "4", "32", "e") GMM_F4_CP("%9", "8", "128", "e") GMM_F4_CP("%9", "12", "160", "q")
-                 GMM_F4_MMA("2", "4", "%4", "4", "8", "t") GMM_F4_MMA("2", "6", "%5", "4", "8", "t")
-                 GMM_F4_TAIL ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(ab_hi), "r"(idesc), "r"(idesc2), "r"(s_lo), "r"(s_hi),
-                 "r"(sfa), "r"(sfb), "r"(accumulate), "r"(two), "r"(empty), "h"(static_cast<uint16_t>(3))
+                 GMM_F4_MMA("2", "4", "%4", "4", "8", "t") GMM_F4_MMA("2", "6", "%5", "4", "8", "t") GMM_F4_COMMIT "}"
+                 ::GMM_F4_OPERANDS
                  : "memory");
   }
 }
+#undef GMM_F4_OPERANDS
+#undef GMM_F4_COMMIT
 #undef GMM_F4_CP
 #undef GMM_F4_MMA
 #undef GMM_F4_HEAD
-#undef GMM_F4_TAIL
 
 // ----------------------------------------------------------------- descriptors
 
