@@ -414,6 +414,17 @@ def gmm_matmul_int4(h: Handle, c, a, b_packed, b_scales, group_size: int = 128, 
 
 # ---------------------------------------------------------------- tokens sorted by expert and back
 
+def _ptr(t, name, dtypes, device, min_numel=0):
+    """_check's pointer as an integer; one test for a tensor that passes."""
+    try:
+        if (t.get_device() == device and t.dtype in dtypes and t.is_contiguous()
+                and (not min_numel or t.numel() >= min_numel)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _check(t, name, dtypes, device, min_numel).value
+
+
 _ROW_TYPES = None
 
 
@@ -432,7 +443,7 @@ def _check_strided(t, name, dtypes, device, out=False):
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.get_device() != device:
+    if t.get_device() != device:
         raise ValueError(f"{name} must live on cuda:{device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
@@ -440,16 +451,16 @@ def _check_strided(t, name, dtypes, device, out=False):
         raise ValueError(f"{name} must be 2-D, got {t.dim()}-D")
     rows, width = t.shape
     if t.is_contiguous():
-        return ctypes.c_void_p(t.data_ptr()), width
+        return t.data_ptr(), width
     stride = t.stride(0) if rows > 1 else width
     if (width > 1 and t.stride(1) != 1) or (out and stride < width):
         raise ValueError(f"{name} must have contiguous rows{' that do not overlap' if out else ''}, got strides {t.stride()}")
-    return ctypes.c_void_p(t.data_ptr()), stride
+    return t.data_ptr(), stride
 
 
 def _slots(t, name, device):
     import torch
-    p = _check(t, name, (torch.int32,), device)
+    p = _ptr(t, name, (torch.int32,), device)
     if t.dim() != 2 or t.shape[1] < 1:
         raise ValueError(f"{name} must be [tokens, top_k]")
     return p, t.shape[0], t.shape[1]
@@ -461,7 +472,7 @@ def _slot_weights(t, name, shape, device):
         return None
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be [tokens, top_k] = {tuple(shape)}, got {tuple(t.shape)}")
-    return _check(t, name, (torch.float32,), device)
+    return _ptr(t, name, (torch.float32,), device)
 
 
 def gmm_dispatch(h: Handle, a_offsets, slot_rows, row_slots, slot_experts, rows=None, tokens=None, stream=None,
@@ -472,9 +483,9 @@ def gmm_dispatch(h: Handle, a_offsets, slot_rows, row_slots, slot_experts, rows=
     rows (asynchronous).  The gradient of the copy is gmm_combine without weights."""
     import torch
     pe, T, k = _slots(slot_experts, "slot_experts", h.device)
-    po = _check(a_offsets, "a_offsets", _i32_types(), h.device, h.num_experts + 1)
+    po = _ptr(a_offsets, "a_offsets", _i32_types(), h.device, h.num_experts + 1)
     psr, T2, k2 = _slots(slot_rows, "slot_rows", h.device)
-    prs = _check(row_slots, "row_slots", (torch.int32,), h.device)
+    prs = _ptr(row_slots, "row_slots", (torch.int32,), h.device)
     if (T2, k2) != (T, k) or row_slots.numel() != T * k:
         raise ValueError(f"slot_rows must be [{T}, {k}] and row_slots [{T * k}]")
     if (rows is None) != (tokens is None):
@@ -485,7 +496,7 @@ def gmm_dispatch(h: Handle, a_offsets, slot_rows, row_slots, slot_experts, rows=
         types = _row_types()
         pt, stride = _check_strided(tokens, "tokens", types, h.device)
         width, dtype = tokens.shape[1], types[tokens.dtype]
-        pr = _check(rows, "rows", (tokens.dtype,), h.device)
+        pr = _ptr(rows, "rows", (tokens.dtype,), h.device)
         if tokens.shape[0] != T or tuple(rows.shape) != (T * k, width):
             raise ValueError(f"tokens must be [{T}, width] and rows [{T * k}, width], got {tuple(tokens.shape)} and "
                              f"{tuple(rows.shape)}")
@@ -502,7 +513,7 @@ def gmm_combine(h: Handle, out, rows, slot_rows, weights=None, stream=None, chec
     types = _row_types()
     psr, T, k = _slots(slot_rows, "slot_rows", h.device)
     po, stride = _check_strided(out, "out", types, h.device, out=True)
-    pr = _check(rows, "rows", (out.dtype,), h.device)
+    pr = _ptr(rows, "rows", (out.dtype,), h.device)
     if rows.dim() != 2 or out.shape[0] != T or out.shape[1] != rows.shape[1]:
         raise ValueError(f"out must be [{T}, width] and rows [num_rows, width], got {tuple(out.shape)} and "
                          f"{tuple(rows.shape)}")
@@ -522,13 +533,13 @@ def gmm_combine_grad(h: Handle, d_rows, d_weights, d_out, rows, slot_rows, weigh
     types = _row_types()
     psr, T, k = _slots(slot_rows, "slot_rows", h.device)
     pg, stride = _check_strided(d_out, "d_out", types, h.device)
-    pd = _check(d_rows, "d_rows", (d_out.dtype,), h.device)
+    pd = _ptr(d_rows, "d_rows", (d_out.dtype,), h.device)
     if d_rows.dim() != 2 or d_out.shape[0] != T or d_out.shape[1] != d_rows.shape[1]:
         raise ValueError(f"d_out must be [{T}, width] and d_rows [num_rows, width], got {tuple(d_out.shape)} and "
                          f"{tuple(d_rows.shape)}")
     pr = None
     if rows is not None:
-        pr = _check(rows, "rows", (d_out.dtype,), h.device)
+        pr = _ptr(rows, "rows", (d_out.dtype,), h.device)
         if tuple(rows.shape) != tuple(d_rows.shape):
             raise ValueError("rows and d_rows must have the same shape")
     elif d_weights is not None:
@@ -562,7 +573,7 @@ def _check_fp4(packed, scales, names, fmt, lead, K, device):
         raise ValueError(f"{names[0]} must be {(*lead, K // 2)}, got {tuple(packed.shape)}")
     if scales.shape != (*lead, fp4_scale_pitch(K, fmt)):
         raise ValueError(f"{names[1]} must be {(*lead, fp4_scale_pitch(K, fmt))}, got {tuple(scales.shape)}")
-    return (_check(packed, names[0], (torch.uint8,), device), _check(scales, names[1], (torch.uint8,), device))
+    return (_ptr(packed, names[0], (torch.uint8,), device), _ptr(scales, names[1], (torch.uint8,), device))
 
 
 def _check_global(t, name, device, numel=1):
@@ -571,7 +582,7 @@ def _check_global(t, name, device, numel=1):
         return None
     if t.numel() != numel:
         raise ValueError(f"{name} must hold {numel} value(s), got {t.numel()}")
-    return _check(t, name, (torch.float32,), device)
+    return _ptr(t, name, (torch.float32,), device)
 
 
 def gmm_quantize_fp4(h: Handle, packed, scales, x, fmt="nvfp4", row_slots=None, top_k: int = 1, global_scale=None,
@@ -587,7 +598,7 @@ def gmm_quantize_fp4(h: Handle, packed, scales, x, fmt="nvfp4", row_slots=None, 
     ps = None
     rows = x.shape[0]
     if row_slots is not None:
-        ps = _check(row_slots, "row_slots", (torch.int32,), h.device)
+        ps = _ptr(row_slots, "row_slots", (torch.int32,), h.device)
         rows = row_slots.numel()
     pp, psc = _check_fp4(packed, scales, ("packed", "scales"), f, (rows,), K, h.device)
     pg = _check_global(global_scale, "global_scale", h.device)
@@ -629,7 +640,7 @@ def gmm_run_fp4(h: Handle, c, a, a_offsets, b, expert_ids, expert_usage_stats, a
     if a.shape[1] != KB or c.shape[1] != N or c.shape[0] != rows or E != h.num_experts:
         raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, c {tuple(c.shape)}, "
                          f"handle E={h.num_experts}")
-    pc = _check(c, "c", (torch.bfloat16,), h.device)
+    pc = _ptr(c, "c", (torch.bfloat16,), h.device)
     pa, pas = _check_fp4(a, a_scales, ("a", "a_scales"), f, (rows,), K, h.device)
     pb, pbs = _check_fp4(b, b_scales, ("b", "b_scales"), f, (E, N), K, h.device)
     pga = _check_global(a_global, "a_global", h.device)

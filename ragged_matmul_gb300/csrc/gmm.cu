@@ -491,7 +491,7 @@ template <int VB>
 int launch_dispatch(gmm_ctx *h, gmm::DispatchParams &p, cudaStream_t stream) {
   const int E = p.num_experts, S = p.num_tokens * p.top_k;
   if (S <= gmm::kRouteSmallSlots && E <= gmm::kRouteSmallExperts) {
-    const long long units = p.tokens ? p.num_tokens * ((p.row_bytes / VB + 127) / 128) : 0;
+    const long long units = p.tokens ? p.num_tokens * ((p.row_bytes / VB + 32 * gmm::kRouteSmallUnit - 1) / (32 * gmm::kRouteSmallUnit)) : 0;
     const long long want = (units + gmm::kRouteWarps - 1) / gmm::kRouteWarps;
     const int grid = static_cast<int>(std::max(1ll, std::min<long long>(want, h->num_sms)));
     gmm::gmm_dispatch_small_kernel<VB><<<grid, gmm::kRouteThreads, small_dispatch_smem(E, S), stream>>>(p);
@@ -507,27 +507,48 @@ int launch_dispatch(gmm_ctx *h, gmm::DispatchParams &p, cudaStream_t stream) {
   const int rc = launch_status("launch of the count kernel");
   if (rc) return rc;
   const size_t smem = (2 * static_cast<size_t>(E) + 1 + static_cast<size_t>(gmm::kRouteBatch) * p.top_k) * 4;
-  gmm::gmm_dispatch_place_kernel<VB><<<p.chunks * p.subs, gmm::kRouteThreads, smem, stream>>>(p);
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.chunks * p.subs));
+  cfg.blockDim = dim3(gmm::kRouteThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, gmm::gmm_dispatch_place_kernel<VB>, p);
   return launch_status("launch of the place kernel");
 }
 
-template <class T, int VN>
-int launch_combine(gmm_ctx *, gmm::CombineParams &p, bool grad, cudaStream_t stream) {
-  const long long nvec = p.row_bytes / static_cast<long long>(sizeof(T) * VN);
-  const long long pieces = (nvec + 31) / 32;
-  if (!grad) {
-    const long long ctas = (p.num_tokens * pieces + gmm::kCombineWarps - 1) / gmm::kCombineWarps;
-    if (ctas > 0x7fffffffll) return GMM_ERR_UNSUPPORTED;
-    gmm::gmm_combine_kernel<T, VN><<<static_cast<unsigned>(ctas), 32 * gmm::kCombineWarps, 0, stream>>>(p);
-    return launch_status("launch of the combine kernel");
-  }
+template <class T, int VN, int kRows, int kUnits>
+void launch_grad(gmm_ctx *h, gmm::CombineParams &p, long long nvec, cudaStream_t stream) {
+  // One warp a token when that fills the SMs (32 resident warps each), else more.
+  const long long pieces = (nvec + 32 * kUnits - 1) / (32 * kUnits);
   int wpt = 1;
-  while (wpt < gmm::kCombineWarps && wpt < pieces && static_cast<long long>(p.num_tokens) * wpt < 152 * 32) wpt *= 2;
+  while (wpt < gmm::kCombineWarps && wpt < pieces && static_cast<long long>(p.num_tokens) * wpt < 32ll * h->num_sms) wpt *= 2;
   p.warps_per_token = wpt;
   const int tpc = gmm::kCombineWarps / wpt;
-  gmm::gmm_combine_grad_kernel<T, VN>
+  gmm::gmm_combine_grad_kernel<T, VN, kRows, kUnits>
       <<<static_cast<unsigned>((p.num_tokens + tpc - 1) / tpc), 32 * gmm::kCombineWarps, 0, stream>>>(p);
-  return launch_status("launch of the combine gradient kernel");
+}
+
+template <class T, int VN>
+int launch_combine(gmm_ctx *h, gmm::CombineParams &p, bool grad, cudaStream_t stream) {
+  const long long nvec = p.row_bytes / static_cast<long long>(sizeof(T) * VN);
+  if (grad) {
+    if (p.top_k == 1) launch_grad<T, VN, 1, 4>(h, p, nvec, stream);
+    else if (p.top_k == 2) launch_grad<T, VN, 2, 2>(h, p, nvec, stream);
+    else launch_grad<T, VN, 4, 1>(h, p, nvec, stream);
+    return launch_status("launch of the combine gradient kernel");
+  }
+  constexpr int kUnits = 2;
+  const long long pieces = (nvec + 32 * kUnits - 1) / (32 * kUnits);
+  const long long ctas = (p.num_tokens * pieces + gmm::kCombineWarps - 1) / gmm::kCombineWarps;
+  if (ctas > (1ll << 28)) return GMM_ERR_UNSUPPORTED;   // warps are numbered in 32 bits
+  gmm::gmm_combine_kernel<T, VN, kUnits><<<static_cast<unsigned>(ctas), 32 * gmm::kCombineWarps, 0, stream>>>(p);
+  return launch_status("launch of the combine kernel");
 }
 
 // 16-byte vectors where every row starts on a 16-byte boundary, else single elements.
@@ -543,21 +564,23 @@ int run_combine(gmm_ctx *h, gmm::CombineParams &p, int dtype, bool vec, bool gra
   }
 }
 
+template <class T, bool kMx, int kAlign>
+void launch_quant(const gmm::QuantParams &p, bool quantise, unsigned grid, cudaStream_t stream) {
+  if (quantise) gmm::gmm_quantize_fp4_kernel<T, kMx, kAlign><<<grid, gmm::kQuantThreads, 0, stream>>>(p);
+  else gmm::gmm_dequantize_fp4_kernel<T, kMx, kAlign><<<grid, gmm::kQuantThreads, 0, stream>>>(p);
+}
+
 template <class T, bool kMx>
-void launch_quant(const gmm::QuantParams &p, bool quantise, bool vec, unsigned grid, cudaStream_t stream) {
-  if (quantise) {
-    if (vec) gmm::gmm_quantize_fp4_kernel<T, kMx, true><<<grid, gmm::kQuantThreads, 0, stream>>>(p);
-    else gmm::gmm_quantize_fp4_kernel<T, kMx, false><<<grid, gmm::kQuantThreads, 0, stream>>>(p);
-  } else {
-    if (vec) gmm::gmm_dequantize_fp4_kernel<T, kMx, true><<<grid, gmm::kQuantThreads, 0, stream>>>(p);
-    else gmm::gmm_dequantize_fp4_kernel<T, kMx, false><<<grid, gmm::kQuantThreads, 0, stream>>>(p);
-  }
+void launch_quant_align(const gmm::QuantParams &p, bool quantise, int align, unsigned grid, cudaStream_t stream) {
+  if (align == 32) launch_quant<T, kMx, 32>(p, quantise, grid, stream);
+  else if (align == 16) launch_quant<T, kMx, 16>(p, quantise, grid, stream);
+  else launch_quant<T, kMx, 1>(p, quantise, grid, stream);
 }
 
 template <class T>
-void launch_quant_fmt(const gmm::QuantParams &p, int format, bool quantise, bool vec, unsigned grid, cudaStream_t stream) {
-  if (format == GMM_FP4_MX) launch_quant<T, true>(p, quantise, vec, grid, stream);
-  else launch_quant<T, false>(p, quantise, vec, grid, stream);
+void launch_quant_fmt(const gmm::QuantParams &p, int format, bool quantise, int align, unsigned grid, cudaStream_t stream) {
+  if (format == GMM_FP4_MX) launch_quant_align<T, true>(p, quantise, align, grid, stream);
+  else launch_quant_align<T, false>(p, quantise, align, grid, stream);
 }
 
 int fp4_block(int format) { return format == GMM_FP4_MX ? 32 : 16; }
@@ -579,12 +602,13 @@ int run_quant(gmm_ctx *h, gmm::QuantParams &p, int dtype, int format, long long 
   const long long threads = static_cast<long long>(p.rows) * (p.K / 16);
   const long long grid = (threads + gmm::kQuantThreads - 1) / gmm::kQuantThreads;
   if (grid > 0x7fffffffll) return GMM_ERR_UNSUPPORTED;
-  const bool vec = aligned16(p.x) && p.x_pitch % 16 == 0;
+  const unsigned long long at = reinterpret_cast<uintptr_t>(p.x) | static_cast<unsigned long long>(p.x_pitch);
+  const int align = at % 32 == 0 ? 32 : (at % 16 == 0 ? 16 : 1);
   DeviceGuard guard(h->device);
   switch (dtype) {
-    case GMM_DTYPE_BF16: launch_quant_fmt<__nv_bfloat16>(p, format, quantise, vec, static_cast<unsigned>(grid), stream); break;
-    case GMM_DTYPE_FP16: launch_quant_fmt<__half>(p, format, quantise, vec, static_cast<unsigned>(grid), stream); break;
-    default: launch_quant_fmt<float>(p, format, quantise, vec, static_cast<unsigned>(grid), stream); break;
+    case GMM_DTYPE_BF16: launch_quant_fmt<__nv_bfloat16>(p, format, quantise, align, static_cast<unsigned>(grid), stream); break;
+    case GMM_DTYPE_FP16: launch_quant_fmt<__half>(p, format, quantise, align, static_cast<unsigned>(grid), stream); break;
+    default: launch_quant_fmt<float>(p, format, quantise, align, static_cast<unsigned>(grid), stream); break;
   }
   return launch_status(quantise ? "launch of the quantisation kernel" : "launch of the dequantisation kernel");
 }

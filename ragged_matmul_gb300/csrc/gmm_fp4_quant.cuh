@@ -58,11 +58,16 @@ struct QuantRaw<__half> { uint32_t w[8]; };
 template <>
 struct QuantRaw<__nv_bfloat16> { uint32_t w[8]; };
 
-template <class T, bool kVec>
+// kAlign: what the address is a multiple of, 32 (whole sectors by one load), 16, or the
+// element's size.
+template <class T, int kAlign>
 __device__ __forceinline__ QuantRaw<T> quant_load(const uint8_t *p) {
   QuantRaw<T> r;
   constexpr int kWords = sizeof(r.w) / 4;
-  if constexpr (kVec) {
+  if constexpr (kAlign == 32) {
+#pragma unroll
+    for (int i = 0; i < kWords / 8; ++i) ld_global_nc_v8(p + 32 * i, *reinterpret_cast<uint32_t(*)[8]>(&r.w[8 * i]));
+  } else if constexpr (kAlign == 16) {
 #pragma unroll
     for (int i = 0; i < kWords / 4; ++i) {
       const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
@@ -155,7 +160,7 @@ __device__ __forceinline__ float e8m0_to_float(uint32_t code) {
 }
 
 // A thread per 16 elements; the two threads of an mxfp4 block exchange their maxima.
-template <class T, bool kMx, bool kVec>
+template <class T, bool kMx, int kAlign>
 __global__ void __launch_bounds__(kQuantThreads) gmm_quantize_fp4_kernel(const __grid_constant__ QuantParams p) {
   const uint32_t per_row = static_cast<uint32_t>(p.K) / 16u;   // K is a multiple of 32: even
   const unsigned long long idx = static_cast<unsigned long long>(blockIdx.x) * kQuantThreads + threadIdx.x;
@@ -174,7 +179,7 @@ __global__ void __launch_bounds__(kQuantThreads) gmm_quantize_fp4_kernel(const _
   }
   const bool live = in && src >= 0;   // both threads of a block agree: they share the row
   QuantRaw<T> raw{};
-  if (live) raw = quant_load<T, kVec>(p.x + src * p.x_pitch + static_cast<long long>(blk) * 16 * sizeof(T));
+  if (live) raw = quant_load<T, kAlign>(p.x + src * p.x_pitch + static_cast<long long>(blk) * 16 * sizeof(T));
   uint32_t amax = quant_amax<T>(raw);
   if (kMx) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   if (!live) return;
@@ -231,7 +236,7 @@ __device__ __forceinline__ float2 e2m1x2_to_float2(uint32_t byte) {
 }
 
 // y = q * (s * g), the product of the scales rounded to fp32 once, then once to T.
-template <class T, bool kMx, bool kVec>
+template <class T, bool kMx, int kAlign>
 __global__ void __launch_bounds__(kQuantThreads) gmm_dequantize_fp4_kernel(const __grid_constant__ QuantParams p) {
   const uint32_t per_row = static_cast<uint32_t>(p.K) / 16u;
   const unsigned long long idx = static_cast<unsigned long long>(blockIdx.x) * kQuantThreads + threadIdx.x;
@@ -243,7 +248,7 @@ __global__ void __launch_bounds__(kQuantThreads) gmm_dequantize_fp4_kernel(const
   float d;
   if constexpr (kMx) d = e8m0_to_float(code);
   else d = e4m3_to_float(code) * (p.global_scale != nullptr ? __ldg(p.global_scale) : 1.0f);
-  T y[16];
+  alignas(32) T y[16];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float2 f = e2m1x2_to_float2(((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 0xffu);
@@ -251,7 +256,11 @@ __global__ void __launch_bounds__(kQuantThreads) gmm_dequantize_fp4_kernel(const
     y[2 * i + 1] = route_from_float<T>(f.y * d);
   }
   T *out = reinterpret_cast<T *>(const_cast<uint8_t *>(p.x) + row * p.x_pitch) + static_cast<size_t>(blk) * 16;
-  if constexpr (kVec) {
+  if constexpr (kAlign == 32) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+      st_global_v8(reinterpret_cast<uint8_t *>(out) + 32 * i, reinterpret_cast<const uint32_t *>(y) + 8 * i);
+  } else if constexpr (kAlign == 16) {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(T)); ++i)
       reinterpret_cast<uint4 *>(out)[i] = reinterpret_cast<const uint4 *>(y)[i];

@@ -18,6 +18,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "gmm_kernel.cuh"
 
@@ -30,9 +31,11 @@ constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kRouteMaxTopK = 32;          // a token's slots are held one per lane
 constexpr int kRouteSmallSlots = 4096;     // up to here (and kRouteSmallExperts) one launch sorts and copies
 constexpr int kRouteSmallExperts = 1024;
+constexpr int kRouteSmallUnit = 1;         // vectors a lane and copy unit there: few bytes, spread over many SMs
 constexpr int kRouteMaxExperts = 4096;     // one group per expert: the grouped kernels' limit
 constexpr int kRouteMaxCounts = 32768;     // chunk counts (chunks x experts) in the workspace
 constexpr int kRouteMaxChunks = 152;
+constexpr long long kRoutePrefetch = 64 * 1024;   // bytes of its tokens that a CTA prefetches while the count runs
 constexpr int kRouteBatch = 64;            // tokens whose rows a CTA holds in shared memory at a time
 
 struct DispatchParams {
@@ -64,9 +67,11 @@ __device__ __forceinline__ uint32_t route_rank_share(const int32_t *ids, int beg
                                                      Emit emit) {
   const uint32_t lane = threadIdx.x & 31u;
   uint32_t flags = 0;
+  int e_next = begin + static_cast<int>(lane) < end ? __ldg(ids + begin + lane) : -1;   // one step ahead
   for (int s0 = begin; s0 < end; s0 += 32) {
     const int s = s0 + static_cast<int>(lane);
-    const int e = s < end ? __ldg(ids + s) : -1;
+    const int e = e_next;
+    e_next = s + 32 < end ? __ldg(ids + s + 32) : -1;
     const bool ok = e >= 0 && e < E;
     if (e >= E) flags = kStatusBadExpert;
     const uint32_t peers = __match_any_sync(0xffffffffu, ok ? e : -1);
@@ -118,13 +123,12 @@ template <>
 struct RouteVec<2> { using type = unsigned short; };
 
 // Copies of tokens [t0, t0 + n) to their rows; rows_s[i * top_k + j] is the row of slot j
-// of token t0 + i (-1: dropped).  A unit is up to 4 vectors a lane of one token: read once,
+// of token t0 + i (-1: dropped).  A unit is up to kU vectors a lane of one token: read once,
 // written to each of its rows.  Units go to the CTA's warps in turn, `part` of `parts` CTAs.
-template <int VB>
+template <int VB, int kU>
 __device__ __forceinline__ void route_copy(const DispatchParams &p, const int *rows_s, int t0, int n, int part,
                                            int parts) {
   using V = typename RouteVec<VB>::type;
-  constexpr int kU = 4;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nvec = static_cast<int>(p.row_bytes / VB);
   const int pieces = (nvec + 32 * kU - 1) / (32 * kU);
@@ -198,7 +202,7 @@ __global__ void __launch_bounds__(kRouteThreads) gmm_dispatch_small_kernel(const
   }
   if (p.tokens == nullptr) return;
   __syncthreads();
-  route_copy<VB>(p, row_s, 0, p.num_tokens, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
+  route_copy<VB, kRouteSmallUnit>(p, row_s, 0, p.num_tokens, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
 }
 
 // Many slots, first launch: CTA c counts the experts of its chunk of tokens and leaves every
@@ -206,6 +210,7 @@ __global__ void __launch_bounds__(kRouteThreads) gmm_dispatch_small_kernel(const
 __global__ void __launch_bounds__(kRouteThreads) gmm_dispatch_count_kernel(const __grid_constant__ DispatchParams p,
                                                                            int warps) {
   extern __shared__ uint32_t route_smem[];
+  grid_launch_dependents();   // the copy's CTAs start, and wait where they need these results
   const int tid = threadIdx.x, warp = tid >> 5;
   const int E = p.num_experts;
   const long long t0 = static_cast<long long>(blockIdx.x) * p.chunk_tokens;
@@ -238,7 +243,7 @@ __global__ void __launch_bounds__(kRouteThreads) gmm_dispatch_count_kernel(const
   }
 }
 
-// Second launch: a CTA sums the chunk counts (at most 128 KB, from L2) into the first row of
+// Second launch, started while the first one runs: a CTA sums the chunk counts (at most 128 KB, from L2) into the first row of
 // every expert's slots in its chunk, then places and copies its tokens, kRouteBatch at a time.
 template <int VB>
 __global__ void __launch_bounds__(kRouteThreads) gmm_dispatch_place_kernel(const __grid_constant__ DispatchParams p) {
@@ -250,11 +255,23 @@ __global__ void __launch_bounds__(kRouteThreads) gmm_dispatch_place_kernel(const
   uint32_t *bef = off + E + 1;                               // [E]: counts of the chunks before this one
   int *row_s = reinterpret_cast<int *>(bef + E);             // [kRouteBatch * top_k]
   const int chunk = static_cast<int>(blockIdx.x) / p.subs, sub = static_cast<int>(blockIdx.x) % p.subs;
+  const long long c0 = static_cast<long long>(chunk) * p.chunk_tokens;
+  const int per = (p.chunk_tokens + p.subs - 1) / p.subs;
+  const int lim = static_cast<int>(min(c0 + p.chunk_tokens, static_cast<long long>(p.num_tokens)));
+  const int t_begin = static_cast<int>(min(c0 + static_cast<long long>(sub) * per, static_cast<long long>(lim)));
+  const int t_end = min(lim, t_begin + per);
+  // Ahead of the count's results: the first of this CTA's tokens into L2.
+  if (p.tokens != nullptr && t_begin < t_end) {
+    const long long bytes = min((t_end - t_begin - 1) * p.token_pitch + p.row_bytes, kRoutePrefetch);
+    const uint8_t *at = p.tokens + t_begin * p.token_pitch;
+    for (long long i = tid * 128ll; i < bytes; i += kRouteThreads * 128ll) prefetch_l2(at + i);
+  }
   for (int e = tid; e < E; e += kRouteThreads) {
     off[e] = 0;
     bef[e] = 0;
   }
   __syncthreads();
+  grid_wait_dependency();
   // Threads in groups of E (one expert a thread) take the chunks in turn.
   const int groups = max(1, kRouteThreads / E);
   const int g = E <= kRouteThreads ? tid / E : 0;
@@ -263,7 +280,7 @@ __global__ void __launch_bounds__(kRouteThreads) gmm_dispatch_place_kernel(const
       uint32_t total = 0, before = 0;
 #pragma unroll 4
       for (int c = g; c < p.chunks; c += groups) {
-        const uint32_t n = __ldg(p.counts + static_cast<size_t>(c) * E + e);
+        const uint32_t n = p.counts[static_cast<size_t>(c) * E + e];
         total += n;
         before += c < chunk ? n : 0u;
       }
@@ -278,11 +295,6 @@ __global__ void __launch_bounds__(kRouteThreads) gmm_dispatch_place_kernel(const
   for (int r = static_cast<int>(off[E]) + static_cast<int>(blockIdx.x) * kRouteThreads + tid; r < S;
        r += static_cast<int>(gridDim.x) * kRouteThreads)
     p.row_slots[r] = -1;
-  const long long c0 = static_cast<long long>(chunk) * p.chunk_tokens;
-  const int per = (p.chunk_tokens + p.subs - 1) / p.subs;
-  const int lim = static_cast<int>(min(c0 + p.chunk_tokens, static_cast<long long>(p.num_tokens)));
-  const int t_begin = static_cast<int>(min(c0 + static_cast<long long>(sub) * per, static_cast<long long>(lim)));
-  const int t_end = min(lim, t_begin + per);
   for (int t = t_begin; t < t_end; t += kRouteBatch) {
     const int n = min(kRouteBatch, t_end - t);
     __syncthreads();   // the previous batch's copies have read row_s
@@ -298,7 +310,7 @@ __global__ void __launch_bounds__(kRouteThreads) gmm_dispatch_place_kernel(const
       row_s[i] = row;
     }
     __syncthreads();
-    if (p.tokens != nullptr) route_copy<VB>(p, row_s, t, n, 0, 1);
+    if (p.tokens != nullptr) route_copy<VB, 4>(p, row_s, t, n, 0, 1);
   }
 }
 
@@ -321,15 +333,6 @@ struct CombineParams {
   uint32_t *status;
 };
 
-// VN consecutive elements of type T in one load or store.
-template <class T>
-__device__ __forceinline__ float route_to_float(T x);
-template <>
-__device__ __forceinline__ float route_to_float(float x) { return x; }
-template <>
-__device__ __forceinline__ float route_to_float(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float route_to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 template <class T>
 __device__ __forceinline__ T route_from_float(float x);
 template <>
@@ -339,29 +342,88 @@ __device__ __forceinline__ __half route_from_float(float x) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 route_from_float(float x) { return __float2bfloat16_rn(x); }
 
+// VN consecutive elements of type T as loaded: 16 bytes, or one element.
 template <class T, int VN>
 struct RoutePack {
-  alignas(sizeof(T) * VN) T v[VN];
+  static constexpr int kWords = sizeof(T) * VN / 4;
+  uint32_t w[kWords];
+};
+template <class T>
+struct RoutePack<T, 1> {
+  T x;
 };
 
 template <class T, int VN>
 __device__ __forceinline__ RoutePack<T, VN> route_load(const uint8_t *row, int i) {
-  if constexpr (sizeof(T) * VN == 16) {
+  RoutePack<T, VN> r;
+  if constexpr (VN > 1) {
     const uint4 x = __ldg(reinterpret_cast<const uint4 *>(row) + i);
-    return *reinterpret_cast<const RoutePack<T, VN> *>(&x);
+    r.w[0] = x.x;
+    r.w[1] = x.y;
+    r.w[2] = x.z;
+    r.w[3] = x.w;
   } else {
-    RoutePack<T, VN> r;
-    r.v[0] = reinterpret_cast<const T *>(row)[i];
-    return r;
+    r.x = reinterpret_cast<const T *>(row)[i];
+  }
+  return r;
+}
+
+// The pack's values in fp32.
+template <class T, int VN>
+__device__ __forceinline__ void route_unpack(const RoutePack<T, VN> &p, float (&v)[VN]) {
+  if constexpr (VN == 1) {
+    if constexpr (std::is_same_v<T, float>) v[0] = p.x;
+    else if constexpr (std::is_same_v<T, __half>) v[0] = __half2float(p.x);
+    else v[0] = __bfloat162float(p.x);
+  } else if constexpr (std::is_same_v<T, float>) {
+#pragma unroll
+    for (int i = 0; i < VN; ++i) v[i] = __uint_as_float(p.w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VN / 2; ++i) {
+      if constexpr (std::is_same_v<T, __half>) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&p.w[i]));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+      } else {
+        v[2 * i] = __uint_as_float(p.w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(p.w[i] & 0xffff0000u);
+      }
+    }
   }
 }
 
+// VN fp32 values rounded to T and stored.
 template <class T, int VN>
-__device__ __forceinline__ void route_store(uint8_t *row, int i, const RoutePack<T, VN> &x) {
-  if constexpr (sizeof(T) * VN == 16)
-    reinterpret_cast<uint4 *>(row)[i] = *reinterpret_cast<const uint4 *>(&x);
-  else
-    reinterpret_cast<T *>(row)[i] = x.v[0];
+__device__ __forceinline__ void route_store(uint8_t *row, int i, const float (&v)[VN]) {
+  if constexpr (VN == 1) {
+    reinterpret_cast<T *>(row)[i] = route_from_float<T>(v[0]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (std::is_same_v<T, float>) {
+        w[j] = __float_as_uint(v[j]);
+      } else if constexpr (std::is_same_v<T, __half>) {
+        const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t *>(&h);
+      } else {
+        w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+      }
+    }
+    reinterpret_cast<uint4 *>(row)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// acc += a * x, paired where there are pairs (each value rounded as by fmaf).
+template <int VN>
+__device__ __forceinline__ void route_fma(float (&acc)[VN], float a, const float (&x)[VN]) {
+  if constexpr (VN == 1) {
+    acc[0] = fmaf(a, x[0], acc[0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VN; i += 2) fma_f32x2(acc[i], acc[i + 1], a, x[i], x[i + 1]);
+  }
 }
 
 // This lane's slot of token t: its row (-1: none) and weight.
@@ -383,54 +445,57 @@ __device__ __forceinline__ int route_slot(const CombineParams &p, int t, int lan
 constexpr int kCombineWarps = 8;
 constexpr int kCombineBatch = 8;   // rows of a token whose loads are in flight together
 
-// A warp per (token, 32 vectors).
-template <class T, int VN>
-__global__ void __launch_bounds__(32 * kCombineWarps) gmm_combine_kernel(const __grid_constant__ CombineParams p) {
+// Bound by the rows' bytes.  A warp per (token, 32 kUnits vectors): its slots are read once, a
+// lane each, and the loads of kCombineBatch rows are in flight together; at 64 registers a
+// thread half of an SM's warps are resident, which keeps enough of them in flight (with 100
+// registers and a quarter, 32768 rows of 8 KB to 4096 tokens took 73 us).
+template <class T, int VN, int kUnits>
+__global__ void __launch_bounds__(32 * kCombineWarps, 4) gmm_combine_kernel(const __grid_constant__ CombineParams p) {
   const int lane = threadIdx.x & 31;
   const int nvec = static_cast<int>(p.row_bytes / (sizeof(T) * VN));
-  const int pieces = (nvec + 31) / 32;
-  const long long u = static_cast<long long>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5);
-  if (u >= static_cast<long long>(p.num_tokens) * pieces) return;
-  const int t = static_cast<int>(u / pieces);
-  const int v = static_cast<int>(u - static_cast<long long>(t) * pieces) * 32 + lane;
+  const int pieces = (nvec + 32 * kUnits - 1) / (32 * kUnits);
+  const uint32_t u = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
+  const uint32_t t = u / static_cast<uint32_t>(pieces);
+  if (t >= static_cast<uint32_t>(p.num_tokens)) return;
+  const int v0 = static_cast<int>(u - t * pieces) * 32 * kUnits + lane;
   float w;
-  const int r = route_slot(p, t, lane, &w);
-  float acc[VN];
+  const int r = route_slot(p, static_cast<int>(t), lane, &w);
 #pragma unroll
-  for (int i = 0; i < VN; ++i) acc[i] = 0.0f;
-  for (int j0 = 0; j0 < p.top_k; j0 += kCombineBatch) {
-    RoutePack<T, VN> x[kCombineBatch];
-    float wj[kCombineBatch];
-    bool has[kCombineBatch];
+  for (int q = 0; q < kUnits; ++q) {
+    const int v = v0 + 32 * q;
+    float acc[VN];
 #pragma unroll
-    for (int q = 0; q < kCombineBatch; ++q) {
-      const int rj = __shfl_sync(0xffffffffu, r, (j0 + q) & 31);
-      wj[q] = __shfl_sync(0xffffffffu, w, (j0 + q) & 31);
-      has[q] = j0 + q < p.top_k && rj >= 0 && v < nvec;
-      if (has[q]) x[q] = route_load<T, VN>(p.rows + rj * p.row_bytes, v);
-    }
+    for (int i = 0; i < VN; ++i) acc[i] = 0.0f;
+    for (int j0 = 0; j0 < p.top_k; j0 += kCombineBatch) {
+      RoutePack<T, VN> x[kCombineBatch];
 #pragma unroll
-    for (int q = 0; q < kCombineBatch; ++q)
-      if (has[q]) {
-#pragma unroll
-        for (int i = 0; i < VN; ++i) acc[i] = fmaf(wj[q], route_to_float<T>(x[q].v[i]), acc[i]);
+      for (int j = 0; j < kCombineBatch; ++j) {
+        const int rj = __shfl_sync(0xffffffffu, r, (j0 + j) & 31);   // (a lane past top_k holds -1)
+        if (rj >= 0 && j0 + j < p.top_k && v < nvec) x[j] = route_load<T, VN>(p.rows + rj * p.row_bytes, v);
       }
-  }
-  if (v < nvec) {
-    RoutePack<T, VN> y;
 #pragma unroll
-    for (int i = 0; i < VN; ++i) y.v[i] = route_from_float<T>(acc[i]);
-    route_store<T, VN>(p.out + t * p.out_pitch, v, y);
+      for (int j = 0; j < kCombineBatch; ++j) {
+        const int rj = __shfl_sync(0xffffffffu, r, (j0 + j) & 31);
+        const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
+        if (rj >= 0 && j0 + j < p.top_k && v < nvec) {
+          float y[VN];
+          route_unpack<T, VN>(x[j], y);
+          route_fma<VN>(acc, wj, y);
+        }
+      }
+    }
+    if (v < nvec) route_store<T, VN>(p.out + t * p.out_pitch, v, acc);
   }
 }
 
-// warps_per_token warps per token (a power of two up to kCombineWarps): they take the
-// token's 32-vector pieces in turn, four rows at a time, and join their dot products
-// through shared memory in warp order.
-template <class T, int VN>
-__global__ void __launch_bounds__(32 * kCombineWarps)
+// Bound by the bytes of d_out, rows and d_rows.  warps_per_token warps per token (a power of two
+// up to kCombineWarps, more than one where there are few tokens): they take the token's
+// 32 kUnits-vector pieces in turn, kRows rows at a time, and join their dot products through
+// shared memory in warp order.  The loads of a piece's kUnits (kRows + 1) vectors are in flight
+// together.
+template <class T, int VN, int kRows, int kUnits>
+__global__ void __launch_bounds__(32 * kCombineWarps, 4)
     gmm_combine_grad_kernel(const __grid_constant__ CombineParams p) {
-  constexpr int kRows = 4;
   __shared__ float part[kCombineWarps][kRouteMaxTopK];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nvec = static_cast<int>(p.row_bytes / (sizeof(T) * VN));
@@ -446,42 +511,51 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
     float wj[kRows], dot[kRows];
     bool any = false;
 #pragma unroll
-    for (int q = 0; q < kRows; ++q) {
-      rj[q] = __shfl_sync(0xffffffffu, r, (j0 + q) & 31);
-      wj[q] = __shfl_sync(0xffffffffu, w, (j0 + q) & 31);
-      if (j0 + q >= p.top_k) rj[q] = -1;
-      any = any || rj[q] >= 0;
-      dot[q] = 0.0f;
+    for (int j = 0; j < kRows; ++j) {
+      rj[j] = __shfl_sync(0xffffffffu, r, (j0 + j) & 31);
+      wj[j] = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
+      if (j0 + j >= p.top_k) rj[j] = -1;
+      any = any || rj[j] >= 0;
+      dot[j] = 0.0f;
     }
     if (any) {
-#pragma unroll 2
-      for (int v = sub * 32 + lane; v < nvec; v += wpt * 32) {
-        const RoutePack<T, VN> g = route_load<T, VN>(g_row, v);
-        RoutePack<T, VN> x[kRows];
-        if (p.d_weights != nullptr) {
+      for (int v0 = sub * 32 * kUnits + lane; v0 < nvec; v0 += wpt * 32 * kUnits) {
+        RoutePack<T, VN> g[kUnits], x[kUnits][kRows];
 #pragma unroll
-          for (int q = 0; q < kRows; ++q)
-            if (rj[q] >= 0) x[q] = route_load<T, VN>(p.rows + rj[q] * p.row_bytes, v);
-        }
+        for (int q = 0; q < kUnits; ++q)
+          if (v0 + 32 * q < nvec) {
+            g[q] = route_load<T, VN>(g_row, v0 + 32 * q);
 #pragma unroll
-        for (int q = 0; q < kRows; ++q)
-          if (rj[q] >= 0) {
-            RoutePack<T, VN> y;
+            for (int j = 0; j < kRows; ++j)
+              if (rj[j] >= 0 && p.d_weights != nullptr)
+                x[q][j] = route_load<T, VN>(p.rows + rj[j] * p.row_bytes, v0 + 32 * q);
+          }
 #pragma unroll
-            for (int i = 0; i < VN; ++i) {
-              const float gi = route_to_float<T>(g.v[i]);
-              if (p.d_weights != nullptr) dot[q] = fmaf(gi, route_to_float<T>(x[q].v[i]), dot[q]);
-              y.v[i] = route_from_float<T>(wj[q] * gi);
-            }
-            route_store<T, VN>(p.d_rows + rj[q] * p.row_bytes, v, y);
+        for (int q = 0; q < kUnits; ++q)
+          if (v0 + 32 * q < nvec) {
+            float gv[VN];
+            route_unpack<T, VN>(g[q], gv);
+#pragma unroll
+            for (int j = 0; j < kRows; ++j)
+              if (rj[j] >= 0) {
+                float y[VN];
+                if (p.d_weights != nullptr) {
+                  route_unpack<T, VN>(x[q][j], y);
+#pragma unroll
+                  for (int i = 0; i < VN; ++i) dot[j] = fmaf(gv[i], y[i], dot[j]);
+                }
+#pragma unroll
+                for (int i = 0; i < VN; ++i) y[i] = wj[j] * gv[i];
+                route_store<T, VN>(p.d_rows + rj[j] * p.row_bytes, v0 + 32 * q, y);
+              }
           }
       }
     }
 #pragma unroll
-    for (int q = 0; q < kRows; ++q) {
+    for (int j = 0; j < kRows; ++j) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) dot[q] += __shfl_xor_sync(0xffffffffu, dot[q], o);
-      if (lane == 0 && j0 + q < p.top_k) part[warp][j0 + q] = dot[q];
+      for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
+      if (lane == 0 && j0 + j < p.top_k) part[warp][j0 + j] = dot[j];
     }
   }
   if (p.d_weights == nullptr) return;

@@ -116,6 +116,20 @@ __device__ __forceinline__ void ld_global_nc_v8(const void *ptr, uint32_t (&x)[8
                : "l"(ptr));
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *ptr) { asm volatile("prefetch.global.L2 [%0];" ::"l"(ptr)); }
+
+// Programmatic dependent launch: let the next launch of the stream start, and wait until the
+// launch before it has finished and its writes are visible.
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait_dependency() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// 32-byte store (32-byte aligned).
+__device__ __forceinline__ void st_global_v8(void *ptr, const uint32_t *x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(ptr), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+               "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
 // ----------------------------------------------------------------- TMA
 
 // L2 eviction-priority policies for TMA loads (.L2::cache_hint operands).
