@@ -600,7 +600,8 @@ int run_quant(gmm_ctx *h, gmm::QuantParams &p, int dtype, int format, long long 
   p.scale_pitch = fp4_scale_pitch(p.K, format);
   p.status = reinterpret_cast<uint32_t *>(h->ws);
   const long long threads = static_cast<long long>(p.rows) * (p.K / 16);
-  const long long grid = (threads + gmm::kQuantThreads - 1) / gmm::kQuantThreads;
+  const long long per_cta = gmm::kQuantThreads * static_cast<long long>(quantise ? gmm::kQuantPer : gmm::kDequantPer);
+  const long long grid = (threads + per_cta - 1) / per_cta;
   if (grid > 0x7fffffffll) return GMM_ERR_UNSUPPORTED;
   const unsigned long long at = reinterpret_cast<uintptr_t>(p.x) | static_cast<unsigned long long>(p.x_pitch);
   const int align = at % 32 == 0 ? 32 : (at % 16 == 0 ? 16 : 1);

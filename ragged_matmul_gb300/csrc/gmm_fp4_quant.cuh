@@ -31,6 +31,8 @@
 namespace gmm {
 
 constexpr int kQuantThreads = 256;
+constexpr int kQuantPer = 2;     // 16-element blocks a thread, quantisation
+constexpr int kDequantPer = 4;   // and its inverse
 constexpr uint32_t kE4m3Nan = 0x7Fu, kE8m0Nan = 0xFFu;
 
 struct QuantParams {
@@ -159,71 +161,97 @@ __device__ __forceinline__ float e8m0_to_float(uint32_t code) {
   return __uint_as_float(code == 0 ? 0x00400000u : (code == kE8m0Nan ? 0x7fffffffu : code << 23));
 }
 
-// A thread per 16 elements; the two threads of an mxfp4 block exchange their maxima.
+// Where 16-element block `idx` of the call lies, and whether there is one.
+struct QuantAt {
+  int row;        // row of packed and scales
+  int src;        // row of x (-1: none)
+  uint32_t blk;   // 16-element block within the row
+  bool live;
+};
+
+__device__ __forceinline__ QuantAt quant_at(const QuantParams &p, unsigned long long idx, uint32_t per_row) {
+  QuantAt a;
+  const unsigned long long row = idx / per_row;
+  const bool in = row < static_cast<unsigned long long>(p.rows);
+  a.row = in ? static_cast<int>(row) : 0;
+  a.blk = static_cast<uint32_t>(idx - row * per_row);
+  a.src = a.row;
+  if (in && p.row_slots != nullptr) {
+    const int s = __ldg(p.row_slots + a.row);
+    a.src = s < 0 ? -1 : s / p.top_k;
+    if (a.src >= p.src_rows) {
+      atomicOr(p.status, kStatusBadSlot);
+      a.src = -1;
+    }
+  }
+  a.live = in && a.src >= 0;
+  return a;
+}
+
+// Bound by the bytes of x and the codes.  A thread takes kQuantPer blocks of 16 elements,
+// kQuantThreads apart, with their loads in flight together (one left 49 KB of an SM's loads in
+// flight, at the limit of the latency); the two threads of an mxfp4 block exchange their maxima.
 template <class T, bool kMx, int kAlign>
 __global__ void __launch_bounds__(kQuantThreads) gmm_quantize_fp4_kernel(const __grid_constant__ QuantParams p) {
   const uint32_t per_row = static_cast<uint32_t>(p.K) / 16u;   // K is a multiple of 32: even
-  const unsigned long long idx = static_cast<unsigned long long>(blockIdx.x) * kQuantThreads + threadIdx.x;
-  const unsigned long long row64 = idx / per_row;
-  const bool in = row64 < static_cast<unsigned long long>(p.rows);
-  const int row = in ? static_cast<int>(row64) : 0;
-  const uint32_t blk = static_cast<uint32_t>(idx - row64 * per_row);
-  int src = row;
-  if (in && p.row_slots != nullptr) {
-    const int s = __ldg(p.row_slots + row);
-    src = s < 0 ? -1 : s / p.top_k;
-    if (src >= p.src_rows) {
-      atomicOr(p.status, kStatusBadSlot);
-      src = -1;
-    }
+  const unsigned long long idx0 = static_cast<unsigned long long>(blockIdx.x) * (kQuantThreads * kQuantPer) + threadIdx.x;
+  QuantAt at[kQuantPer];
+  QuantRaw<T> raw[kQuantPer];
+#pragma unroll
+  for (int u = 0; u < kQuantPer; ++u) {   // both threads of a block agree on it: they share the row
+    at[u] = quant_at(p, idx0 + static_cast<unsigned long long>(u) * kQuantThreads, per_row);
+    raw[u] = QuantRaw<T>{};
+    if (at[u].live)
+      raw[u] = quant_load<T, kAlign>(p.x + at[u].src * p.x_pitch + static_cast<long long>(at[u].blk) * 16 * sizeof(T));
   }
-  const bool live = in && src >= 0;   // both threads of a block agree: they share the row
-  QuantRaw<T> raw{};
-  if (live) raw = quant_load<T, kAlign>(p.x + src * p.x_pitch + static_cast<long long>(blk) * 16 * sizeof(T));
-  uint32_t amax = quant_amax<T>(raw);
-  if (kMx) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  if (!live) return;
-  float v[16];
-  quant_values<T>(raw, v);
-  uint32_t code;
-  if (amax >= 0x7f800000u) {
-    code = kMx ? kE8m0Nan : kE4m3Nan;
+  const float g = !kMx && p.global_scale != nullptr ? __ldg(p.global_scale) : 1.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-  } else if constexpr (kMx) {
-    // floor(log2 amax) is the exponent field less 127; a subnormal's field is 0.
-    const uint32_t field = amax >> 23;
-    code = field > 2u ? field - 2u : 0u;
-    // 1 / d is a power of two too, and x / d is x with another exponent.
-    const float inv = __uint_as_float((254u - code) << 23);   // code is at most 252
+  for (int u = 0; u < kQuantPer; ++u) {
+    const uint32_t blk = at[u].blk;
+    uint32_t amax = quant_amax<T>(raw[u]);
+    if (kMx) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    if (!at[u].live) continue;
+    float v[16];
+    quant_values<T>(raw[u], v);
+    uint32_t code;
+    if (amax >= 0x7f800000u) {
+      code = kMx ? kE8m0Nan : kE4m3Nan;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] *= inv;
-  } else {
-    const float g = p.global_scale != nullptr ? __ldg(p.global_scale) : 1.0f;
-    code = float_to_e4m3(__fdiv_rn(__uint_as_float(amax), 6.0f * g));
-    const float d = e4m3_to_float(code) * g;
-    const float r = __frcp_rn(d);
-    if (d > 1e-30f && d < 1e30f && __uint_as_float(amax) * r < 1e30f) {
+      for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+    } else if constexpr (kMx) {
+      // floor(log2 amax) is the exponent field less 127; a subnormal's field is 0.
+      const uint32_t field = amax >> 23;
+      code = field > 2u ? field - 2u : 0u;
+      // 1 / d is a power of two too, and x / d is x with another exponent.
+      const float inv = __uint_as_float((254u - code) << 23);   // code is at most 252
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float y = v[i] * r;
-        v[i] = fmaf(fmaf(y, d, -v[i]), -r, y);   // in these signs a -0 stays -0
-      }
+      for (int i = 0; i < 16; ++i) v[i] *= inv;
     } else {
+      code = float_to_e4m3(__fdiv_rn(__uint_as_float(amax), 6.0f * g));
+      const float d = e4m3_to_float(code) * g;
+      const float r = __frcp_rn(d);
+      if (d > 1e-30f && d < 1e30f && __uint_as_float(amax) * r < 1e30f) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = d == 0.0f ? 0.0f : __fdiv_rn(v[i], d);
+        for (int i = 0; i < 16; ++i) {
+          const float y = v[i] * r;
+          v[i] = fmaf(fmaf(y, d, -v[i]), -r, y);   // in these signs a -0 stays -0
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = d == 0.0f ? 0.0f : __fdiv_rn(v[i], d);
+      }
     }
+    const uint2 w = make_uint2(pack_e2m1x8(v), pack_e2m1x8(v + 8));
+    reinterpret_cast<uint2 *>(p.packed + static_cast<size_t>(at[u].row) * (p.K / 2))[blk] = w;
+    uint8_t *srow = p.scales + static_cast<size_t>(at[u].row) * p.scale_pitch;
+    if (kMx) {
+      if ((blk & 1u) == 0) srow[blk >> 1] = static_cast<uint8_t>(code);
+    } else {
+      srow[blk] = static_cast<uint8_t>(code);
+    }
+    if (blk == per_row - 1)   // the row's padding
+      for (int i = static_cast<int>(kMx ? per_row / 2 : per_row); i < p.scale_pitch; ++i) srow[i] = 0;
   }
-  const uint2 w = make_uint2(pack_e2m1x8(v), pack_e2m1x8(v + 8));
-  reinterpret_cast<uint2 *>(p.packed + static_cast<size_t>(row) * (p.K / 2))[blk] = w;
-  uint8_t *srow = p.scales + static_cast<size_t>(row) * p.scale_pitch;
-  if (kMx) {
-    if ((blk & 1u) == 0) srow[blk >> 1] = static_cast<uint8_t>(code);
-  } else {
-    srow[blk] = static_cast<uint8_t>(code);
-  }
-  if (blk == per_row - 1)   // the row's padding
-    for (int i = static_cast<int>(kMx ? per_row / 2 : per_row); i < p.scale_pitch; ++i) srow[i] = 0;
 }
 
 // One byte (two e2m1 codes) to two fp32 values.
@@ -235,38 +263,51 @@ __device__ __forceinline__ float2 e2m1x2_to_float2(uint32_t byte) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
-// y = q * (s * g), the product of the scales rounded to fp32 once, then once to T.
+// y = q * (s * g), the product of the scales rounded to fp32 once, then once to T.  Bound by
+// the bytes of y; a thread takes kDequantPer blocks of 16 elements.
 template <class T, bool kMx, int kAlign>
 __global__ void __launch_bounds__(kQuantThreads) gmm_dequantize_fp4_kernel(const __grid_constant__ QuantParams p) {
   const uint32_t per_row = static_cast<uint32_t>(p.K) / 16u;
-  const unsigned long long idx = static_cast<unsigned long long>(blockIdx.x) * kQuantThreads + threadIdx.x;
-  const unsigned long long row = idx / per_row;
-  if (row >= static_cast<unsigned long long>(p.rows)) return;
-  const uint32_t blk = static_cast<uint32_t>(idx - row * per_row);
-  const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p.packed + row * (p.K / 2)) + blk);
-  const uint32_t code = __ldg(p.scales + row * p.scale_pitch + (kMx ? blk >> 1 : blk));
-  float d;
-  if constexpr (kMx) d = e8m0_to_float(code);
-  else d = e4m3_to_float(code) * (p.global_scale != nullptr ? __ldg(p.global_scale) : 1.0f);
-  alignas(32) T y[16];
+  const unsigned long long idx0 = static_cast<unsigned long long>(blockIdx.x) * (kQuantThreads * kDequantPer) + threadIdx.x;
+  const float g = !kMx && p.global_scale != nullptr ? __ldg(p.global_scale) : 1.0f;
+  uint2 w[kDequantPer];
+  uint32_t code[kDequantPer];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = e2m1x2_to_float2(((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 0xffu);
-    y[2 * i] = route_from_float<T>(f.x * d);
-    y[2 * i + 1] = route_from_float<T>(f.y * d);
+  for (int u = 0; u < kDequantPer; ++u) {
+    const unsigned long long idx = idx0 + static_cast<unsigned long long>(u) * kQuantThreads, row = idx / per_row;
+    if (row >= static_cast<unsigned long long>(p.rows)) continue;
+    const uint32_t blk = static_cast<uint32_t>(idx - row * per_row);
+    w[u] = __ldg(reinterpret_cast<const uint2 *>(p.packed + row * (p.K / 2)) + blk);
+    code[u] = __ldg(p.scales + row * p.scale_pitch + (kMx ? blk >> 1 : blk));
   }
-  T *out = reinterpret_cast<T *>(const_cast<uint8_t *>(p.x) + row * p.x_pitch) + static_cast<size_t>(blk) * 16;
-  if constexpr (kAlign == 32) {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-      st_global_v8(reinterpret_cast<uint8_t *>(out) + 32 * i, reinterpret_cast<const uint32_t *>(y) + 8 * i);
-  } else if constexpr (kAlign == 16) {
+  for (int u = 0; u < kDequantPer; ++u) {
+    const unsigned long long idx = idx0 + static_cast<unsigned long long>(u) * kQuantThreads, row = idx / per_row;
+    if (row >= static_cast<unsigned long long>(p.rows)) continue;
+    const uint32_t blk = static_cast<uint32_t>(idx - row * per_row);
+    float d;
+    if constexpr (kMx) d = e8m0_to_float(code[u]);
+    else d = e4m3_to_float(code[u]) * g;
+    alignas(32) T y[16];
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T)); ++i)
-      reinterpret_cast<uint4 *>(out)[i] = reinterpret_cast<const uint4 *>(y)[i];
-  } else {
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = e2m1x2_to_float2(((i < 4 ? w[u].x : w[u].y) >> (8 * (i & 3))) & 0xffu);
+      y[2 * i] = route_from_float<T>(f.x * d);
+      y[2 * i + 1] = route_from_float<T>(f.y * d);
+    }
+    T *out = reinterpret_cast<T *>(const_cast<uint8_t *>(p.x) + row * p.x_pitch) + static_cast<size_t>(blk) * 16;
+    if constexpr (kAlign == 32) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) out[i] = y[i];
+      for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+        st_global_v8(reinterpret_cast<uint8_t *>(out) + 32 * i, reinterpret_cast<const uint32_t *>(y) + 8 * i);
+    } else if constexpr (kAlign == 16) {
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(T)); ++i)
+        reinterpret_cast<uint4 *>(out)[i] = reinterpret_cast<const uint4 *>(y)[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) out[i] = y[i];
+    }
   }
 }
 
