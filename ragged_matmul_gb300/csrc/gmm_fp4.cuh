@@ -32,8 +32,8 @@
 //   warps 10..12  scales: the weight rows' block, and the tokens' two.
 //   warp 13       scheduler: decodes the CTA's tiles into a queue that every role reads.
 //
-// Tiles are the static share of each pair (tile t, t + pairs, ...).  Every wait is bounded as
-// in the grouped kernel.
+// Tiles are claimed by the pair as the grouped kernel's are (a static share where there are
+// few).  Every wait is bounded as in the grouped kernel.
 #pragma once
 
 #include <type_traits>
@@ -54,6 +54,8 @@ constexpr uint32_t kF4TBytes = kF4MaxTok / 2 * 128;         // a CTA's half of t
 constexpr uint32_t kF4Atom = 512;                           // one scale word of 128 rows
 constexpr uint32_t kF4AccCols = kF4MaxTok;
 constexpr uint32_t kF4ScaleCol = 2 * kF4AccCols;            // scale columns follow the accumulators
+constexpr uint32_t kF4Queue = 3;                            // tile queue entries
+constexpr uint32_t kF4DynamicTiles = 8;                     // claimed tiles from this many tiles a pair
 constexpr uint32_t kF4StgBytes = kEpiRows * kEpiRowBytes;   // one epilogue staging buffer
 constexpr uint32_t kF4StgBufs = 2;                          // per epilogue warp
 
@@ -93,8 +95,8 @@ struct F4Feed {
   uint32_t pos = 0;
   template <bool kWarp = true>
   __device__ __forceinline__ int next(Ctrl &ctl, volatile int *abort, Tile *x) {
-    const uint32_t slot = pos % kTileQueue, parity = (pos / kTileQueue) & 1u;
-    bool ok = wait_phase(smem_addr(&ctl.tq_full[slot]), parity, abort);
+    const uint32_t slot = pos % kF4Queue, parity = (pos / kF4Queue) & 1u;
+    bool ok = wait_phase_cluster(smem_addr(&ctl.tq_full[slot]), parity, abort);   // the leader fills both CTAs' queues
     if (kWarp) ok = __all_sync(0xffffffffu, ok);
     if (!ok) return -1;
     uint4 w0 = ld_shared_v4(smem_addr(&ctl.tq_info[slot])), w1 = ld_shared_v4(smem_addr(&ctl.tq_info[slot]) + 16u);
@@ -125,6 +127,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
   constexpr uint32_t kFullArrivals = 1 + 2 * kF4ScaleWarps;   // the values, both CTAs' scale warps
   constexpr uint32_t kEpiArrivals = 2 * kF4EpiWarps;
   __shared__ Ctrl ctl;
+  __shared__ uint64_t peer_free[kF4Queue];   // leader: the peer's readers have taken a queue entry
   extern __shared__ uint8_t dyn_smem[];
 
   // Warp-uniform values that steer the roles are broadcast from lane 0: the compiler then knows
@@ -153,7 +156,8 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
       mbar_init(smem_addr(&ctl.acc_empty[a]), kEpiArrivals);
     }
     mbar_init(smem_addr(&ctl.maps_ready), 1);
-    for (int q = 0; q < kTileQueue; ++q) {
+    for (uint32_t q = 0; q < kF4Queue; ++q) {
+      mbar_init(smem_addr(&peer_free[q]), 1);
       mbar_init(smem_addr(&ctl.tq_full[q]), 1);
       mbar_init(smem_addr(&ctl.tq_empty[q]), 1 + (rank == 0) + kF4EpiWarps + kF4ScaleWarps);
     }
@@ -535,26 +539,71 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
     if (!ok && lane == 0) atomicOr(p.status, kStatusTimeout);
   } else if (lane == 0) {
     // ------------------------------------------------------------ scheduler
-    // Decodes the CTA's tiles ahead of the roles (a search and loads of about a microsecond,
-    // which in the MMA warp left the tensor cores idle at every tile) and closes the queue
-    // with a tile of no rows.
+    // The leader decodes the pair's tiles ahead of the roles (a search and loads of about a
+    // microsecond, which in the MMA warp left the tensor cores idle at every tile) into both
+    // CTAs' queues and closes them with a tile of no rows; the peer tells it which entries
+    // its readers have taken.  With many tiles a pair claims them (after its first) from a
+    // counter, so that pairs which draw cheaper tiles take more; where group sizes are very
+    // uneven every second pair claims from the back of the tile order, so that the small
+    // groups' weights stream while the others run the large groups' arithmetic (as in the
+    // grouped kernel).
     bool ok = true;
-    uint32_t pos = 0;
-    for (uint32_t t = unit0;; t += units, ++pos) {
-      const uint32_t slot = pos % kTileQueue, parity = (pos / kTileQueue) & 1u;
-      Tile x{};
-      if (t < total) x = decode_tile<G>(t, prefix, p);
-      ok = wait_phase(smem_addr(&ctl.tq_empty[slot]), parity ^ 1u, abort);
-      if (!ok) break;
-      ctl.tq_info[slot] = x;
-      mbar_arrive(smem_addr(&ctl.tq_full[slot]));
-      if (t >= total) break;
+    if (rank == 0) {
+      const bool dynamic = total >= kF4DynamicTiles * units;
+      const bool two_ended = dynamic && ctl.max_group_tiles >= kUnevenRatio * ctl.min_group_tiles;
+      const bool back = two_ended && (unit0 & 1u);
+      const uint32_t backs = two_ended ? units / 2u : 0u, fronts = units - backs;   // first tiles, not claimed
+      const uint32_t info1 = map_to_rank(smem_addr(&ctl.tq_info[0]), 1), full1 = map_to_rank(smem_addr(&ctl.tq_full[0]), 1);
+      uint32_t t = two_ended ? (back ? total - 1u - unit0 / 2u : unit0 / 2u) : unit0;
+      for (uint32_t pos = 0;; ++pos) {
+        const uint32_t slot = pos % kF4Queue, parity = (pos / kF4Queue) & 1u;
+        ok = wait_phase(smem_addr(&ctl.tq_empty[slot]), parity ^ 1u, abort) &&
+             (pos < kF4Queue || wait_phase_cluster(smem_addr(&peer_free[slot]), parity ^ 1u, abort));
+        if (!ok) break;
+        if (pos > 0 && dynamic) {   // claimed only now: no further ahead of its use than the queue is long
+          const unsigned long long old =
+              atomicAdd(reinterpret_cast<unsigned long long *>(p.tile_counter), back ? (1ull << 32) : 1ull);
+          const unsigned long long f = fronts + (old & 0xffffffffull), b = backs + (old >> 32);
+          t = f + b >= total ? total : static_cast<uint32_t>(back ? total - 1u - b : f);
+        }
+        Tile x{};
+        if (t < total) x = decode_tile<G>(t, prefix, p);
+        ctl.tq_info[slot] = x;
+        const uint32_t *xw = reinterpret_cast<const uint32_t *>(&x);
+#pragma unroll
+        for (uint32_t i = 0; i < sizeof(Tile) / 4; ++i)
+          st_shared_cluster_u32(info1 + slot * static_cast<uint32_t>(sizeof(Tile)) + 4u * i, xw[i]);
+        mbar_arrive(smem_addr(&ctl.tq_full[slot]));
+        mbar_arrive_cluster(full1 + slot * 8u);
+        if (t >= total) break;
+        t += units;   // the static share's next
+      }
+    } else {
+      const uint32_t free0 = map_to_rank(smem_addr(&peer_free[0]), 0);
+      for (uint32_t pos = 0;; ++pos) {
+        const uint32_t slot = pos % kF4Queue, parity = (pos / kF4Queue) & 1u;
+        if (pos >= kF4Queue) {
+          ok = wait_phase(smem_addr(&ctl.tq_empty[slot]), parity ^ 1u, abort);
+          if (!ok) break;
+          mbar_arrive_cluster(free0 + slot * 8u);
+        }
+        ok = wait_phase_cluster(smem_addr(&ctl.tq_full[slot]), parity, abort);
+        if (!ok || *reinterpret_cast<volatile uint32_t *>(&ctl.tq_info[slot].nrows) == 0u) break;
+      }
     }
     if (!ok) atomicOr(p.status, kStatusTimeout);
   }
 
   __syncthreads();
   cluster_sync();   // no CTA leaves while its peer may still signal it
+  if (tid == 0) {
+    // The last CTA to finish returns the tile counter to zero for the next launch.
+    __threadfence();
+    if (atomicAdd(p.tile_counter + 2, 1u) == gridDim.x - 1) {
+      atomicExch(reinterpret_cast<unsigned long long *>(p.tile_counter), 0ull);
+      atomicExch(p.tile_counter + 2, 0u);
+    }
+  }
   if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc_pair(tmem_base, kTmemCols);
