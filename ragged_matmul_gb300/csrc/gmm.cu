@@ -491,7 +491,8 @@ template <int VB>
 int launch_dispatch(gmm_ctx *h, gmm::DispatchParams &p, cudaStream_t stream) {
   const int E = p.num_experts, S = p.num_tokens * p.top_k;
   if (S <= gmm::kRouteSmallSlots && E <= gmm::kRouteSmallExperts) {
-    const long long units = p.tokens ? p.num_tokens * ((p.row_bytes / VB + 32 * gmm::kRouteSmallUnit - 1) / (32 * gmm::kRouteSmallUnit)) : 0;
+    constexpr int kUnit = 32 * gmm::kRouteUnit<VB, true>;
+    const long long units = p.tokens ? p.num_tokens * ((p.row_bytes / VB + kUnit - 1) / kUnit) : 0;
     const long long want = (units + gmm::kRouteWarps - 1) / gmm::kRouteWarps;
     const int grid = static_cast<int>(std::max(1ll, std::min<long long>(want, h->num_sms)));
     gmm::gmm_dispatch_small_kernel<VB><<<grid, gmm::kRouteThreads, small_dispatch_smem(E, S), stream>>>(p);
@@ -534,21 +535,33 @@ void launch_grad(gmm_ctx *h, gmm::CombineParams &p, long long nvec, cudaStream_t
       <<<static_cast<unsigned>((p.num_tokens + tpc - 1) / tpc), 32 * gmm::kCombineWarps, 0, stream>>>(p);
 }
 
+template <class T, int VN, int kBatch, int kSeq, int kUnits>
+int launch_sum(gmm::CombineParams &p, long long nvec, cudaStream_t stream) {
+  const long long pieces = (nvec + 32 * kSeq * kUnits - 1) / (32 * kSeq * kUnits);
+  const long long ctas = (p.num_tokens * pieces + gmm::kCombineWarps - 1) / gmm::kCombineWarps;
+  if (ctas > (1ll << 28)) return GMM_ERR_UNSUPPORTED;   // warps are numbered in 32 bits
+  gmm::gmm_combine_kernel<T, VN, kBatch, kSeq, kUnits>
+      <<<static_cast<unsigned>(ctas), 32 * gmm::kCombineWarps, 0, stream>>>(p);
+  return launch_status("launch of the combine kernel");
+}
+
 template <class T, int VN>
 int launch_combine(gmm_ctx *h, gmm::CombineParams &p, bool grad, cudaStream_t stream) {
   const long long nvec = p.row_bytes / static_cast<long long>(sizeof(T) * VN);
   if (grad) {
-    if (p.top_k == 1) launch_grad<T, VN, 1, 4>(h, p, nvec, stream);
-    else if (p.top_k == 2) launch_grad<T, VN, 2, 2>(h, p, nvec, stream);
-    else launch_grad<T, VN, 4, 1>(h, p, nvec, stream);
+    // Rows at a time by top_k, and as many vectors of each as the registers hold; of single
+    // elements more, for as many bytes.
+    constexpr bool kOne = VN == 1;
+    if (p.top_k == 1) launch_grad<T, VN, 1, (kOne ? 8 : 4)>(h, p, nvec, stream);
+    else if (p.top_k == 2) launch_grad<T, VN, 2, (kOne ? 8 : 2)>(h, p, nvec, stream);
+    else if (p.top_k <= 4) launch_grad<T, VN, 4, (kOne ? 4 : 1)>(h, p, nvec, stream);
+    else launch_grad<T, VN, 8, (kOne ? 2 : 1)>(h, p, nvec, stream);
     return launch_status("launch of the combine gradient kernel");
   }
-  constexpr int kUnits = 2;
-  const long long pieces = (nvec + 32 * kUnits - 1) / (32 * kUnits);
-  const long long ctas = (p.num_tokens * pieces + gmm::kCombineWarps - 1) / gmm::kCombineWarps;
-  if (ctas > (1ll << 28)) return GMM_ERR_UNSUPPORTED;   // warps are numbered in 32 bits
-  gmm::gmm_combine_kernel<T, VN, kUnits><<<static_cast<unsigned>(ctas), 32 * gmm::kCombineWarps, 0, stream>>>(p);
-  return launch_status("launch of the combine kernel");
+  constexpr bool kOne = VN == 1;
+  if (p.top_k <= 2) return launch_sum<T, VN, 2, (kOne ? 1 : 2), (kOne ? 16 : 2)>(p, nvec, stream);
+  if (p.top_k <= 4) return launch_sum<T, VN, 4, 1, (kOne ? 8 : 2)>(p, nvec, stream);
+  return launch_sum<T, VN, 8, (kOne ? 1 : 2), (kOne ? 4 : 1)>(p, nvec, stream);
 }
 
 // 16-byte vectors where every row starts on a 16-byte boundary, else single elements.
@@ -599,19 +612,33 @@ int run_quant(gmm_ctx *h, gmm::QuantParams &p, int dtype, int format, long long 
   p.x_pitch = stride * es;
   p.scale_pitch = fp4_scale_pitch(p.K, format);
   p.status = reinterpret_cast<uint32_t *>(h->ws);
-  const long long threads = static_cast<long long>(p.rows) * (p.K / 16);
-  const long long per_cta = gmm::kQuantThreads * static_cast<long long>(quantise ? gmm::kQuantPer : gmm::kDequantPer);
-  const long long grid = (threads + per_cta - 1) / per_cta;
-  if (grid > 0x7fffffffll) return GMM_ERR_UNSUPPORTED;
   const unsigned long long at = reinterpret_cast<uintptr_t>(p.x) | static_cast<unsigned long long>(p.x_pitch);
   const int align = at % 32 == 0 ? 32 : (at % 16 == 0 ? 16 : 1);
+  // Blocks of 16 elements are numbered in 31 bits (block / blocks a row is then a multiply and
+  // a shift: for block < 2^31 and m = floor(2^(31 + l) / d) + 1 with 2^l >= d, block * m >> (31 + l));
+  // longer calls go in slabs of rows.
+  const unsigned d = static_cast<unsigned>(p.K / 16);
+  unsigned l = 0;
+  while ((1ull << l) < d) ++l;
+  p.div_mul = static_cast<uint32_t>((1ull << (31 + l)) / d + 1);
+  p.div_shift = l - 1;   // K >= 32: d >= 2
+  const int per_cta = gmm::kQuantThreads * (quantise ? gmm::kQuantPer : gmm::kDequantPer);
+  const int slab = static_cast<int>(((1ll << 31) - per_cta) / d);
   DeviceGuard guard(h->device);
-  switch (dtype) {
-    case GMM_DTYPE_BF16: launch_quant_fmt<__nv_bfloat16>(p, format, quantise, align, static_cast<unsigned>(grid), stream); break;
-    case GMM_DTYPE_FP16: launch_quant_fmt<__half>(p, format, quantise, align, static_cast<unsigned>(grid), stream); break;
-    default: launch_quant_fmt<float>(p, format, quantise, align, static_cast<unsigned>(grid), stream); break;
+  const int rows = p.rows;
+  for (int row0 = 0; row0 < rows; row0 += std::min(slab, rows - row0)) {
+    p.row0 = row0;
+    p.rows = std::min(slab, rows - row0);
+    const unsigned grid = static_cast<unsigned>((static_cast<long long>(p.rows) * d + per_cta - 1) / per_cta);
+    switch (dtype) {
+      case GMM_DTYPE_BF16: launch_quant_fmt<__nv_bfloat16>(p, format, quantise, align, grid, stream); break;
+      case GMM_DTYPE_FP16: launch_quant_fmt<__half>(p, format, quantise, align, grid, stream); break;
+      default: launch_quant_fmt<float>(p, format, quantise, align, grid, stream); break;
+    }
+    const int rc = launch_status(quantise ? "launch of the quantisation kernel" : "launch of the dequantisation kernel");
+    if (rc) return rc;
   }
-  return launch_status(quantise ? "launch of the quantisation kernel" : "launch of the dequantisation kernel");
+  return GMM_OK;
 }
 
 uint32_t max_tok(const gmm_ctx *h, bool int4) {

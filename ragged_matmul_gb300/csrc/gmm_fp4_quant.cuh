@@ -42,7 +42,10 @@ struct QuantParams {
   const int32_t *row_slots;   // quantise: source row = row_slots[r] / top_k, or null (row r)
   const float *global_scale;  // one value, or null (1)
   long long x_pitch;          // bytes
+  int row0;                   // this launch's rows: row0 .. row0 + rows - 1
   int rows;
+  uint32_t div_mul;           // block / (K / 16) = umulhi(block, div_mul) >> div_shift, for block < 2^31
+  uint32_t div_shift;
   int src_rows;               // rows of x
   int K;
   int scale_pitch;
@@ -110,21 +113,23 @@ __device__ __forceinline__ uint32_t quant_amax(const QuantRaw<T> &r) {
   }
 }
 
+// The 16 elements negated, in fp32 (see the kernel: in these signs a -0 stays -0).
 template <class T>
-__device__ __forceinline__ void quant_values(const QuantRaw<T> &r, float (&v)[16]) {
+__device__ __forceinline__ void quant_negated(const QuantRaw<T> &r, float (&v)[16]) {
   if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r.w[i]);
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r.w[i] ^ 0x80000000u);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      const uint32_t w = r.w[i] ^ 0x80008000u;
       if constexpr (std::is_same_v<T, __half>) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&r.w[i]));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
         v[2 * i] = f.x;
         v[2 * i + 1] = f.y;
       } else {
-        v[2 * i] = __uint_as_float(r.w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+        v[2 * i] = __uint_as_float(w << 16);
+        v[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
       }
     }
   }
@@ -169,12 +174,12 @@ struct QuantAt {
   bool live;
 };
 
-__device__ __forceinline__ QuantAt quant_at(const QuantParams &p, unsigned long long idx, uint32_t per_row) {
+__device__ __forceinline__ QuantAt quant_at(const QuantParams &p, uint32_t idx, uint32_t per_row) {
   QuantAt a;
-  const unsigned long long row = idx / per_row;
-  const bool in = row < static_cast<unsigned long long>(p.rows);
-  a.row = in ? static_cast<int>(row) : 0;
-  a.blk = static_cast<uint32_t>(idx - row * per_row);
+  const uint32_t row = __umulhi(idx, p.div_mul) >> p.div_shift;
+  const bool in = row < static_cast<uint32_t>(p.rows);
+  a.row = p.row0 + static_cast<int>(in ? row : 0u);
+  a.blk = idx - row * per_row;
   a.src = a.row;
   if (in && p.row_slots != nullptr) {
     const int s = __ldg(p.row_slots + a.row);
@@ -194,12 +199,12 @@ __device__ __forceinline__ QuantAt quant_at(const QuantParams &p, unsigned long 
 template <class T, bool kMx, int kAlign>
 __global__ void __launch_bounds__(kQuantThreads) gmm_quantize_fp4_kernel(const __grid_constant__ QuantParams p) {
   const uint32_t per_row = static_cast<uint32_t>(p.K) / 16u;   // K is a multiple of 32: even
-  const unsigned long long idx0 = static_cast<unsigned long long>(blockIdx.x) * (kQuantThreads * kQuantPer) + threadIdx.x;
+  const uint32_t idx0 = blockIdx.x * (kQuantThreads * kQuantPer) + threadIdx.x;
   QuantAt at[kQuantPer];
   QuantRaw<T> raw[kQuantPer];
 #pragma unroll
   for (int u = 0; u < kQuantPer; ++u) {   // both threads of a block agree on it: they share the row
-    at[u] = quant_at(p, idx0 + static_cast<unsigned long long>(u) * kQuantThreads, per_row);
+    at[u] = quant_at(p, idx0 + static_cast<uint32_t>(u) * kQuantThreads, per_row);
     raw[u] = QuantRaw<T>{};
     if (at[u].live)
       raw[u] = quant_load<T, kAlign>(p.x + at[u].src * p.x_pitch + static_cast<long long>(at[u].blk) * 16 * sizeof(T));
@@ -211,13 +216,13 @@ __global__ void __launch_bounds__(kQuantThreads) gmm_quantize_fp4_kernel(const _
     uint32_t amax = quant_amax<T>(raw[u]);
     if (kMx) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     if (!at[u].live) continue;
-    float v[16];
-    quant_values<T>(raw[u], v);
+    float v[16], y[16];   // -x, and x / d
+    quant_negated<T>(raw[u], v);
     uint32_t code;
     if (amax >= 0x7f800000u) {
       code = kMx ? kE8m0Nan : kE4m3Nan;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+      for (int i = 0; i < 16; ++i) y[i] = 0.0f;
     } else if constexpr (kMx) {
       // floor(log2 amax) is the exponent field less 127; a subnormal's field is 0.
       const uint32_t field = amax >> 23;
@@ -225,23 +230,24 @@ __global__ void __launch_bounds__(kQuantThreads) gmm_quantize_fp4_kernel(const _
       // 1 / d is a power of two too, and x / d is x with another exponent.
       const float inv = __uint_as_float((254u - code) << 23);   // code is at most 252
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] *= inv;
+      for (int i = 0; i < 16; i += 2) mul_f32x2(y[i], y[i + 1], -inv, v[i], v[i + 1]);
     } else {
       code = float_to_e4m3(__fdiv_rn(__uint_as_float(amax), 6.0f * g));
       const float d = e4m3_to_float(code) * g;
       const float r = __frcp_rn(d);
       if (d > 1e-30f && d < 1e30f && __uint_as_float(amax) * r < 1e30f) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float y = v[i] * r;
-          v[i] = fmaf(fmaf(y, d, -v[i]), -r, y);   // in these signs a -0 stays -0
+        for (int i = 0; i < 16; i += 2) {
+          mul_f32x2(y[i], y[i + 1], -r, v[i], v[i + 1]);      // y = x r
+          fma_f32x2(v[i], v[i + 1], d, y[i], y[i + 1]);       // e = y d - x
+          fma_f32x2(y[i], y[i + 1], -r, v[i], v[i + 1]);      // y - e r
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = d == 0.0f ? 0.0f : __fdiv_rn(v[i], d);
+        for (int i = 0; i < 16; ++i) y[i] = d == 0.0f ? 0.0f : __fdiv_rn(-v[i], d);
       }
     }
-    const uint2 w = make_uint2(pack_e2m1x8(v), pack_e2m1x8(v + 8));
+    const uint2 w = make_uint2(pack_e2m1x8(y), pack_e2m1x8(y + 8));
     reinterpret_cast<uint2 *>(p.packed + static_cast<size_t>(at[u].row) * (p.K / 2))[blk] = w;
     uint8_t *srow = p.scales + static_cast<size_t>(at[u].row) * p.scale_pitch;
     if (kMx) {
@@ -268,23 +274,25 @@ __device__ __forceinline__ float2 e2m1x2_to_float2(uint32_t byte) {
 template <class T, bool kMx, int kAlign>
 __global__ void __launch_bounds__(kQuantThreads) gmm_dequantize_fp4_kernel(const __grid_constant__ QuantParams p) {
   const uint32_t per_row = static_cast<uint32_t>(p.K) / 16u;
-  const unsigned long long idx0 = static_cast<unsigned long long>(blockIdx.x) * (kQuantThreads * kDequantPer) + threadIdx.x;
+  const uint32_t idx0 = blockIdx.x * (kQuantThreads * kDequantPer) + threadIdx.x;
   const float g = !kMx && p.global_scale != nullptr ? __ldg(p.global_scale) : 1.0f;
   uint2 w[kDequantPer];
   uint32_t code[kDequantPer];
 #pragma unroll
   for (int u = 0; u < kDequantPer; ++u) {
-    const unsigned long long idx = idx0 + static_cast<unsigned long long>(u) * kQuantThreads, row = idx / per_row;
-    if (row >= static_cast<unsigned long long>(p.rows)) continue;
-    const uint32_t blk = static_cast<uint32_t>(idx - row * per_row);
+    const uint32_t idx = idx0 + static_cast<uint32_t>(u) * kQuantThreads, q = __umulhi(idx, p.div_mul) >> p.div_shift;
+    if (q >= static_cast<uint32_t>(p.rows)) continue;
+    const uint32_t blk = idx - q * per_row;
+    const size_t row = static_cast<size_t>(p.row0) + q;
     w[u] = __ldg(reinterpret_cast<const uint2 *>(p.packed + row * (p.K / 2)) + blk);
     code[u] = __ldg(p.scales + row * p.scale_pitch + (kMx ? blk >> 1 : blk));
   }
 #pragma unroll
   for (int u = 0; u < kDequantPer; ++u) {
-    const unsigned long long idx = idx0 + static_cast<unsigned long long>(u) * kQuantThreads, row = idx / per_row;
-    if (row >= static_cast<unsigned long long>(p.rows)) continue;
-    const uint32_t blk = static_cast<uint32_t>(idx - row * per_row);
+    const uint32_t idx = idx0 + static_cast<uint32_t>(u) * kQuantThreads, q = __umulhi(idx, p.div_mul) >> p.div_shift;
+    if (q >= static_cast<uint32_t>(p.rows)) continue;
+    const uint32_t blk = idx - q * per_row;
+    const size_t row = static_cast<size_t>(p.row0) + q;
     float d;
     if constexpr (kMx) d = e8m0_to_float(code[u]);
     else d = e4m3_to_float(code[u]) * g;

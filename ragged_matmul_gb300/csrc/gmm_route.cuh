@@ -31,7 +31,6 @@ constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kRouteMaxTopK = 32;          // a token's slots are held one per lane
 constexpr int kRouteSmallSlots = 4096;     // up to here (and kRouteSmallExperts) one launch sorts and copies
 constexpr int kRouteSmallExperts = 1024;
-constexpr int kRouteSmallUnit = 1;         // vectors a lane and copy unit there: few bytes, spread over many SMs
 constexpr int kRouteMaxExperts = 4096;     // one group per expert: the grouped kernels' limit
 constexpr int kRouteMaxCounts = 32768;     // chunk counts (chunks x experts) in the workspace
 constexpr int kRouteMaxChunks = 152;
@@ -112,6 +111,12 @@ __device__ __forceinline__ void route_scan(uint32_t *v, int n, uint32_t *warp_su
   if (tid == kRouteThreads - 1) v[n] = run;
   __syncthreads();
 }
+
+// Vectors a lane and copy unit: 2 KB of a token with 16-byte vectors; with narrow ones more of
+// them, to keep as many bytes in flight.  In the one-launch form, few bytes spread over many
+// SMs: 512 bytes.
+template <int VB, bool kSmall>
+constexpr int kRouteUnit = VB == 16 ? (kSmall ? 1 : 4) : (kSmall ? 4 : 16);
 
 template <int VB>
 struct RouteVec;
@@ -202,7 +207,7 @@ __global__ void __launch_bounds__(kRouteThreads) gmm_dispatch_small_kernel(const
   }
   if (p.tokens == nullptr) return;
   __syncthreads();
-  route_copy<VB, kRouteSmallUnit>(p, row_s, 0, p.num_tokens, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
+  route_copy<VB, kRouteUnit<VB, true>>(p, row_s, 0, p.num_tokens, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
 }
 
 // Many slots, first launch: CTA c counts the experts of its chunk of tokens and leaves every
@@ -310,7 +315,7 @@ __global__ void __launch_bounds__(kRouteThreads) gmm_dispatch_place_kernel(const
       row_s[i] = row;
     }
     __syncthreads();
-    if (p.tokens != nullptr) route_copy<VB, 4>(p, row_s, t, n, 0, 1);
+    if (p.tokens != nullptr) route_copy<VB, kRouteUnit<VB, false>>(p, row_s, t, n, 0, 1);
   }
 }
 
@@ -443,48 +448,61 @@ __device__ __forceinline__ int route_slot(const CombineParams &p, int t, int lan
 }
 
 constexpr int kCombineWarps = 8;
-constexpr int kCombineBatch = 8;   // rows of a token whose loads are in flight together
 
-// Bound by the rows' bytes.  A warp per (token, 32 kUnits vectors): its slots are read once, a
-// lane each, and the loads of kCombineBatch rows are in flight together; at 64 registers a
-// thread half of an SM's warps are resident, which keeps enough of them in flight (with 100
-// registers and a quarter, 32768 rows of 8 KB to 4096 tokens took 73 us).
-template <class T, int VN, int kUnits>
+// Bound by the rows' bytes.  A warp per (token, 32 kSeq kUnits vectors): its slots are read
+// once, a lane each, and the loads of kBatch rows of kUnits vectors are in flight together
+// (kBatch by top_k; fewer rows in larger units, and single elements, for rows that are not
+// 16-byte aligned, in larger ones still).  At 64
+// registers a thread half of an SM's warps are resident, which keeps enough loads in flight
+// (with 100 registers and a quarter, 32768 rows of 8 KB to 4096 tokens took 73 us, now 49).
+template <class T, int VN, int kBatch, int kSeq, int kUnits>
 __global__ void __launch_bounds__(32 * kCombineWarps, 4) gmm_combine_kernel(const __grid_constant__ CombineParams p) {
   const int lane = threadIdx.x & 31;
   const int nvec = static_cast<int>(p.row_bytes / (sizeof(T) * VN));
-  const int pieces = (nvec + 32 * kUnits - 1) / (32 * kUnits);
+  constexpr int kPiece = 32 * kSeq * kUnits;
+  const uint32_t pieces = static_cast<uint32_t>((nvec + kPiece - 1) / kPiece);
   const uint32_t u = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
-  const uint32_t t = u / static_cast<uint32_t>(pieces);
+  const uint32_t t = u / pieces;
   if (t >= static_cast<uint32_t>(p.num_tokens)) return;
-  const int v0 = static_cast<int>(u - t * pieces) * 32 * kUnits + lane;
+  const int first = static_cast<int>(u - t * pieces) * kPiece + lane;
   float w;
   const int r = route_slot(p, static_cast<int>(t), lane, &w);
 #pragma unroll
-  for (int q = 0; q < kUnits; ++q) {
-    const int v = v0 + 32 * q;
-    float acc[VN];
+  for (int s = 0; s < kSeq; ++s) {
+    const int v0 = first + 32 * kUnits * s;
+    float acc[kUnits][VN];
 #pragma unroll
-    for (int i = 0; i < VN; ++i) acc[i] = 0.0f;
-    for (int j0 = 0; j0 < p.top_k; j0 += kCombineBatch) {
-      RoutePack<T, VN> x[kCombineBatch];
+    for (int q = 0; q < kUnits; ++q)
 #pragma unroll
-      for (int j = 0; j < kCombineBatch; ++j) {
+      for (int i = 0; i < VN; ++i) acc[q][i] = 0.0f;
+    for (int j0 = 0; j0 < p.top_k; j0 += kBatch) {
+      RoutePack<T, VN> x[kBatch][kUnits];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
         const int rj = __shfl_sync(0xffffffffu, r, (j0 + j) & 31);   // (a lane past top_k holds -1)
-        if (rj >= 0 && j0 + j < p.top_k && v < nvec) x[j] = route_load<T, VN>(p.rows + rj * p.row_bytes, v);
+#pragma unroll
+        for (int q = 0; q < kUnits; ++q)
+          if (rj >= 0 && j0 + j < p.top_k && v0 + 32 * q < nvec)
+            x[j][q] = route_load<T, VN>(p.rows + rj * p.row_bytes, v0 + 32 * q);
       }
 #pragma unroll
-      for (int j = 0; j < kCombineBatch; ++j) {
+      for (int j = 0; j < kBatch; ++j) {
         const int rj = __shfl_sync(0xffffffffu, r, (j0 + j) & 31);
         const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
-        if (rj >= 0 && j0 + j < p.top_k && v < nvec) {
-          float y[VN];
-          route_unpack<T, VN>(x[j], y);
-          route_fma<VN>(acc, wj, y);
+        if (rj >= 0 && j0 + j < p.top_k) {
+#pragma unroll
+          for (int q = 0; q < kUnits; ++q)
+            if (v0 + 32 * q < nvec) {
+              float y[VN];
+              route_unpack<T, VN>(x[j][q], y);
+              route_fma<VN>(acc[q], wj, y);
+            }
         }
       }
     }
-    if (v < nvec) route_store<T, VN>(p.out + t * p.out_pitch, v, acc);
+#pragma unroll
+    for (int q = 0; q < kUnits; ++q)
+      if (v0 + 32 * q < nvec) route_store<T, VN>(p.out + t * p.out_pitch, v0 + 32 * q, acc[q]);
   }
 }
 
@@ -494,7 +512,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 4) gmm_combine_kernel(cons
 // shared memory in warp order.  The loads of a piece's kUnits (kRows + 1) vectors are in flight
 // together.
 template <class T, int VN, int kRows, int kUnits>
-__global__ void __launch_bounds__(32 * kCombineWarps, 4)
+__global__ void __launch_bounds__(32 * kCombineWarps, kRows == 8 ? 3 : 4)
     gmm_combine_grad_kernel(const __grid_constant__ CombineParams p) {
   __shared__ float part[kCombineWarps][kRouteMaxTopK];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

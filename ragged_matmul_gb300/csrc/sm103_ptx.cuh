@@ -376,6 +376,17 @@ __device__ __forceinline__ void fma_f32x2(float &d0, float &d1, float a, float b
       : "f"(a), "f"(b0), "f"(b1));
 }
 
+// (d0, d1) = a * (b0, b1), each rounded by itself.
+__device__ __forceinline__ void mul_f32x2(float &d0, float &d1, float a, float b0, float b1) {
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %2};\n\t"
+      "mov.b64 y, {%3, %4};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\t"
+      "mov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a), "f"(b0), "f"(b1));
+}
+
 // 16 TMEM lanes x 32 columns in the 16x256b shape (four repeats of 16 lanes x 8
 // columns).  In repeat j (v[4j] .. v[4j + 3]) thread t holds lane t/4, columns
 // 8j + 2(t%4) and 8j + 2(t%4) + 1 (v[4j], v[4j + 1]), and the same two columns of
