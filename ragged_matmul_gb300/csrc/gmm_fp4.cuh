@@ -6,7 +6,7 @@
 // The scales enter in the tensor core (tcgen05.mma kind::mxf4nvf4), fp32 accumulation.
 //
 // Orientation and pairs are the grouped kernel's: weights are the MMA's M (256 rows over a
-// CTA pair), tokens its N (a multiple of 32 up to 224).  A stage is 256 of K: 128-byte rows
+// CTA pair), tokens its N (a multiple of 16 up to 240).  A stage is 256 of K: 128-byte rows
 // of packed values, so the value operands go through the bf16 kernel's tensor maps, swizzle
 // and descriptors unchanged.
 //
@@ -23,7 +23,7 @@
 // Both CTAs of a pair hold the scales of all the tile's tokens (each computes its own 128
 // weight rows against all of them), and of their own 128 weight rows.
 //
-// Tensor memory: two accumulators of 224 columns and 48 columns of scales.
+// Tensor memory: two accumulators of 240 columns and 24 columns of scales (half a stage's).
 //
 // Roles (448 threads per CTA):
 //   warp 0        TMA producer of the stage's weight and token values.
@@ -46,8 +46,10 @@ constexpr uint32_t kF4EpiWarps = 8;
 constexpr uint32_t kF4ScaleWarps = 3;
 constexpr uint32_t kF4FirstScaleWarp = 2 + kF4EpiWarps;
 constexpr int kF4Threads = 32 * static_cast<int>(2 + kF4EpiWarps + kF4ScaleWarps + 1);
-constexpr uint32_t kF4MaxTok = 224;
-constexpr uint32_t kF4TokAlign = 32;
+constexpr uint32_t kF4MaxTok = 240;
+constexpr uint32_t kF4TokAlign = 16;
+constexpr uint32_t kF4TokMaps = kF4MaxTok / 16;             // a CTA loads half of a tile's tokens: 8, 16, ... 120 rows
+static_assert(kF4TokMaps <= static_cast<uint32_t>(kTokMaps), "a map slot per copy height");
 constexpr uint32_t kF4StageK = 256;
 constexpr uint32_t kF4WBytes = kBlockN * 128;               // 128 weight rows x 128 bytes
 constexpr uint32_t kF4TBytes = kF4MaxTok / 2 * 128;         // a CTA's half of the tokens
@@ -66,7 +68,8 @@ struct F4Scale {
   static constexpr uint32_t kStepsPerWord = kMx ? 2 : 1;
   static constexpr uint32_t kBlock = kMx ? 32 : 16;
   static constexpr uint32_t kBytes = 3 * kWords * kF4Atom;   // a stage's atoms: weights, then tokens
-  static_assert(kF4ScaleCol + 12 * kWords <= kTmemCols, "scales beside the accumulators");
+  static constexpr uint32_t kHalfWords = kWords / 2;         // words of half a stage, in tensor memory at a time
+  static_assert(kF4ScaleCol + 12 * kHalfWords <= kTmemCols, "scales beside the accumulators");
 };
 
 template <bool kMx>
@@ -215,10 +218,10 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
         const uint64_t t_pol = p.cache_hints ? pol_last : pol_normal;
         if (!maps_acquired) {
           if (!wait_phase(smem_addr(&ctl.maps_ready), 0, abort)) { ok = false; break; }
-          for (uint32_t i = 0; i < kF4MaxTok / 32; ++i) tensormap_acquire(slot + i * 128);
+          for (uint32_t i = 0; i < kF4TokMaps; ++i) tensormap_acquire(slot + i * 128);
           maps_acquired = true;
         }
-        const CUtensorMap *tok = tok_maps + (my_tok / 16u - 1u);
+        const CUtensorMap *tok = tok_maps + (my_tok / 8u - 1u);
         for (int kb = 0; kb < KB; ++kb) {
           const uint32_t full_local = smem_addr(&ctl.full[rt.slot]);
           if (!wait_phase(smem_addr(&ctl.empty[rt.slot]), rt.phase ^ 1u, abort)) { ok = false; break; }
@@ -252,7 +255,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
       const uint32_t v_hi = static_cast<uint32_t>(w_desc >> 32);   // the same for both value operands
       const uint32_t s_lo = static_cast<uint32_t>(s_desc), s_hi = static_cast<uint32_t>(s_desc >> 32);
       const uint32_t full0 = smem_addr(&ctl.full[0]), empty0 = smem_addr(&ctl.empty[0]);
-      const uint32_t sfa = tmem_base + kF4ScaleCol, sfb = sfa + 4u * S::kWords;
+      const uint32_t sfa = tmem_base + kF4ScaleCol, sfb = sfa + 4u * S::kHalfWords;
       F4Feed feed;
       Tile ti, tn;
       int got = feed.next(ctl, abort, &ti);
@@ -292,15 +295,15 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
   } else if (warp < static_cast<int>(kF4FirstScaleWarp)) {
     // ------------------------------------------------------------ epilogue
     if (warp == 2) {
-      // The producer's token maps, as in the grouped kernel.
+      // The producer's token maps, as in the grouped kernel, of 8, 16, ... rows.
       uint8_t *slot = p.map_slots + static_cast<size_t>(blockIdx.x) * kMapSlotBytes;
-      if (total > 0 && lane < static_cast<int>(kF4MaxTok / 32)) {
+      if (total > 0 && lane < static_cast<int>(kF4TokMaps)) {
         const uint4 *src = reinterpret_cast<const uint4 *>(&p.tok_map);
         uint4 *dst = reinterpret_cast<uint4 *>(slot + lane * 128);
 #pragma unroll
         for (int i = 0; i < 8; ++i) dst[i] = src[i];
         tensormap_set_dim1(dst, __ldg(p.a_offsets + p.num_groups));
-        tensormap_set_box1(dst, 16u * static_cast<uint32_t>(lane + 1));
+        tensormap_set_box1(dst, 8u * static_cast<uint32_t>(lane + 1));
         tensormap_release();
       }
       __syncwarp();
@@ -329,7 +332,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
       const float gs = ga * (p.g_w != nullptr ? __ldg(p.g_w + ti.e) : 1.0f);
       // Operands of the fused epilogue, loaded before the accumulator wait: the bias of the
       // thread's 4 fragment columns, the row scales of this warp's chunks (lane l: row l).
-      constexpr int kRowRegs = static_cast<int>((kF4MaxTok / 32 + kSub - 1) / kSub);
+      constexpr int kRowRegs = static_cast<int>(((kF4MaxTok + 31) / 32 + kSub - 1) / kSub);
       float rs[kRowRegs], bias4[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
     if (lane == 0) bulk_wait_all();
   } else if (warp < static_cast<int>(kF4FirstScaleWarp + kF4ScaleWarps)) {
     // ------------------------------------------------------------ scales
-    // Warp role 0: the CTA's 128 weight rows; 1 and 2: token rows 0 .. 127 and 128 .. 223.
+    // Warp role 0: the CTA's 128 weight rows; 1 and 2: token rows 0 .. 127 and 128 .. 239.
     // Rows past the matrix or the group repeat the last one (their results are not stored);
     // scale bytes past K are zeroed, as the values there are.  A row is read 32 bytes (a whole
     // L2 sector, kStages stages) at a time, one chunk ahead of its use in registers, by one

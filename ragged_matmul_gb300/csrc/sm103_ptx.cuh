@@ -688,10 +688,11 @@ __device__ __forceinline__ void mma_stage_f8_x4(uint32_t d_tmem, uint32_t a_lo, 
 // memory.  kVec4 (four scales per row and instruction): word j serves instruction j; else
 // (two) word j serves instructions 2j and 2j + 1, its first and second half by the scale ids
 // of the instruction descriptor (idesc, idesc2).  In shared memory (descriptor s_lo, s_hi) the
-// weights' atoms come first, then per word the tokens' two; tensor memory holds the weights'
-// words from column `sfa`, 4 apart, and the tokens' from `sfb`, 8 apart.  `two` = 0 leaves
-// out the second token atom (at most 128 tokens).
-// The copies run in order with the MMAs; one elected lane issues everything from operands
+// weights' atoms come first, then per word the tokens' two; tensor memory holds a half's
+// words: the weights' from column `sfa`, 4 apart, and the tokens' from `sfb`, 8 apart, the
+// next half's in the same columns.  `two` = 0 leaves out the second token atom (at most 128
+// tokens).
+// The copies run in order with the MMAs, so columns can be reused at once; one elected lane issues everything from operands
 // that need no further address arithmetic but adds to the low words: with an elect and
 // 64-bit descriptor arithmetic per instruction the issuing warp took twice the MMAs' time.
 // The halves leave room to test the next stage's barrier while MMAs are in the pipe.
@@ -726,10 +727,10 @@ __device__ __forceinline__ void mma_half_stage_e2m1_pair(uint32_t d_tmem, uint32
                  : "memory");
   } else if constexpr (kVec4) {
     asm volatile(GMM_F4_HEAD
-                 GMM_F4_CP("%8", "8", "64", "e") GMM_F4_CP("%9", "16", "256", "e") GMM_F4_CP("%9", "20", "288", "q")
-                 GMM_F4_MMA("4", "4", "%4", "8", "16", "t")
-                 GMM_F4_CP("%8", "12", "96", "e") GMM_F4_CP("%9", "24", "320", "e") GMM_F4_CP("%9", "28", "352", "q")
-                 GMM_F4_MMA("4", "6", "%4", "12", "24", "t") GMM_F4_COMMIT "}" ::GMM_F4_OPERANDS
+                 GMM_F4_CP("%8", "0", "64", "e") GMM_F4_CP("%9", "0", "256", "e") GMM_F4_CP("%9", "4", "288", "q")
+                 GMM_F4_MMA("4", "4", "%4", "0", "0", "t")
+                 GMM_F4_CP("%8", "4", "96", "e") GMM_F4_CP("%9", "8", "320", "e") GMM_F4_CP("%9", "12", "352", "q")
+                 GMM_F4_MMA("4", "6", "%4", "4", "8", "t") GMM_F4_COMMIT "}" ::GMM_F4_OPERANDS
                  : "memory");
   } else if constexpr (kHalf == 0) {
     asm volatile(GMM_F4_HEAD
@@ -738,8 +739,8 @@ __device__ __forceinline__ void mma_half_stage_e2m1_pair(uint32_t d_tmem, uint32
                  : "memory");
   } else {
     asm volatile(GMM_F4_HEAD
-                 GMM_F4_CP("%8", "4", "32", "e") GMM_F4_CP("%9", "8", "128", "e") GMM_F4_CP("%9", "12", "160", "q")
-                 GMM_F4_MMA("2", "4", "%4", "4", "8", "t") GMM_F4_MMA("2", "6", "%5", "4", "8", "t") GMM_F4_COMMIT "}"
+                 GMM_F4_CP("%8", "0", "32", "e") GMM_F4_CP("%9", "0", "128", "e") GMM_F4_CP("%9", "4", "160", "q")
+                 GMM_F4_MMA("2", "4", "%4", "0", "0", "t") GMM_F4_MMA("2", "6", "%5", "0", "0", "t") GMM_F4_COMMIT "}"
                  ::GMM_F4_OPERANDS
                  : "memory");
   }
