@@ -35,8 +35,8 @@
  *
  * A handle owns a small device workspace (a status word, a 64-bit tile-claim
  * word and a finished-CTA counter that each launch returns to zero, the routing of
- * gmm_matmul_int4's single group, and per-CTA tensor-map slots) that
- * every launch made through it rewrites.  Launches made through the
+ * gmm_matmul_int4's single group, per-CTA tensor-map slots, and the chunk counts of
+ * gmm_dispatch) that every launch made through it rewrites.  Launches made through the
  * same handle must therefore not overlap on the GPU: issue them on one stream, or
  * use one handle per stream.
  */
