@@ -525,10 +525,13 @@ int launch_dispatch(gmm_ctx *h, gmm::DispatchParams &p, cudaStream_t stream) {
 
 template <class T, int VN, int kRows, int kUnits>
 void launch_grad(gmm_ctx *h, gmm::CombineParams &p, long long nvec, cudaStream_t stream) {
-  // One warp a token when that fills the SMs (32 resident warps each), else more.
+  // One warp a token when that fills the SMs (32 resident warps each; 24 for single elements,
+  // whose pieces are shorter: 1003 tokens of 1411 fp32 17.3 us with four warps a token, 18.8
+  // with eight), else more.
+  constexpr long long kFill = VN == 1 ? 24 : 32;
   const long long pieces = (nvec + 32 * kUnits - 1) / (32 * kUnits);
   int wpt = 1;
-  while (wpt < gmm::kCombineWarps && wpt < pieces && static_cast<long long>(p.num_tokens) * wpt < 32ll * h->num_sms) wpt *= 2;
+  while (wpt < gmm::kCombineWarps && wpt < pieces && p.num_tokens * static_cast<long long>(wpt) < kFill * h->num_sms) wpt *= 2;
   p.warps_per_token = wpt;
   const int tpc = gmm::kCombineWarps / wpt;
   gmm::gmm_combine_grad_kernel<T, VN, kRows, kUnits>
@@ -554,8 +557,8 @@ int launch_combine(gmm_ctx *h, gmm::CombineParams &p, bool grad, cudaStream_t st
     constexpr bool kOne = VN == 1;
     if (p.top_k == 1) launch_grad<T, VN, 1, (kOne ? 8 : 4)>(h, p, nvec, stream);
     else if (p.top_k == 2) launch_grad<T, VN, 2, (kOne ? 8 : 2)>(h, p, nvec, stream);
-    else if (p.top_k <= 4) launch_grad<T, VN, 4, (kOne ? 4 : 1)>(h, p, nvec, stream);
-    else launch_grad<T, VN, 8, (kOne ? 2 : 1)>(h, p, nvec, stream);
+    else if (kOne || p.top_k <= 4) launch_grad<T, VN, 4, (kOne ? 2 : 1)>(h, p, nvec, stream);
+    else launch_grad<T, VN, 8, 1>(h, p, nvec, stream);
     return launch_status("launch of the combine gradient kernel");
   }
   constexpr bool kOne = VN == 1;

@@ -193,7 +193,8 @@ __device__ __forceinline__ QuantAt quant_at(const QuantParams &p, uint32_t idx, 
   return a;
 }
 
-// Bound by the bytes of x and the codes.  A thread takes kQuantPer blocks of 16 elements,
+// Bound by the bytes of x and the codes (32768 rows of 4096 bf16 to mxfp4 and back in 105 us,
+// 6.5 TB/s; nvfp4's arithmetic takes a fifth more).  A thread takes kQuantPer blocks of 16 elements,
 // kQuantThreads apart, with their loads in flight together (one left 49 KB of an SM's loads in
 // flight, at the limit of the latency); the two threads of an mxfp4 block exchange their maxima.
 template <class T, bool kMx, int kAlign>
