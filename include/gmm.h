@@ -278,8 +278,8 @@ int gmm_combine_grad(gmm_handle_t h, void *d_rows, float *d_weights, const void 
 /*
  * Microscaled 4-bit floating point.  A value is e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
  * negatives) times its block's scale; blocks run along K.
- *   GMM_FP4_NV (nvfp4): blocks of 16, e4m3 scales, and an optional fp32 scale of the whole
- *                       tensor (of each expert's weights).
+ *   GMM_FP4_NV (nvfp4): blocks of 16, e4m3 scales (sign bit clear), and an optional fp32
+ *                       scale of the whole tensor (of each expert's weights).
  *   GMM_FP4_MX (mxfp4): blocks of 32, e8m0 scales (powers of two: 2^(code - 127)).
  * packed: uint8 [rows, K / 2], element k in nibble k % 2 of byte k / 2, low nibble first.
  * scales: uint8 [rows, GMM_FP4_SCALE_PITCH(K, block)]: one byte per block, each row padded to

@@ -421,6 +421,92 @@ def test_product_replays_in_a_graph():
         check_product(c, C, S, live, K)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("budget", [200 * 1024, 170 * 1024])
+def test_product_with_less_shared_memory(fmt, budget, monkeypatch):
+    """Shallower rings on a device that offers a block less shared memory."""
+    _, binding = _mods()
+    monkeypatch.setenv("GMM_SMEM_BUDGET", str(budget))
+    h = binding.gmm_create(2, 0)
+    monkeypatch.delenv("GMM_SMEM_BUDGET")
+    monkeypatch.setitem(_handles, 2, h)
+    rng = np.random.default_rng(18)
+    K, N, off, ids = 1600, 328, [0, 250, 611], [1, 0]
+    a, a_s = ref.random_operand(rng, (611,), K, fmt)
+    b, b_s = ref.random_operand(rng, (2, N), K, fmt)
+    C, S, live = ref.product(a, a_s, off, b, b_s, ids, fmt)
+    c, _, status = run_product(a, a_s, off, b, b_s, ids, fmt)
+    assert status == 0
+    check_product(c, C, S, live, K)
+
+
+def test_product_most_groups():
+    """4096 groups (the limit) of zero to two rows, repeated experts, some skipped; one more is refused."""
+    torch, binding = _mods()
+    rng = np.random.default_rng(19)
+    K, N, G, E = 96, 24, 4096, 5
+    loads, ids = rng.integers(0, 3, G), rng.integers(-1, E, G)
+    off = np.concatenate([[0], np.cumsum(loads)])
+    a, a_s = ref.random_operand(rng, (off[-1],), K, "mxfp4")
+    b, b_s = ref.random_operand(rng, (E, N), K, "mxfp4")
+    C, S, live = ref.product(a, a_s, off, b, b_s, ids, "mxfp4")
+    c, stats, status = run_product(a, a_s, off, b, b_s, ids, "mxfp4")
+    assert status == 0 and stats[1] == (ids >= 0).sum()
+    check_product(c, C, S, live, K)
+    with pytest.raises(binding.GmmError) as err:
+        run_product(a, a_s, np.append(off, off[-1]), b, b_s, np.append(ids, 0), "mxfp4")
+    assert err.value.code == binding.GMM_ERR_UNSUPPORTED
+
+
+def test_product_launches_leave_the_handle_clean():
+    """Launches that claim tiles from the handle's counter, from one end and from both, one after
+    the other and between other products of the handle: each finds the counter at zero."""
+    torch, binding = _mods()
+    rng = np.random.default_rng(20)
+    K, N, E = 64, 2048, 8
+    h = handle(E)
+    w16 = torch.randn((E, N, K), device="cuda").bfloat16()
+    for loads in ([900] * 8, [6000, 1, 5, 900, 0, 240, 241, 33], [6000, 1, 5, 900, 0, 240, 241, 33]):
+        off = np.concatenate([[0], np.cumsum(loads)])
+        a, a_s = ref.random_operand(rng, (off[-1],), K, "nvfp4")
+        b, b_s = ref.random_operand(rng, (E, N), K, "nvfp4")
+        C, S, live = ref.product(a, a_s, off, b, b_s, range(E), "nvfp4")
+        for _ in range(2):
+            c, stats, status = run_product(a, a_s, off, b, b_s, range(E), "nvfp4")
+            assert status == 0
+            check_product(c, C, S, live, K)
+        x = torch.randn((int(off[-1]), K), device="cuda").bfloat16()
+        y = torch.zeros((int(off[-1]), N), dtype=torch.bfloat16, device="cuda")
+        st = torch.zeros(2, dtype=torch.int32, device="cuda")
+        binding.gmm_run(h, y, x, dev(off.astype(np.int32)), w16, dev(np.arange(E, dtype=np.int32)), st)
+        want = torch.cat([x[off[e]:off[e + 1]].double() @ w16[e].double().t() for e in range(E)])
+        assert binding.gmm_query_status(h) == 0
+        assert float((y.double() - want).abs().max()) <= float(want.abs().max()) * 2.0 ** -7
+
+
+def test_two_handles_on_two_streams():
+    torch, binding = _mods()
+    rng = np.random.default_rng(21)
+    K, N, E, R = 512, 1024, 2, 900
+    jobs = []
+    for i in range(2):
+        a, a_s = ref.random_operand(rng, (R,), K, "nvfp4")
+        b, b_s = ref.random_operand(rng, (E, N), K, "nvfp4")
+        off = [0, 300 + 100 * i, R]
+        jobs.append((a, a_s, off, b, b_s, binding.gmm_create(E, 0), torch.cuda.Stream(),
+                     torch.zeros((R, N), dtype=torch.bfloat16, device="cuda"),
+                     [dev(x) for x in (a, np.asarray(off, np.int32), b, np.arange(E, dtype=np.int32), np.zeros(2, np.int32), a_s, b_s)]))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for a, a_s, off, b, b_s, h, s, c, d in jobs:
+            binding.gmm_run_fp4(h, c, *d, stream=s)
+    for a, a_s, off, b, b_s, h, s, c, d in jobs:
+        assert binding.gmm_query_status(h, s) == 0
+        C, S, live = ref.product(a, a_s, off, b, b_s, range(E), "nvfp4")
+        check_product(c, C, S, live, K)
+        binding.gmm_destroy(h)
+
+
 def test_refusals():
     torch, binding = _mods()
     h = handle(2)
