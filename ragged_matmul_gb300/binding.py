@@ -191,6 +191,17 @@ def _check(t, name, dtypes, device, min_numel=0):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _ptr(t, name, dtypes, device, min_numel=0):
+    """_check's pointer as an integer; one test for a tensor that passes."""
+    try:
+        if (t.get_device() == device and t.dtype in dtypes and t.is_contiguous()
+                and (not min_numel or t.numel() >= min_numel)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _check(t, name, dtypes, device, min_numel).value
+
+
 _I32_TYPES = None
 
 
@@ -203,11 +214,10 @@ def _i32_types():
 
 
 def _routing_args(h, a_offsets, expert_ids, stats):
-    import torch
     G = expert_ids.numel()
-    return (_check(a_offsets, "a_offsets", _i32_types(), h.device, G + 1),
-            _check(expert_ids, "expert_ids", (torch.int32,), h.device),
-            _check(stats, "expert_usage_stats", _i32_types(), h.device, 2), G)
+    i32 = _i32_types()
+    return (_ptr(a_offsets, "a_offsets", i32, h.device, G + 1), _ptr(expert_ids, "expert_ids", i32[:1], h.device),
+            _ptr(stats, "expert_usage_stats", i32, h.device, 2), G)
 
 
 def _epilogue(h: Handle, rows: int, N: int, bias, row_scale, activation) -> GmmEpilogue:
@@ -414,17 +424,6 @@ def gmm_matmul_int4(h: Handle, c, a, b_packed, b_scales, group_size: int = 128, 
 
 # ---------------------------------------------------------------- tokens sorted by expert and back
 
-def _ptr(t, name, dtypes, device, min_numel=0):
-    """_check's pointer as an integer; one test for a tensor that passes."""
-    try:
-        if (t.get_device() == device and t.dtype in dtypes and t.is_contiguous()
-                and (not min_numel or t.numel() >= min_numel)):
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    return _check(t, name, dtypes, device, min_numel).value
-
-
 _ROW_TYPES = None
 
 
@@ -569,11 +568,12 @@ def fp4_scale_pitch(K: int, fmt="nvfp4") -> int:
 
 def _check_fp4(packed, scales, names, fmt, lead, K, device):
     import torch
-    if packed.shape != (*lead, K // 2):
-        raise ValueError(f"{names[0]} must be {(*lead, K // 2)}, got {tuple(packed.shape)}")
-    if scales.shape != (*lead, fp4_scale_pitch(K, fmt)):
-        raise ValueError(f"{names[1]} must be {(*lead, fp4_scale_pitch(K, fmt))}, got {tuple(scales.shape)}")
-    return (_ptr(packed, names[0], (torch.uint8,), device), _ptr(scales, names[1], (torch.uint8,), device))
+    u8 = (torch.uint8,)
+    pitch = (K // FP4_BLOCKS[fmt] + 15) // 16 * 16
+    if packed.shape != lead + (K // 2,) or scales.shape != lead + (pitch,):
+        raise ValueError(f"{names[0]} must be {lead + (K // 2,)} and {names[1]} {lead + (pitch,)}, got "
+                         f"{tuple(packed.shape)} and {tuple(scales.shape)}")
+    return _ptr(packed, names[0], u8, device), _ptr(scales, names[1], u8, device)
 
 
 def _check_global(t, name, device, numel=1):
