@@ -113,10 +113,10 @@ __device__ __forceinline__ void route_scan(uint32_t *v, int n, uint32_t *warp_su
 }
 
 // Vectors a lane and copy unit: 2 KB of a token with 16-byte vectors; with narrow ones more of
-// them, to keep as many bytes in flight.  In the one-launch form, few bytes spread over many
-// SMs: 512 bytes.
-template <int VB, bool kSmall>
-constexpr int kRouteUnit = VB == 16 ? (kSmall ? 1 : 4) : (kSmall ? 4 : 16);
+// them, to keep as many bytes in flight.  Few bytes (kFew) are spread over many SMs instead:
+// 512 bytes a unit.
+template <int VB, bool kFew>
+constexpr int kRouteUnit = VB == 16 ? (kFew ? 1 : 4) : (kFew ? 4 : 16);
 
 template <int VB>
 struct RouteVec;
@@ -161,7 +161,7 @@ __device__ __forceinline__ void route_copy(const DispatchParams &p, const int *r
 // count before the copy would need.  CTA 0 writes the maps.  Bound by its latency: 256
 // tokens of 2048 bf16 to 8 of 64 experts take 6.5 us (9.4 with 2 KB copy units, which only
 // 32 CTAs shared).
-template <int VB>
+template <int VB, bool kFew>
 __global__ void __launch_bounds__(kRouteThreads) gmm_dispatch_small_kernel(const __grid_constant__ DispatchParams p) {
   extern __shared__ uint32_t route_smem[];
   __shared__ uint32_t warp_sums[kRouteWarps];
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kRouteThreads) gmm_dispatch_small_kernel(const
   }
   if (p.tokens == nullptr) return;
   __syncthreads();
-  route_copy<VB, kRouteUnit<VB, true>>(p, row_s, 0, p.num_tokens, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
+  route_copy<VB, kRouteUnit<VB, kFew>>(p, row_s, 0, p.num_tokens, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
 }
 
 // Many slots, first launch: CTA c counts the experts of its chunk of tokens and leaves every
