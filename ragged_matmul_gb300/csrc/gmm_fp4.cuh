@@ -32,11 +32,13 @@
 //   warps 10..12  scales: the weight rows' block, and the tokens' two.
 //   warp 13       scheduler: decodes the CTA's tiles into a queue that every role reads.
 //
-// Measured: 32768 rows over 8 experts, K = 4096, N = 14336, nvfp4: 0.633 ms, 6.1 PFLOP/s.  The
-// MMAs alone would take 0.41 ms; what bounds it is shared memory and its load / store pipe (per
-// stage 31 KB written by the copies, 31 KB read by the MMAs, about 20 KB for the scales, 7 KB for
-// C), so a tile holds as many tokens as tensor memory allows (224 instead of 240: 0.693 ms).  2048
-// rows over 64 experts, K = 2048, N = 2816: 45 us with cold weights, 4.9 TB/s.
+// Measured: 32768 rows over 8 experts, K = 4096, N = 14336, nvfp4: 0.64 ms, 6.0 PFLOP/s.  What
+// bounds it is what enters an SM: 37 KB a stage (31 KB of values, 6 KB of scales), which without
+// the MMAs and the epilogue takes 0.518 ms (18.4 TB/s, 64 bytes a clock and SM; multicast to
+// clusters of 2, 4 or 8 does not raise that rate), with the epilogue 0.574 ms; the MMAs alone
+// 0.42 ms.  So a tile holds as many tokens as tensor memory allows beside a second accumulator
+// (224 instead of 240: 0.693 ms).  2048 rows over 64 experts, K = 2048, N = 2816: 45 us with cold
+// weights, 4.9 TB/s.
 //
 // Tiles are claimed by the pair as the grouped kernel's are (a static share where there are
 // few).  Every wait is bounded as in the grouped kernel.
