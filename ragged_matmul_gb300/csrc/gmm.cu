@@ -545,8 +545,8 @@ int launch_dispatch(gmm_ctx *h, gmm::DispatchParams &p, cudaStream_t stream) {
 template <class T, int VN, int kRows, int kUnits>
 void launch_grad(gmm_ctx *h, gmm::CombineParams &p, long long nvec, cudaStream_t stream) {
   // One warp a token when that fills the SMs (32 resident warps each; 24 for single elements,
-  // whose pieces are shorter: 1003 tokens of 1411 fp32 17.3 us with four warps a token, 18.8
-  // with eight), else more.
+  // whose pieces are shorter: 1003 tokens of 1411 fp32, top-6, 16.0 us with four warps a token,
+  // 16.5 with eight), else more.
   constexpr long long kFill = VN == 1 ? 24 : 32;
   const long long pieces = (nvec + 32 * kUnits - 1) / (32 * kUnits);
   int wpt = 1;
@@ -571,19 +571,35 @@ template <class T, int VN>
 int launch_combine(gmm_ctx *h, gmm::CombineParams &p, bool grad, cudaStream_t stream) {
   const long long nvec = p.row_bytes / static_cast<long long>(sizeof(T) * VN);
   if (grad) {
-    // Rows at a time by top_k, and as many vectors of each as the registers hold; of single
-    // elements more, for as many bytes.
-    constexpr bool kOne = VN == 1;
-    if (p.top_k == 1) launch_grad<T, VN, 1, (kOne ? 8 : 4)>(h, p, nvec, stream);
-    else if (p.top_k == 2) launch_grad<T, VN, 2, (kOne ? 8 : 2)>(h, p, nvec, stream);
-    else if (kOne || p.top_k <= 4) launch_grad<T, VN, 4, (kOne ? 2 : 1)>(h, p, nvec, stream);
-    else launch_grad<T, VN, 8, 1>(h, p, nvec, stream);
+    // Rows at a time by top_k, so that few of the unrolled rows are idle, and as many vectors of each
+    // as the registers hold; of single elements more, for as many bytes.  3, 5 and 6 rows (1500,
+    // 1000, 1000 tokens of 2047 bf16): 15.5, 14.0 and 16.7 us, with code for four rows 19.3, 19.3
+    // and 20.0.  In vectors top-5 and top-6 take three rows twice where there are few tokens (1000 of
+    // 2048 bf16, top-6: 11.1 us, 13.3 with eight), else all at once, for d_out is then read once
+    // (4096 of 2048 fp32: 69.5 us, 73.4 three by three).
+    if constexpr (VN == 1) {
+      if (p.top_k == 1) launch_grad<T, VN, 1, 8>(h, p, nvec, stream);
+      else if (p.top_k == 2) launch_grad<T, VN, 2, 8>(h, p, nvec, stream);
+      else if (p.top_k == 3) launch_grad<T, VN, 3, 4>(h, p, nvec, stream);
+      else if (p.top_k == 5 || p.top_k == 6) launch_grad<T, VN, 6, 2>(h, p, nvec, stream);
+      else launch_grad<T, VN, 4, 3>(h, p, nvec, stream);
+    } else {
+      const bool few = p.num_tokens < 16ll * h->num_sms;
+      if (p.top_k == 1) launch_grad<T, VN, 1, 4>(h, p, nvec, stream);
+      else if (p.top_k == 2) launch_grad<T, VN, 2, 2>(h, p, nvec, stream);
+      else if (p.top_k == 3 || (few && (p.top_k == 5 || p.top_k == 6))) launch_grad<T, VN, 3, 2>(h, p, nvec, stream);
+      else if (p.top_k == 4) launch_grad<T, VN, 4, 1>(h, p, nvec, stream);
+      else launch_grad<T, VN, 8, 1>(h, p, nvec, stream);
+    }
     return launch_status("launch of the combine gradient kernel");
   }
-  constexpr bool kOne = VN == 1;
-  if (p.top_k <= 2) return launch_sum<T, VN, 2, (kOne ? 1 : 2), (kOne ? 16 : 2)>(p, nvec, stream);
-  if (p.top_k <= 4) return launch_sum<T, VN, 4, 1, (kOne ? 8 : 2)>(p, nvec, stream);
-  return launch_sum<T, VN, 8, (kOne ? 1 : 2), (kOne ? 4 : 1)>(p, nvec, stream);
+  // As for the gradient; single elements in larger units, for as many bytes.  4096 tokens of 2048
+  // bf16, top-8: four rows of two vectors 25.7 us, eight of one 26.6; of 2047: 36.0 and 41.0.
+  // 1500 tokens, top-3: 4.2 and 6.2 us with code for three rows, 5.8 and 10.5 for eight.
+  constexpr int kUnits = VN == 1 ? 8 : 2;
+  if (p.top_k <= 2) return launch_sum<T, VN, 2, (VN == 1 ? 1 : 2), (VN == 1 ? 16 : 2)>(p, nvec, stream);
+  if (p.top_k == 3 || p.top_k == 5 || p.top_k == 6) return launch_sum<T, VN, 3, 1, kUnits>(p, nvec, stream);
+  return launch_sum<T, VN, 4, 1, kUnits>(p, nvec, stream);
 }
 
 // 16-byte vectors where every row starts on a 16-byte boundary, else single elements.

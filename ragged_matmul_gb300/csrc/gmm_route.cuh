@@ -455,8 +455,8 @@ constexpr int kCombineWarps = 8;
 
 // Bound by the rows' bytes.  A warp per (token, 32 kSeq kUnits vectors): its slots are read
 // once, a lane each, and the loads of kBatch rows of kUnits vectors are in flight together
-// (kBatch by top_k; fewer rows in larger units, and single elements, for rows that are not
-// 16-byte aligned, in larger ones still: top-2 with batches of 8 took twice as long).  At 64
+// (kBatch by top_k, so that few of the unrolled rows are idle: top-2 with batches of 8 took twice
+// as long; single elements, for rows that are not 16-byte aligned, in larger units).  At 64
 // registers a thread half of an SM's warps are resident, which keeps enough loads in flight
 // (with 100 registers and a quarter, 32768 rows of 8 KB to 4096 tokens took 73 us, now 48: 6.2 TB/s).
 template <class T, int VN, int kBatch, int kSeq, int kUnits>
@@ -515,7 +515,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 4) gmm_combine_kernel(cons
 // 32 kUnits-vector pieces in turn, kRows rows at a time, and join their dot products through
 // shared memory in warp order.  The loads of a piece's kUnits (kRows + 1) vectors are in flight
 // together.  16384 tokens of 8 KB, top-2: 101.5 us, 6.6 TB/s (118 with a third of the warps
-// resident and four rows' code for two).
+// resident and four rows' code for two); 1003 tokens of 1411 fp32, top-6: 16.0 us with six
+// rows' code, 17.5 with four's.
 template <class T, int VN, int kRows, int kUnits>
 __global__ void __launch_bounds__(32 * kCombineWarps, kRows == 8 ? 3 : 4)
     gmm_combine_grad_kernel(const __grid_constant__ CombineParams p) {

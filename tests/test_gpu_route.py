@@ -237,6 +237,58 @@ def test_combine_grad(dtype, T, k, width, weighted):
     assert torch.equal(again, d_rows)
 
 
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("width", [1, 2, 3, 62, 63, 64, 65, 66, 127, 129, 513, 2047, 4098])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_rows_on_any_two_bytes(dtype, width, shift):
+    """Rows of 2-byte elements whose words do not coincide: every parity of the source, the result
+    and the gradients, and nothing written beside them (exact values: integers, weights 1 and 2)."""
+    torch, binding = _mods()
+    rng = np.random.default_rng([width, shift])
+    dt, h = getattr(torch, dtype), handle(4)
+    for T, k in ((5, 1), (6, 2), (7, 3), (4, 7)):
+        sr = rng.permutation(T * k).astype(np.int32).reshape(T, k)
+        sr[rng.random((T, k)) < 0.2] = -1
+        srt = torch.from_numpy(sr).cuda()
+        w = rng.integers(1, 3, (T, k)).astype(np.float32)
+        n = T * k
+
+        def flat(count, at, fill=None):
+            """`count` elements `at` elements into a buffer, and the buffer."""
+            buf = torch.full((count + 8,), 99.0, dtype=dt, device="cuda")
+            view = buf[at:at + count]
+            if fill is not None:
+                view.copy_(fill)
+            return view, buf
+
+        ints = lambda *s: torch.from_numpy(rng.integers(-4, 5, s).astype(np.float32)).cuda()
+        rows = flat(n * width, shift, ints(n * width).to(dt))[0].view(n, width)
+        x = rows.double().cpu().numpy()
+        ww = np.where(sr >= 0, w, 0.0)
+        for at in (0, 1, 2, 3):
+            for pitch in (width, width + 1, width + 2):
+                out_v, out_b = flat((T - 1) * pitch + width, at)
+                out = out_v.as_strided((T, width), (pitch, 1))
+                binding.gmm_combine(h, out, rows, srt, torch.from_numpy(w).cuda())
+                want = torch.full_like(out_b, 99.0)
+                want[at:at + out_v.numel()].as_strided((T, width), (pitch, 1)).copy_(
+                    torch.from_numpy((ww[:, :, None] * x[np.maximum(sr, 0)]).sum(1)).cuda().to(dt))
+                assert torch.equal(out_b, want), (T, k, at, pitch)
+            g_v, _ = flat((T - 1) * (width + 1) + width, at, ints((T - 1) * (width + 1) + width).to(dt))
+            d_out = g_v.as_strided((T, width), (width + 1, 1))
+            g = d_out.double().cpu().numpy()
+            d_v, d_b = flat(n * width, (at + shift) % 3)
+            d_w = torch.full((T, k), 7.0, device="cuda")
+            binding.gmm_combine_grad(h, d_v.view(n, width), d_w, d_out, rows, srt, torch.from_numpy(w).cuda())
+            want = torch.full_like(d_b, 99.0)
+            wr = want[(at + shift) % 3:(at + shift) % 3 + n * width].view(n, width)
+            for t, j in zip(*np.nonzero(sr >= 0)):
+                wr[int(sr[t, j])] = torch.from_numpy(w[t, j] * g[t]).cuda().to(dt)
+            assert torch.equal(d_b, want), (T, k, at)
+            want_w = np.where(sr >= 0, (g[:, None, :] * x[np.maximum(sr, 0)]).sum(2), 0.0)
+            assert (d_w.cpu().numpy() == want_w).all(), (T, k, at)
+
+
 def test_gradient_against_differences():
     """The weighted sum is linear in the rows and in the weights, so a central difference of the
     forward call with step 1 is its derivative up to rounding: with L = <out, G> and every
