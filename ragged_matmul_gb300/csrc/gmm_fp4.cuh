@@ -184,9 +184,11 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
     tmem_relinquish_pair();
     tc_fence_before_sync();
   }
+  if (tid == 0) prefetch_tensormap(&p.w_map);
   __syncthreads();
+  cluster_arrive();   // the peer's barriers are initialised before anyone signals them
   build_schedule<G>(p, ctl, prefix, kF4Threads);
-  cluster_sync();   // the peer's barriers are initialised before anyone signals them
+  cluster_wait();
 
   if (blockIdx.x == 0 && tid == 0) {
     p.stats[1] = ctl.active;
@@ -204,7 +206,6 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
     uint8_t *slot = p.map_slots + static_cast<size_t>(blockIdx.x) * kMapSlotBytes;
     if (lane == 0) {
       const CUtensorMap *tok_maps = reinterpret_cast<const CUtensorMap *>(slot);
-      prefetch_tensormap(&p.w_map);
       const uint64_t pol_first = l2_policy_evict_first();
       const uint64_t pol_last = l2_policy_evict_last();
       const uint64_t pol_normal = l2_policy_evict_normal();
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
       acc ^= 1u;
       if (acc == 0) acc_phase ^= 1u;
     }
-    if (lane == 0) bulk_wait_all();
+    if (lane == 0) bulk_wait_read<0>();   // the staging buffers; the stores complete with the grid
   } else if (warp < static_cast<int>(kF4FirstScaleWarp + kF4ScaleWarps)) {
     // ------------------------------------------------------------ scales
     // Warp role 0: the CTA's 128 weight rows; 1 and 2: token rows 0 .. 127 and 128 .. 239.
@@ -552,26 +553,31 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
     // ------------------------------------------------------------ scheduler
     // The leader decodes the pair's tiles ahead of the roles (a search and loads of about a
     // microsecond, which in the MMA warp left the tensor cores idle at every tile) into both
-    // CTAs' queues and closes them with a tile of no rows; the peer tells it which entries
-    // its readers have taken.  With many tiles a pair claims them (after its first) from a
-    // counter, so that pairs which draw cheaper tiles take more; where group sizes are very
-    // uneven every second pair claims from the back of the tile order, so that the small
-    // groups' weights stream while the others run the large groups' arithmetic (as in the
-    // grouped kernel).
+    // CTAs' queues and closes them with a tile of no rows; the peer decodes the first one itself,
+    // which saves it a remote write's microsecond, and tells the leader which entries its readers
+    // have taken.  With many tiles a pair claims them (after its first) from a counter, so that
+    // pairs which draw cheaper tiles take more; where group sizes are very uneven every second
+    // pair claims from the back of the tile order, so that the small groups' weights stream while
+    // the others run the large groups' arithmetic (as in the grouped kernel).
     bool ok = true;
+    const bool dynamic = total >= kF4DynamicTiles * units;
+    const bool two_ended = dynamic && ctl.max_group_tiles >= kUnevenRatio * ctl.min_group_tiles;
+    const bool back = two_ended && (unit0 & 1u);
+    uint32_t t = two_ended ? (back ? total - 1u - unit0 / 2u : unit0 / 2u) : unit0;
+    Tile first{};
+    if (t < total) first = decode_tile<G>(t, prefix, p);
+    ctl.tq_info[0] = first;
+    mbar_arrive(smem_addr(&ctl.tq_full[0]));
     if (rank == 0) {
-      const bool dynamic = total >= kF4DynamicTiles * units;
-      const bool two_ended = dynamic && ctl.max_group_tiles >= kUnevenRatio * ctl.min_group_tiles;
-      const bool back = two_ended && (unit0 & 1u);
       const uint32_t backs = two_ended ? units / 2u : 0u, fronts = units - backs;   // first tiles, not claimed
       const uint32_t info1 = map_to_rank(smem_addr(&ctl.tq_info[0]), 1), full1 = map_to_rank(smem_addr(&ctl.tq_full[0]), 1);
-      uint32_t t = two_ended ? (back ? total - 1u - unit0 / 2u : unit0 / 2u) : unit0;
-      for (uint32_t pos = 0;; ++pos) {
+      for (uint32_t pos = 1; t < total; ++pos) {
+        t += units;   // the static share's next
         const uint32_t slot = pos % kF4Queue, parity = (pos / kF4Queue) & 1u;
         ok = wait_phase(smem_addr(&ctl.tq_empty[slot]), parity ^ 1u, abort) &&
              (pos < kF4Queue || wait_phase_cluster(smem_addr(&peer_free[slot]), parity ^ 1u, abort));
         if (!ok) break;
-        if (pos > 0 && dynamic) {   // claimed only now: no further ahead of its use than the queue is long
+        if (dynamic) {   // claimed only now: no further ahead of its use than the queue is long
           const unsigned long long old =
               atomicAdd(reinterpret_cast<unsigned long long *>(p.tile_counter), back ? (1ull << 32) : 1ull);
           const unsigned long long f = fronts + (old & 0xffffffffull), b = backs + (old >> 32);
@@ -586,8 +592,6 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
           st_shared_cluster_u32(info1 + slot * static_cast<uint32_t>(sizeof(Tile)) + 4u * i, xw[i]);
         mbar_arrive(smem_addr(&ctl.tq_full[slot]));
         mbar_arrive_cluster(full1 + slot * 8u);
-        if (t >= total) break;
-        t += units;   // the static share's next
       }
     } else {
       const uint32_t free0 = map_to_rank(smem_addr(&peer_free[0]), 0);
