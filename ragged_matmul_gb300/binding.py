@@ -424,54 +424,61 @@ def gmm_matmul_int4(h: Handle, c, a, b_packed, b_scales, group_size: int = 128, 
 
 # ---------------------------------------------------------------- tokens sorted by expert and back
 
-_ROW_TYPES = None
+_ROW_TYPES = _TENSOR = _I32 = _U8 = _F32 = _BF16 = None
 
 
 def _row_types():
-    """torch dtype -> GMM_DTYPE_*"""
-    global _ROW_TYPES
+    """torch dtype -> GMM_DTYPE_*; the first call also sets the other types that the calls below test
+    for (a statement that imports torch costs each of them as much as a tensor's test)."""
+    global _ROW_TYPES, _TENSOR, _I32, _U8, _F32, _BF16
     if _ROW_TYPES is None:
         import torch
+        _TENSOR, _I32, _U8 = torch.Tensor, (torch.int32,), (torch.uint8,)
+        _F32, _BF16 = (torch.float32,), (torch.bfloat16,)
         _ROW_TYPES = {torch.bfloat16: GMM_DTYPE_BF16, torch.float16: GMM_DTYPE_FP16, torch.float32: GMM_DTYPE_FP32}
     return _ROW_TYPES
 
 
+def _shaped(t, name, dtypes, device, shape):
+    """The pointer of a contiguous tensor of exactly this shape."""
+    try:
+        if t.shape == shape and t.get_device() == device and t.dtype in dtypes and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    p = _check(t, name, dtypes, device).value
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return p
+
+
 def _check_strided(t, name, dtypes, device, out=False):
     """A 2-D tensor of contiguous rows, any distance apart (an output's must not overlap):
-    its pointer and row stride in elements."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+    its pointer, row stride in elements and shape."""
+    if not isinstance(t, _TENSOR):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.get_device() != device:
         raise ValueError(f"{name} must live on cuda:{device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got {t.dim()}-D")
-    rows, width = t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got {len(shape)}-D")
+    rows, width = shape
     if t.is_contiguous():
-        return t.data_ptr(), width
+        return t.data_ptr(), width, shape
     stride = t.stride(0) if rows > 1 else width
     if (width > 1 and t.stride(1) != 1) or (out and stride < width):
         raise ValueError(f"{name} must have contiguous rows{' that do not overlap' if out else ''}, got strides {t.stride()}")
-    return t.data_ptr(), stride
+    return t.data_ptr(), stride, shape
 
 
 def _slots(t, name, device):
-    import torch
-    p = _ptr(t, name, (torch.int32,), device)
-    if t.dim() != 2 or t.shape[1] < 1:
+    p = _ptr(t, name, _I32, device)
+    shape = t.shape
+    if len(shape) != 2 or shape[1] < 1:
         raise ValueError(f"{name} must be [tokens, top_k]")
-    return p, t.shape[0], t.shape[1]
-
-
-def _slot_weights(t, name, shape, device):
-    import torch
-    if t is None:
-        return None
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be [tokens, top_k] = {tuple(shape)}, got {tuple(t.shape)}")
-    return _ptr(t, name, (torch.float32,), device)
+    return p, shape
 
 
 def gmm_dispatch(h: Handle, a_offsets, slot_rows, row_slots, slot_experts, rows=None, tokens=None, stream=None,
@@ -480,25 +487,25 @@ def gmm_dispatch(h: Handle, a_offsets, slot_rows, row_slots, slot_experts, rows=
     writes a_offsets [E + 1], slot_rows [tokens, top_k] and row_slots [tokens * top_k], and, when
     `rows` [tokens * top_k, width] and `tokens` [tokens, width] are given, copies each token to its
     rows (asynchronous).  The gradient of the copy is gmm_combine without weights."""
-    import torch
-    pe, T, k = _slots(slot_experts, "slot_experts", h.device)
-    po = _ptr(a_offsets, "a_offsets", _i32_types(), h.device, h.num_experts + 1)
-    psr, T2, k2 = _slots(slot_rows, "slot_rows", h.device)
-    prs = _ptr(row_slots, "row_slots", (torch.int32,), h.device)
-    if (T2, k2) != (T, k) or row_slots.numel() != T * k:
-        raise ValueError(f"slot_rows must be [{T}, {k}] and row_slots [{T * k}]")
+    types, dev = _row_types(), h.device
+    pe, shape = _slots(slot_experts, "slot_experts", dev)
+    T, k = shape
+    po = _ptr(a_offsets, "a_offsets", _i32_types(), dev, h.num_experts + 1)
+    psr = _shaped(slot_rows, "slot_rows", _I32, dev, shape)
+    prs = _ptr(row_slots, "row_slots", _I32, dev)
+    if row_slots.numel() != T * k:
+        raise ValueError(f"row_slots must hold {T * k} entries, got {row_slots.numel()}")
     if (rows is None) != (tokens is None):
         raise ValueError("rows and tokens go together")
     pr = pt = None
     stride, width, dtype = 0, 1, GMM_DTYPE_BF16
     if tokens is not None:
-        types = _row_types()
-        pt, stride = _check_strided(tokens, "tokens", types, h.device)
-        width, dtype = tokens.shape[1], types[tokens.dtype]
-        pr = _ptr(rows, "rows", (tokens.dtype,), h.device)
-        if tokens.shape[0] != T or tuple(rows.shape) != (T * k, width):
-            raise ValueError(f"tokens must be [{T}, width] and rows [{T * k}, width], got {tuple(tokens.shape)} and "
-                             f"{tuple(rows.shape)}")
+        pt, stride, (n, width) = _check_strided(tokens, "tokens", types, dev)
+        if n != T:
+            raise ValueError(f"tokens must be [{T}, width], got {tuple(tokens.shape)}")
+        element = tokens.dtype
+        dtype = types[element]
+        pr = _shaped(rows, "rows", (element,), dev, (T * k, width))
     rc = load_library().gmm_dispatch(h.ptr, po, psr, prs, pr, pe, pt, stride, T, k, width, dtype,
                                      stream_handle(h.device, stream))
     if check and rc != GMM_OK:
@@ -509,16 +516,19 @@ def gmm_dispatch(h: Handle, a_offsets, slot_rows, row_slots, slot_experts, rows=
 def gmm_combine(h: Handle, out, rows, slot_rows, weights=None, stream=None, check: bool = True) -> int:
     """out[t] = sum_j weights[t, j] * rows[slot_rows[t, j]] (negative slot_rows: nothing); weights fp32
     [tokens, top_k], None: ones.  out [tokens, width] and rows [num_rows, width] of one dtype."""
-    types = _row_types()
-    psr, T, k = _slots(slot_rows, "slot_rows", h.device)
-    po, stride = _check_strided(out, "out", types, h.device, out=True)
-    pr = _ptr(rows, "rows", (out.dtype,), h.device)
-    if rows.dim() != 2 or out.shape[0] != T or out.shape[1] != rows.shape[1]:
+    types, dev = _row_types(), h.device
+    psr, shape = _slots(slot_rows, "slot_rows", dev)
+    T, k = shape
+    po, stride, (n, width) = _check_strided(out, "out", types, dev, out=True)
+    element = out.dtype
+    pr = _ptr(rows, "rows", (element,), dev)
+    row_shape = rows.shape
+    if len(row_shape) != 2 or n != T or row_shape[1] != width:
         raise ValueError(f"out must be [{T}, width] and rows [num_rows, width], got {tuple(out.shape)} and "
                          f"{tuple(rows.shape)}")
-    pw = _slot_weights(weights, "weights", (T, k), h.device)
-    rc = load_library().gmm_combine(h.ptr, po, stride, pr, rows.shape[0], psr, pw, T, k, out.shape[1],
-                                    types[out.dtype], stream_handle(h.device, stream))
+    pw = None if weights is None else _shaped(weights, "weights", _F32, dev, shape)
+    rc = load_library().gmm_combine(h.ptr, po, stride, pr, row_shape[0], psr, pw, T, k, width, types[element],
+                                    stream_handle(dev, stream))
     if check and rc != GMM_OK:
         raise GmmError(rc, "gmm_combine")
     return rc
@@ -529,24 +539,25 @@ def gmm_combine_grad(h: Handle, d_rows, d_weights, d_out, rows, slot_rows, weigh
     """The gradient of gmm_combine: d_rows[slot_rows[t, j]] = weights[t, j] * d_out[t] (rows that no slot
     names stay untouched) and d_weights[t, j] = <d_out[t], rows[slot_rows[t, j]]> in fp32 (None: not
     computed, and `rows` may be None)."""
-    types = _row_types()
-    psr, T, k = _slots(slot_rows, "slot_rows", h.device)
-    pg, stride = _check_strided(d_out, "d_out", types, h.device)
-    pd = _ptr(d_rows, "d_rows", (d_out.dtype,), h.device)
-    if d_rows.dim() != 2 or d_out.shape[0] != T or d_out.shape[1] != d_rows.shape[1]:
+    types, dev = _row_types(), h.device
+    psr, shape = _slots(slot_rows, "slot_rows", dev)
+    T, k = shape
+    pg, stride, (n, width) = _check_strided(d_out, "d_out", types, dev)
+    element = d_out.dtype
+    pd = _ptr(d_rows, "d_rows", (element,), dev)
+    row_shape = d_rows.shape
+    if len(row_shape) != 2 or n != T or row_shape[1] != width:
         raise ValueError(f"d_out must be [{T}, width] and d_rows [num_rows, width], got {tuple(d_out.shape)} and "
                          f"{tuple(d_rows.shape)}")
     pr = None
     if rows is not None:
-        pr = _ptr(rows, "rows", (d_out.dtype,), h.device)
-        if tuple(rows.shape) != tuple(d_rows.shape):
-            raise ValueError("rows and d_rows must have the same shape")
+        pr = _shaped(rows, "rows", (element,), dev, row_shape)
     elif d_weights is not None:
         raise ValueError("d_weights needs rows")
-    pw = _slot_weights(weights, "weights", (T, k), h.device)
-    pdw = _slot_weights(d_weights, "d_weights", (T, k), h.device)
-    rc = load_library().gmm_combine_grad(h.ptr, pd, pdw, pg, stride, pr, d_rows.shape[0], psr, pw, T, k,
-                                         d_out.shape[1], types[d_out.dtype], stream_handle(h.device, stream))
+    pw = None if weights is None else _shaped(weights, "weights", _F32, dev, shape)
+    pdw = None if d_weights is None else _shaped(d_weights, "d_weights", _F32, dev, shape)
+    rc = load_library().gmm_combine_grad(h.ptr, pd, pdw, pg, stride, pr, row_shape[0], psr, pw, T, k, width,
+                                         types[element], stream_handle(dev, stream))
     if check and rc != GMM_OK:
         raise GmmError(rc, "gmm_combine_grad")
     return rc
@@ -566,23 +577,17 @@ def fp4_scale_pitch(K: int, fmt="nvfp4") -> int:
     return (K // FP4_BLOCKS[_fp4_format(fmt)] + 15) // 16 * 16
 
 
-def _check_fp4(packed, scales, names, fmt, lead, K, device):
-    import torch
-    u8 = (torch.uint8,)
-    pitch = (K // FP4_BLOCKS[fmt] + 15) // 16 * 16
-    if packed.shape != lead + (K // 2,) or scales.shape != lead + (pitch,):
-        raise ValueError(f"{names[0]} must be {lead + (K // 2,)} and {names[1]} {lead + (pitch,)}, got "
-                         f"{tuple(packed.shape)} and {tuple(scales.shape)}")
-    return _ptr(packed, names[0], u8, device), _ptr(scales, names[1], u8, device)
+def _check_fp4(packed, scales, names, fmt, rows, K, device):
+    """Pointers of packed values [rows, K / 2] and their scales [rows, pitch]."""
+    return (_shaped(packed, names[0], _U8, device, (rows, K // 2)),
+            _shaped(scales, names[1], _U8, device, (rows, (K // FP4_BLOCKS[fmt] + 15) // 16 * 16)))
 
 
 def _check_global(t, name, device, numel=1):
-    import torch
-    if t is None:
-        return None
+    p = _ptr(t, name, _F32, device)
     if t.numel() != numel:
         raise ValueError(f"{name} must hold {numel} value(s), got {t.numel()}")
-    return _ptr(t, name, (torch.float32,), device)
+    return p
 
 
 def gmm_quantize_fp4(h: Handle, packed, scales, x, fmt="nvfp4", row_slots=None, top_k: int = 1, global_scale=None,
@@ -590,20 +595,17 @@ def gmm_quantize_fp4(h: Handle, packed, scales, x, fmt="nvfp4", row_slots=None, 
     """Quantise x [src_rows, K] to e2m1 with block scales: packed uint8 [rows, K / 2], scales uint8
     [rows, fp4_scale_pitch(K, fmt)].  With row_slots (int32 [rows], gmm_dispatch's) row r is quantised
     from x[row_slots[r] // top_k]; a negative entry leaves it untouched."""
-    import torch
+    types, dev = _row_types(), h.device
     f = _fp4_format(fmt)
-    types = _row_types()
-    px, stride = _check_strided(x, "x", types, h.device)
-    K = x.shape[1]
-    ps = None
-    rows = x.shape[0]
+    px, stride, (src_rows, K) = _check_strided(x, "x", types, dev)
+    ps, rows = None, src_rows
     if row_slots is not None:
-        ps = _ptr(row_slots, "row_slots", (torch.int32,), h.device)
+        ps = _ptr(row_slots, "row_slots", _I32, dev)
         rows = row_slots.numel()
-    pp, psc = _check_fp4(packed, scales, ("packed", "scales"), f, (rows,), K, h.device)
-    pg = _check_global(global_scale, "global_scale", h.device)
-    rc = load_library().gmm_quantize_fp4(h.ptr, pp, psc, px, stride, x.shape[0], ps, int(top_k), pg, rows, K,
-                                         types[x.dtype], f, stream_handle(h.device, stream))
+    pp, psc = _check_fp4(packed, scales, ("packed", "scales"), f, rows, K, dev)
+    pg = None if global_scale is None else _check_global(global_scale, "global_scale", dev)
+    rc = load_library().gmm_quantize_fp4(h.ptr, pp, psc, px, stride, src_rows, ps, int(top_k), pg, rows, K,
+                                         types[x.dtype], f, stream_handle(dev, stream))
     if check and rc != GMM_OK:
         raise GmmError(rc, "gmm_quantize_fp4")
     return rc
@@ -612,12 +614,11 @@ def gmm_quantize_fp4(h: Handle, packed, scales, x, fmt="nvfp4", row_slots=None, 
 def gmm_dequantize_fp4(h: Handle, y, packed, scales, fmt="nvfp4", global_scale=None, stream=None,
                        check: bool = True) -> int:
     """y [rows, K] (bf16, fp16 or fp32) = the values that packed and scales stand for."""
+    types, dev = _row_types(), h.device
     f = _fp4_format(fmt)
-    types = _row_types()
-    py, stride = _check_strided(y, "y", types, h.device, out=True)
-    rows, K = y.shape
-    pp, psc = _check_fp4(packed, scales, ("packed", "scales"), f, (rows,), K, h.device)
-    pg = _check_global(global_scale, "global_scale", h.device)
+    py, stride, (rows, K) = _check_strided(y, "y", types, dev, out=True)
+    pp, psc = _check_fp4(packed, scales, ("packed", "scales"), f, rows, K, dev)
+    pg = None if global_scale is None else _check_global(global_scale, "global_scale", dev)
     rc = load_library().gmm_dequantize_fp4(h.ptr, py, stride, pp, psc, pg, rows, K, types[y.dtype], f,
                                            stream_handle(h.device, stream))
     if check and rc != GMM_OK:
@@ -631,26 +632,30 @@ def gmm_run_fp4(h: Handle, c, a, a_offsets, b, expert_ids, expert_usage_stats, a
     """Grouped GEMM on microscaled 4-bit operands: a uint8 [rows, K / 2] with a_scales [rows, pitch],
     b uint8 [E, N, K / 2] with b_scales [E, N, pitch] (pitch = fp4_scale_pitch(K, fmt)); a_global one
     fp32 value, b_global fp32 [E]; then the optional epilogue."""
-    import torch
-    f = _fp4_format(fmt)
-    if a.dim() != 2 or b.dim() != 3 or c.dim() != 2:
-        raise ValueError("a must be [rows, K / 2], b [E, N, K / 2], c [rows, N]")
-    E, N, KB = b.shape
-    rows, K = a.shape[0], 2 * KB
-    if a.shape[1] != KB or c.shape[1] != N or c.shape[0] != rows or E != h.num_experts:
-        raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, c {tuple(c.shape)}, "
-                         f"handle E={h.num_experts}")
-    pc = _ptr(c, "c", (torch.bfloat16,), h.device)
-    pa, pas = _check_fp4(a, a_scales, ("a", "a_scales"), f, (rows,), K, h.device)
-    pb, pbs = _check_fp4(b, b_scales, ("b", "b_scales"), f, (E, N), K, h.device)
-    pga = _check_global(a_global, "a_global", h.device)
-    pgb = _check_global(b_global, "b_global", h.device, E)
+    _row_types()
+    f, dev = _fp4_format(fmt), h.device
+    pb = _ptr(b, "b", _U8, dev)
+    shape = b.shape
+    if len(shape) != 3 or shape[0] != h.num_experts:
+        raise ValueError(f"b must be [{h.num_experts}, N, K / 2], got {tuple(shape)}")
+    E, N, KB = shape
+    K = 2 * KB
+    pitch = (K // FP4_BLOCKS[f] + 15) // 16 * 16
+    if a.dim() != 2:
+        raise ValueError(f"a must be [rows, K / 2], got {tuple(a.shape)}")
+    rows = a.shape[0]
+    pa = _shaped(a, "a", _U8, dev, (rows, KB))
+    pc = _shaped(c, "c", _BF16, dev, (rows, N))
+    pas = _shaped(a_scales, "a_scales", _U8, dev, (rows, pitch))
+    pbs = _shaped(b_scales, "b_scales", _U8, dev, (E, N, pitch))
+    pga = None if a_global is None else _check_global(a_global, "a_global", dev)
+    pgb = None if b_global is None else _check_global(b_global, "b_global", dev, E)
     po, pi, ps, G = _routing_args(h, a_offsets, expert_ids, expert_usage_stats)
     epi = None
     if bias is not None or row_scale is not None or activation:
         epi = ctypes.byref(_epilogue(h, rows, N, bias, row_scale, activation))
     rc = load_library().gmm_run_fp4(h.ptr, pc, pa, po, pb, pi, ps, G, N, K, pas, pbs, f, pga, pgb, epi,
-                                    stream_handle(h.device, stream))
+                                    stream_handle(dev, stream))
     if check and rc != GMM_OK:
         raise GmmError(rc, "gmm_run_fp4")
     return rc
