@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
                   }
                   fence_async_smem();   // these writes, before the tensor-memory copies read them
                   __syncwarp();
-                  if (lane == 0) mbar_arrive_remote(full0 + rt.slot * 8u);
+                  if (lane == 0) mbar_arrive_cluster_shared(full0 + rt.slot * 8u);
                   rt.next(ST);
                 }
               }

@@ -498,14 +498,16 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// Arrive, possibly on another CTA's mbarrier, ordering this thread's earlier writes for
-// readers in its own CTA (release at CTA scope).  For data that a pair MMA or a tensor-memory
-// copy reads through the async proxy of the CTA that wrote it, after fence.proxy.async: the
-// leader's instruction makes each CTA's tensor core read its own shared memory, and no
-// generic read crosses CTAs.  A release at cluster scope waits for every memory operation of
-// the thread, about 0.7 us here.
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// Arrive on an mbarrier that may live in another CTA of the cluster, ordering the writes to this
+// CTA's shared memory before it (this thread's, and those that a warp or block barrier ordered
+// before) for the threads of the cluster that acquire the phase.  The fence is restricted to
+// shared memory: a release at cluster scope without the restriction also waits for the accesses to
+// global memory, about a microsecond here.
+__device__ __forceinline__ void mbar_arrive_cluster_shared(uint32_t cluster_addr) {
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+      : "memory");
 }
 
 __device__ __forceinline__ bool mbar_test_wait_cluster(uint32_t bar, uint32_t parity) {
