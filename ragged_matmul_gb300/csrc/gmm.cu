@@ -1029,6 +1029,14 @@ int gmm_dispatch(gmm_handle_t h, uint32_t *a_offsets, int32_t *slot_rows, int32_
                          !aligned_to(row_slots, 4) || !aligned_to(slot_experts, 4)))
     return GMM_ERR_INVALID_ARG;
   if (h->num_experts > gmm::kRouteMaxExperts) return GMM_ERR_UNSUPPORTED;
+  if (num_tokens == 0) {   // nothing to sort: every expert has no rows
+    DeviceGuard guard(h->device);
+    const cudaError_t err = cudaMemsetAsync(a_offsets, 0, (static_cast<size_t>(h->num_experts) + 1) * 4, stream);
+    if (err == cudaSuccess) return GMM_OK;
+    debug_report("cudaMemsetAsync", static_cast<int>(err), cudaGetErrorString(err));
+    cudaGetLastError();
+    return GMM_ERR_CUDA;
+  }
   gmm::DispatchParams p;
   std::memset(&p, 0, sizeof(p));
   p.slot_experts = slot_experts;
