@@ -241,7 +241,7 @@ int gmm_run_fp8(gmm_handle_t h, void *c, const void *a, const uint32_t *a_offset
  * num_tokens == 0 writes a_offsets only.
  * Errors (nothing is launched): GMM_ERR_INVALID_ARG (NULL or misaligned for its element
  * type, negative size, unknown dtype, only one of rows and tokens), GMM_ERR_UNSUPPORTED
- * (top_k > 32, more than 2^30 slots, more than 4096 experts), GMM_ERR_CUDA.
+ * (top_k > 32, more than 2^30 slots, width > 2^31 - 4096, more than 4096 experts), GMM_ERR_CUDA.
  */
 int gmm_dispatch(gmm_handle_t h, uint32_t *a_offsets, int32_t *slot_rows, int32_t *row_slots, void *rows,
                  const int32_t *slot_experts, const void *tokens, long long tokens_stride, int num_tokens, int top_k,

@@ -481,6 +481,7 @@ int check_rows(gmm_ctx *h, int num_tokens, int top_k, int width, int dtype, long
   if (!h || num_tokens < 0 || top_k < 1 || width < 1 || !dtype_bytes(dtype)) return GMM_ERR_INVALID_ARG;
   if (stride < 0) return GMM_ERR_INVALID_ARG;
   if (top_k > gmm::kRouteMaxTopK || static_cast<long long>(num_tokens) * top_k > (1ll << 30)) return GMM_ERR_UNSUPPORTED;
+  if (width > gmm::kRouteMaxWidth) return GMM_ERR_UNSUPPORTED;
   return GMM_OK;
 }
 

@@ -29,6 +29,7 @@ constexpr uint32_t kStatusBadSlot = 16u;   // a slot_rows / row_slots value outs
 constexpr int kRouteThreads = 512;
 constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kRouteMaxTopK = 32;          // a token's slots are held one per lane
+constexpr int kRouteMaxWidth = 0x7fffffff - 4095;   // columns are counted in 32 bits, by steps of up to 2048 past the last one
 constexpr int kRouteSmallSlots = 4096;     // up to here (and kRouteSmallExperts) one launch sorts and copies
 constexpr int kRouteSmallExperts = 1024;
 constexpr int kRouteMaxExperts = 4096;     // one group per expert: the grouped kernels' limit

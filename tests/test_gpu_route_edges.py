@@ -33,3 +33,19 @@ def test_sort_no_tokens_writes_the_offsets(E, copy):
     torch.cuda.synchronize()
     assert (off[: E + 1] == 0).all() and (off[E + 1:] == -7).all()
     binding.gmm_destroy(h)
+
+
+@pytest.mark.parametrize("dtype", [0, 1, 2])
+def test_rows_wider_than_the_column_count_are_refused(dtype):
+    """Widths whose column numbers would pass 31 bits are refused before any launch."""
+    torch, binding = _mods()
+    lib, h = binding.load_library(), binding.gmm_create(2, 0)
+    buf = torch.full((64,), 7, dtype=torch.int32, device="cuda")
+    p, stream = buf.data_ptr(), binding.stream_handle(0)
+    for width in ((1 << 31) - 4095, (1 << 31) - 1):
+        assert lib.gmm_dispatch(h.ptr, p, p, p, p, p, p, 0, 1, 1, width, dtype, stream) == binding.GMM_ERR_UNSUPPORTED
+        assert lib.gmm_combine(h.ptr, p, width, p, 1, p, None, 1, 1, width, dtype, stream) == binding.GMM_ERR_UNSUPPORTED
+        assert lib.gmm_combine_grad(h.ptr, p, p, p, 0, p, 1, p, None, 1, 1, width, dtype, stream) \
+            == binding.GMM_ERR_UNSUPPORTED
+    assert binding.gmm_query_status(h) == binding.GMM_OK and (buf == 7).all()
+    binding.gmm_destroy(h)
