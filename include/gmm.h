@@ -216,7 +216,8 @@ int gmm_run_fp8(gmm_handle_t h, void *c, const void *a, const uint32_t *a_offset
  * s = t * top_k + j is its j-th.  Rows (the grouped calls' A and C) hold one slot each, all
  * slots of expert 0 first, then expert 1, ..., each expert's in ascending slot order.
  * The calls below are asynchronous on `stream`, allocate nothing, can be captured in a CUDA
- * graph, and give the same bits every time.  Element types of the moved rows:
+ * graph, and give the same bits every time (gmm_combine_grad for distinct rows, which it
+ * requires).  Element types of the moved rows:
  */
 #define GMM_DTYPE_BF16 0
 #define GMM_DTYPE_FP16 1
@@ -266,9 +267,13 @@ int gmm_combine(gmm_handle_t h, void *out, long long out_stride, const void *row
  *     d_rows[slot_rows[t, j], :] = weights[t, j] * d_out[t, :]
  *     d_weights[t, j] = sum_n d_out[t, n] * rows[slot_rows[t, j], n]     (0 for a dropped slot)
  *   d_rows: [num_rows, width], contiguous; rows that no slot names stay untouched;
+ *   slot_rows: the rows that it names (those in 0 .. num_rows - 1) must be distinct, as
+ *   gmm_dispatch's are, also where a token names an expert twice.  This is not checked: a
+ *   row that several slots name receives their products element by element in no particular
+ *   order, not the sum (gmm_combine itself may name a row more than once);
  *   d_weights: fp32 [num_tokens, top_k], or NULL (rows may then be NULL too);
  *   d_out: [num_tokens, width], rows d_out_stride elements apart (0: one row for all);
- *   rows, slot_rows, weights: as gmm_combine took them.
+ *   rows, weights: as gmm_combine took them.
  * Products and sums in fp32 (each element of d_rows rounded once).  Errors: as gmm_combine.
  */
 int gmm_combine_grad(gmm_handle_t h, void *d_rows, float *d_weights, const void *d_out, long long d_out_stride,

@@ -538,7 +538,8 @@ def gmm_combine_grad(h: Handle, d_rows, d_weights, d_out, rows, slot_rows, weigh
                      check: bool = True) -> int:
     """The gradient of gmm_combine: d_rows[slot_rows[t, j]] = weights[t, j] * d_out[t] (rows that no slot
     names stay untouched) and d_weights[t, j] = <d_out[t], rows[slot_rows[t, j]]> in fp32 (None: not
-    computed, and `rows` may be None)."""
+    computed, and `rows` may be None).  The rows that slot_rows names must be distinct, as
+    gmm_dispatch's are (not checked): the products of slots that share a row are not summed."""
     types, dev = _row_types(), h.device
     psr, shape = _slots(slot_rows, "slot_rows", dev)
     T, k = shape

@@ -10,7 +10,8 @@
 //   combine       out[t, :] = sum_j w[t, j] * rows[slot_rows[t, j], :]
 //                 (w = 1: the gradient of dispatch's copy).
 //   combine_grad  d_rows[slot_rows[t, j], :] = w[t, j] * d_out[t, :],
-//                 d_w[t, j] = < d_out[t, :], rows[slot_rows[t, j], :] >.
+//                 d_w[t, j] = < d_out[t, :], rows[slot_rows[t, j], :] >;
+//                 the caller's named rows are distinct (dispatch's are), so each has one writer.
 // Every sum has a fixed order (j ascending; a dot product per lane, then a fixed tree),
 // no result depends on the order of atomics.
 #pragma once

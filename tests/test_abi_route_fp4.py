@@ -52,3 +52,14 @@ def test_tensors_on_another_device_are_refused():
             call()
     with pytest.raises(TypeError):
         binding.gmm_combine(h, x, x, [1.0])
+
+
+def test_the_gradient_states_that_its_rows_are_distinct():
+    """Each row of d_rows has one writer only if no two slots name it: a condition of the call that the
+    header and the binding both state."""
+    import os
+    with open(os.path.join(os.path.dirname(gbuild.PKG_DIR), "include", "gmm.h")) as f:
+        header = f.read()
+    comment = header[header.index(" * The gradient of gmm_combine:"):header.index("int gmm_combine_grad(")]
+    for text in (comment, binding.gmm_combine_grad.__doc__):
+        assert "must be distinct" in text and "not checked" in text
