@@ -85,6 +85,9 @@ int gmm_create(gmm_handle_t *out, int num_experts, int device);
  * N and K: multiples of 8 (16-byte rows, a TMA requirement), both >= 8.
  * c, a, b: 16-byte aligned.  num_groups: 0 .. 4096.
  * With num_groups == 0 only expert_usage_stats[1] = 0 is written (expert_ids may then be NULL).
+ * A call without rows (a batch that gave this device no tokens) has c and a both NULL, as
+ * an empty tensor's pointer is: all its groups are empty, a_offsets is not read, and only
+ * expert_usage_stats[1] is written.  The other grouped calls of a handle take it too.
  * Errors (nothing is launched): GMM_ERR_INVALID_ARG, GMM_ERR_UNSUPPORTED,
  *         GMM_ERR_CUDA (tensor-map encoding or launch failed).
  */
@@ -195,7 +198,8 @@ int gmm_run_planes(gmm_handle_t h, void *c, const void *a, const uint32_t *a_off
  * for the rows and groups of gmm_run, a and b e4m3 (1 sign, 4 exponent bits with
  * bias 7, 3 mantissa bits), sums in fp32.  Then the optional epilogue.
  *   a: e4m3 bytes [rows, K] (16-byte aligned); b: e4m3 bytes [num_experts, N, K]
- *   (16-byte aligned); input_scale: fp32 [ceil(rows / gm), ceil(K / gk)];
+ *   (16-byte aligned); input_scale: fp32 [ceil(rows / gm), ceil(K / gk)] (without rows it
+ *   may be NULL);
  *   weight_scale: fp32 [num_experts, ceil(N / gn), ceil(K / gk)] (both row-major,
  *   4-byte aligned, read only for active groups); c and the rest as gmm_run.
  * Requirements: those of gmm_run with K a multiple of 16 (an e4m3 row is K bytes, a
@@ -334,7 +338,7 @@ int gmm_dequantize_fp4(gmm_handle_t h, void *y, long long y_stride, const void *
  *   aligned, both operands of `format`; a_global: fp32, one value, b_global: fp32
  *   [num_experts], each NULL for ones; c and the rest as gmm_run.
  * Requirements: those of gmm_run with K a multiple of 32.  Padding bytes of the scales are
- * not used.  With num_groups == 0, c, a and a_scales may be NULL.
+ * not used.  With num_groups == 0 or without rows, c, a and a_scales may be NULL.
  * Errors: as gmm_run_ex, plus GMM_ERR_INVALID_ARG for an unknown format and NULL or
  * misaligned scales, GMM_ERR_UNSUPPORTED where the device cannot run the CTA-pair kernel.
  */

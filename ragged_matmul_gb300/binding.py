@@ -213,6 +213,11 @@ def _i32_types():
     return _I32_TYPES
 
 
+def _no_rows(rows, pc, pa):
+    """Pointers of c and a: both NULL, the library's call without rows, where one of two empty tensors has none."""
+    return (pc, pa) if rows or (pc and pa) else (None, None)
+
+
 def _routing_args(h, a_offsets, expert_ids, stats):
     G = expert_ids.numel()
     i32 = _i32_types()
@@ -254,8 +259,7 @@ def gmm_run_ex(h: Handle, c, a, a_offsets, b, expert_ids, expert_usage_stats, bi
         raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, c {tuple(c.shape)}, "
                          f"handle E={h.num_experts}")
     bf = (torch.bfloat16,)
-    pc = _check(c, "c", bf, h.device)
-    pa = _check(a, "a", bf, h.device)
+    pc, pa = _no_rows(c.shape[0], _check(c, "c", bf, h.device), _check(a, "a", bf, h.device))
     pb = _check(b, "b", bf, h.device)
     po, pi, ps, G = _routing_args(h, a_offsets, expert_ids, expert_usage_stats)
     lib = load_library()
@@ -290,8 +294,7 @@ def gmm_run_int4_ex(h: Handle, c, a, a_offsets, b_packed, b_scales, expert_ids, 
             or group_size <= 0 or tuple(b_scales.shape) != (E, N, K // group_size)):
         raise ValueError("shape mismatch between a, b_packed, b_scales, c")
     bf = (torch.bfloat16,)
-    pc = _check(c, "c", bf, h.device)
-    pa = _check(a, "a", bf, h.device)
+    pc, pa = _no_rows(c.shape[0], _check(c, "c", bf, h.device), _check(a, "a", bf, h.device))
     pq = _check(b_packed, "b_packed", _i32_types(), h.device)
     psc = _check(b_scales, "b_scales", bf, h.device)
     po, pi, ps, G = _routing_args(h, a_offsets, expert_ids, expert_usage_stats)
@@ -323,8 +326,7 @@ def gmm_run_planes(h: Handle, c, a, a_offsets, b, expert_ids, expert_usage_stats
         raise ValueError(f"shape mismatch: a {tuple(a.shape)} (needs {planes} planes of {c.shape[0]} rows), "
                          f"b {tuple(b.shape)}, c {tuple(c.shape)}, handle E={h.num_experts}")
     bf = (torch.bfloat16,)
-    pc = _check(c, "c", bf, h.device)
-    pa = _check(a, "a", bf, h.device)
+    pc, pa = _no_rows(c.shape[0], _check(c, "c", bf, h.device), _check(a, "a", bf, h.device))
     pb = _check(b, "b", bf, h.device)
     po, pi, ps, G = _routing_args(h, a_offsets, expert_ids, expert_usage_stats)
     splits = (ctypes.c_int * 2)(s0, s1)
@@ -365,8 +367,7 @@ def gmm_run_fp8(h: Handle, c, a, a_offsets, b, expert_ids, expert_usage_stats, i
         raise ValueError(f"input_scale needs ceil(rows / gm) * ceil(K / gk) = {-(-rows // gm) * nkb} entries")
     if gn > 0 and (weight_scale.shape[0] != E or weight_scale.numel() != E * -(-N // gn) * nkb):
         raise ValueError(f"weight_scale must be [E, ceil(N / gn), ceil(K / gk)] = [{E}, {-(-N // gn)}, {nkb}]")
-    pc = _check(c, "c", (torch.bfloat16,), h.device)
-    pa = _check(a, "a", _fp8_types(), h.device)
+    pc, pa = _no_rows(rows, _check(c, "c", (torch.bfloat16,), h.device), _check(a, "a", _fp8_types(), h.device))
     pb = _check(b, "b", _fp8_types(), h.device)
     pis = _check(input_scale, "input_scale", (torch.float32,), h.device)
     pws = _check(weight_scale, "weight_scale", (torch.float32,), h.device)
@@ -645,8 +646,7 @@ def gmm_run_fp4(h: Handle, c, a, a_offsets, b, expert_ids, expert_usage_stats, a
     if a.dim() != 2:
         raise ValueError(f"a must be [rows, K / 2], got {tuple(a.shape)}")
     rows = a.shape[0]
-    pa = _shaped(a, "a", _U8, dev, (rows, KB))
-    pc = _shaped(c, "c", _BF16, dev, (rows, N))
+    pc, pa = _no_rows(rows, _shaped(c, "c", _BF16, dev, (rows, N)), _shaped(a, "a", _U8, dev, (rows, KB)))
     pas = _shaped(a_scales, "a_scales", _U8, dev, (rows, pitch))
     pbs = _shaped(b_scales, "b_scales", _U8, dev, (E, N, pitch))
     pga = None if a_global is None else _check_global(a_global, "a_global", dev)

@@ -29,7 +29,8 @@ using gmm::GmmParams;
 // Workspace layout: a 256-byte block with the status word at byte 0, the 64-bit
 // tile-claim word (front count | back count << 32) at byte 64 and the finished-CTA
 // counter at byte 72 (all zero between launches), the dense call's routing at 128 and
-// its usage stats at 144; then one slot of tensor maps per CTA.
+// its usage stats at 144; then one slot of tensor maps per CTA, the zero offsets of calls
+// without rows and the chunk counts of gmm_dispatch.
 constexpr size_t kStatusBytes = 256;
 constexpr size_t kTileCounterOffset = 64;
 constexpr size_t kDenseRoutingOffset = 128;   // gmm_matmul_int4: a_offsets {0, M} and expert id 0
@@ -87,8 +88,9 @@ struct gmm_ctx {
   bool debug = false;             // GMM_DEBUG was set when the handle was created
   int use_pairs = 1;              // bf16 path: 1 = CTA-pair kernels (cta_group::2), 0 = one CTA per tile
   int use_pairs_int4 = 1;         // 4-bit path: the same
-  uint8_t *ws = nullptr;          // [status word | per-CTA tensor-map slots | chunk counts]
+  uint8_t *ws = nullptr;          // [status word | per-CTA tensor-map slots | zero offsets | chunk counts]
   size_t ws_bytes = 0;
+  const uint32_t *zero_offsets = nullptr;   // in ws: a_offsets of a call without rows, never written
   uint32_t *route_counts = nullptr;   // in ws; null with more experts than gmm_dispatch takes
   PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   PFN_cuMemsetD32Async_v3020 memset32 = nullptr;   // value writes that a captured CUDA graph replays as such
@@ -145,6 +147,17 @@ void set_epilogue(GmmParams &p, const gmm_epilogue *e) {
   p.epi_bias = e ? static_cast<const __nv_bfloat16 *>(e->bias) : nullptr;
   p.epi_row_scale = e ? e->row_scale : nullptr;
   p.epi_act = e ? e->activation : GMM_ACT_NONE;
+}
+
+// A call without rows: c and a both NULL, as an empty tensor's pointer is.  Its groups are empty
+// whatever a_offsets holds (it gets offsets of zero), so what now stands for c and a is neither
+// read nor written.
+bool take_no_rows(gmm_ctx *h, void **c, const void **a, const uint32_t **a_offsets) {
+  if (!h || *c || *a || !*a_offsets) return false;
+  *c = h->ws;
+  *a = h->ws;
+  *a_offsets = h->zero_offsets;
+  return true;
 }
 
 int check_common(gmm_ctx *h, void *c, const void *a, const uint32_t *a_offsets, const int32_t *ids,
@@ -790,7 +803,8 @@ int gmm_create(gmm_handle_t *out, int num_experts, int device) {
     for (int i = 0; i < 7; ++i)
       fprintf(stderr, "gmm: %-16s stages %d smem %zu grid %d\n", names[i], vs[i]->stages, vs[i]->smem, vs[i]->grid);
   }
-  const size_t counts_at = kStatusBytes + static_cast<size_t>(sms) * gmm::kMapSlotBytes;
+  const size_t zero_at = kStatusBytes + static_cast<size_t>(sms) * gmm::kMapSlotBytes;
+  const size_t counts_at = zero_at + (gmm::kMaxGroups + 4) / 4 * 16;   // kMaxGroups + 1 words, whole 16 bytes
   h->ws_bytes = counts_at + (num_experts <= gmm::kRouteMaxExperts ? gmm::kRouteMaxCounts * sizeof(uint32_t) : 0);
   if (cudaMalloc(&h->ws, h->ws_bytes) != cudaSuccess ||
       cudaMemset(h->ws, 0, h->ws_bytes) != cudaSuccess) {
@@ -799,6 +813,7 @@ int gmm_create(gmm_handle_t *out, int num_experts, int device) {
     delete h;
     return GMM_ERR_CUDA;
   }
+  h->zero_offsets = reinterpret_cast<const uint32_t *>(h->ws + zero_at);
   if (num_experts <= gmm::kRouteMaxExperts) h->route_counts = reinterpret_cast<uint32_t *>(h->ws + counts_at);
   *out = h;
   return GMM_OK;
@@ -816,6 +831,7 @@ int gmm_destroy(gmm_handle_t h) {
 int gmm_run_ex(gmm_handle_t h, void *c, const void *a, const uint32_t *a_offsets, const void *b,
                const int32_t *expert_ids, uint32_t *expert_usage_stats, int num_groups, int N, int K,
                const gmm_epilogue *epilogue, cudaStream_t stream) {
+  take_no_rows(h, &c, &a, &a_offsets);
   int rc = check_common(h, c, a, a_offsets, expert_ids, expert_usage_stats, num_groups, N, K);
   if (rc) return rc;
   rc = check_epilogue(epilogue);
@@ -855,6 +871,7 @@ int gmm_run_planes(gmm_handle_t h, void *c, const void *a, const uint32_t *a_off
   const int s0 = a_plane_splits[0], s1 = a_plane_splits[1];
   if (s0 < 0 || s1 < 0 || s0 > N || s1 > N - s0) return GMM_ERR_INVALID_ARG;
   if (s0 % 256 || s1 % 256) return GMM_ERR_UNSUPPORTED;   // a tile's 256 weight rows in one plane
+  take_no_rows(h, &c, &a, &a_offsets);
   int rc = check_common(h, c, a, a_offsets, expert_ids, expert_usage_stats, num_groups, N, K);
   if (rc) return rc;
   rc = check_epilogue(epilogue);
@@ -890,6 +907,7 @@ int gmm_run_fp8(gmm_handle_t h, void *c, const void *a, const uint32_t *a_offset
                 const gmm_epilogue *epilogue, cudaStream_t stream) {
   if (K < 16 || K % 16) return GMM_ERR_INVALID_ARG;
   const int KU = K / 2;   // two-byte units per row
+  if (take_no_rows(h, &c, &a, &a_offsets) && !input_scale) input_scale = reinterpret_cast<const float *>(h->ws);
   int rc = check_common(h, c, a, a_offsets, expert_ids, expert_usage_stats, num_groups, N, KU);
   if (rc) return rc;
   rc = check_epilogue(epilogue);
@@ -986,6 +1004,7 @@ int gmm_run_int4_ex(gmm_handle_t h, void *c, const void *a, const uint32_t *a_of
                     uint32_t *expert_usage_stats, int num_groups, int N, int K, int group_size,
                     const gmm_epilogue *epilogue, cudaStream_t stream) {
   if (!h) return GMM_ERR_INVALID_ARG;
+  take_no_rows(h, &c, &a, &a_offsets);
   return run_int4(h, h->num_experts, c, a, a_offsets, b_packed, b_scales, expert_ids, expert_usage_stats,
                   num_groups, N, K, group_size, epilogue, stream);
 }
@@ -1166,7 +1185,8 @@ int gmm_run_fp4(gmm_handle_t h, void *c, const void *a, const uint32_t *a_offset
   if (format != GMM_FP4_NV && format != GMM_FP4_MX) return GMM_ERR_INVALID_ARG;
   if (K < 32 || K % 32) return GMM_ERR_INVALID_ARG;
   const int KU = K / 4;
-  if (h && num_groups == 0) {   // no rows: c, a and a_scales may be NULL (an empty tensor's), nothing is read or written
+  const bool no_rows = take_no_rows(h, &c, &a, &a_offsets);
+  if (h && (no_rows || num_groups == 0)) {   // nothing of them is read or written
     if (!c) c = h->ws;
     if (!a) a = h->ws;
     if (!a_scales) a_scales = h->ws;
