@@ -98,13 +98,29 @@ struct gmm_ctx {
 
 namespace {
 
+// A driver call.  It needs a current context, which a thread that has made no runtime call but
+// cudaGetDevice lacks (autograd runs a backward pass on such a thread): the device's primary
+// context is then made current, and the call made again.
+template <class Call>
+CUresult with_context(gmm_ctx *h, Call call) {
+  const CUresult r = call();
+  if (r != CUDA_ERROR_INVALID_CONTEXT) return r;
+  DeviceGuard guard(h->device);
+  if (cudaSetDevice(h->device) != cudaSuccess) {
+    cudaGetLastError();
+    return r;
+  }
+  return call();
+}
+
 int encode_map(gmm_ctx *h, CUtensorMap *m, CUtensorMapDataType type, uint32_t rank, const void *base,
                const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
                CUtensorMapSwizzle swizzle) {
   cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = h->encode(m, type, rank, const_cast<void *>(base), dims, strides, box, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = with_context(h, [&] {
+    return h->encode(m, type, rank, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
   if (r != CUDA_SUCCESS) debug_report("cuTensorMapEncodeTiled", static_cast<int>(r), nullptr);
   return r == CUDA_SUCCESS ? GMM_OK : GMM_ERR_CUDA;
 }
@@ -197,9 +213,11 @@ void fill_common(gmm_ctx *h, GmmParams &p, void *c, const uint32_t *a_offsets, c
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), 1ull << 31};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(N) * 2u};
     const cuuint32_t box[2] = {32, 32}, estr[2] = {1, 1};
-    p.c_tma = h->encode(&p.c_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c, dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    p.c_tma = with_context(h, [&] {
+                return h->encode(&p.c_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c, dims, strides, box, estr,
+                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                                 CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+              }) == CUDA_SUCCESS;
   }
   if (const char *env = getenv("GMM_TMA_STORE")) p.c_tma = p.c_tma && atoi(env) != 0;   // tuning override
   const double block_bytes = static_cast<double>(max_tok) * K * 2.0;
@@ -1018,7 +1036,7 @@ int gmm_matmul_int4(gmm_handle_t h, void *c, const void *a, const uint32_t *b_pa
   // writes (memset nodes in a captured CUDA graph, so a replay needs no host memory).
   DeviceGuard guard(h->device);
   const CUdeviceptr routing = reinterpret_cast<CUdeviceptr>(h->ws + kDenseRoutingOffset);   // a_offsets[0..1], expert_ids[0]
-  if (h->memset32(routing, 0u, 3, reinterpret_cast<CUstream>(stream)) != CUDA_SUCCESS ||
+  if (with_context(h, [&] { return h->memset32(routing, 0u, 3, reinterpret_cast<CUstream>(stream)); }) != CUDA_SUCCESS ||
       h->memset32(routing + 4, static_cast<unsigned int>(M), 1, reinterpret_cast<CUstream>(stream)) != CUDA_SUCCESS) {
     cudaGetLastError();
     return GMM_ERR_CUDA;
