@@ -50,7 +50,8 @@ def _quantise(h, x, fmt, row_slots=None, top_k=1):
     scales = torch.empty((rows, gmm.fp4_scale_pitch(x.shape[1], fmt)), dtype=torch.uint8, device=x.device)
     g = None
     if fmt == "nvfp4":
-        g = (x.abs().amax().float().clamp(min=1e-20) / (6 * 448)).reshape(1)
+        top = x.abs().amax() if x.numel() else x.new_zeros(())     # no tokens: no largest one
+        g = (top.float().clamp(min=1e-20) / (6 * 448)).reshape(1)
     gmm.gmm_quantize_fp4(h, packed, scales, x, fmt=fmt, row_slots=row_slots, top_k=top_k, global_scale=g)
     return packed, scales, g
 

@@ -1,0 +1,40 @@
+"""examples/moe_layer.py on a batch without tokens and under the gradients that autograd really passes."""
+import pytest
+import torch
+from test_gpu_moe_layer import _example
+
+pytestmark = pytest.mark.gpu
+
+
+def _layer(T, E=4, top_k=2, K=96, N=136, seed=3):
+    m = _example()
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    x, w = rnd(T, K).bfloat16(), (rnd(E, N, K) * 0.1).bfloat16()
+    ids, weights = m.route(x, rnd(K, E), top_k)
+    x, weights = x.requires_grad_(), weights.detach().requires_grad_()
+    h = m.gmm.gmm_create(E, 0)
+    out = m.Experts.apply(x, weights, ids, w, w.transpose(1, 2).contiguous(), h)
+    return m, h, x, weights, out
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_serve_without_tokens(fmt):
+    m = _example()
+    E, width, hidden = 4, 160, 288
+    h = m.gmm.gmm_create(E, 0)
+    up = m.Fp4Weights(h, torch.randn((E, hidden, width), device="cuda"), fmt)
+    down = m.Fp4Weights(h, torch.randn((E, width, hidden), device="cuda"), fmt)
+    x = torch.zeros((0, width), dtype=torch.bfloat16, device="cuda")
+    out = m.serve(h, x, torch.randn((width, E), device="cuda"), up, down, 2)
+    assert out.shape == (0, width) and m.gmm.gmm_query_status(h) == m.gmm.GMM_OK
+    m.gmm.gmm_destroy(h)
+
+
+def test_training_without_tokens():
+    m, h, x, weights, out = _layer(0)
+    out.backward(torch.zeros_like(out))
+    assert x.grad.shape == x.shape and weights.grad.shape == weights.shape
+    assert m.gmm.gmm_query_status(h) == m.gmm.GMM_OK
+    m.gmm.gmm_destroy(h)
