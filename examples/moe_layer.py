@@ -111,6 +111,8 @@ class Experts(torch.autograd.Function):
     def backward(ctx, d_out):
         y, weights, off, slot_rows, experts, stats, w_t = ctx.saved_tensors
         h = ctx.h
+        if d_out.stride(1) != 1:     # an expanded or transposed gradient (that of out.sum(), for one)
+            d_out = d_out.contiguous()
         d_y, d_weights = torch.empty_like(y), torch.empty_like(weights)
         gmm.gmm_combine_grad(h, d_y, d_weights, d_out, y, slot_rows, weights)
         d_rows = torch.empty((y.shape[0], w_t.shape[1]), dtype=y.dtype, device=y.device)

@@ -38,3 +38,23 @@ def test_training_without_tokens():
     assert x.grad.shape == x.shape and weights.grad.shape == weights.shape
     assert m.gmm.gmm_query_status(h) == m.gmm.GMM_OK
     m.gmm.gmm_destroy(h)
+
+
+@pytest.mark.parametrize("kind", ["sum", "transposed", "row", "column"])
+def test_gradients_of_any_strides(kind):
+    """The gradient that reaches the layer may be expanded (out.sum()), column-major or one row for
+    all tokens; it gives what its contiguous copy gives."""
+    m, h, x, weights, out = _layer(37)
+    T, N = out.shape
+    g = torch.randn((N, T), device="cuda").bfloat16()
+    grad = {"sum": torch.ones((), device="cuda").bfloat16().expand(T, N), "transposed": g.t(),
+            "row": g.t()[:1].contiguous().expand(T, N), "column": g.t()[:, :1].expand(T, N)}[kind]
+    assert not grad.is_contiguous()
+    want = torch.autograd.grad(out, (x, weights), grad.contiguous(), retain_graph=True)
+    got = torch.autograd.grad(out, (x, weights), grad, retain_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    if kind == "sum":
+        out.sum().backward()
+        assert torch.equal(x.grad, want[0]) and torch.equal(weights.grad, want[1])
+    assert m.gmm.gmm_query_status(h) == m.gmm.GMM_OK
+    m.gmm.gmm_destroy(h)
