@@ -16,6 +16,7 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from ragged_matmul_gb300 import binding as gmm  # noqa: E402
@@ -108,6 +109,7 @@ class Experts(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_out):
         y, weights, off, slot_rows, experts, stats, w_t = ctx.saved_tensors
         h = ctx.h

@@ -58,3 +58,13 @@ def test_gradients_of_any_strides(kind):
         assert torch.equal(x.grad, want[0]) and torch.equal(weights.grad, want[1])
     assert m.gmm.gmm_query_status(h) == m.gmm.GMM_OK
     m.gmm.gmm_destroy(h)
+
+
+def test_second_derivatives_are_refused():
+    """The layer's gradients are constants to autograd: a second derivative through them is an error and
+    not the part of it that other terms contribute."""
+    m, h, x, weights, out = _layer(9)
+    g, = torch.autograd.grad(out.float().square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (g.sum() + x.square().sum()).backward()
+    m.gmm.gmm_destroy(h)
