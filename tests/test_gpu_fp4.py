@@ -190,6 +190,31 @@ def test_quantise_strided_and_unaligned(fmt):
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
+@pytest.mark.parametrize("shift,pitch", [(0, 160), (8, 168), (4, 164), (1, 163), (0, 161), (2, 162)])
+def test_quantise_every_alignment(fmt, dtype, shift, pitch):
+    """Rows that start on 32 bytes, on 16, on 8, 4 and 2, of each type, gathered and not: the codes and
+    scales of the same values in rows on 32 bytes, which the tests above compare with the reference."""
+    torch, _ = _mods()
+    R, K = 11, 160
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(shift + pitch)
+    values = (torch.randn((R, K), generator=gen, device="cuda") * 3).to(getattr(torch, dtype))
+    values[3, 40] = float("inf")
+    buf = torch.full((shift + R * pitch,), 1e4, dtype=values.dtype, device="cuda")
+    x = buf[shift:].as_strided((R, K), (pitch, 1))
+    x.copy_(values)
+    slots = [4, 21, -1, 0, 13, 7]
+    for kw in ({}, dict(row_slots=slots, top_k=2, rows=len(slots))):
+        got, want = quantise(x, fmt, **kw), quantise(values, fmt, **kw)
+        assert got[2] == want[2] == 0
+        assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+    finite = [r for r in range(R) if r != 3]
+    packed, scales, _ = quantise(x, fmt)
+    check_codes(x.double().cpu().numpy()[finite], packed[finite], scales[finite], fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
 @pytest.mark.parametrize("off", [0, 1])
 def test_dequantise_every_code(fmt, dtype, off):
     """All 16 codes under all scale codes; NaN scales give NaN."""
