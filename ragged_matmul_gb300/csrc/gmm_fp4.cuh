@@ -27,7 +27,8 @@
 //
 // Roles (448 threads per CTA):
 //   warp 0        TMA producer of the stage's weight and token values.
-//   warp 1        TMEM allocation; in the pair's leader the scale copies and MMAs.
+//   warp 1        TMEM allocation; in the pair's leader the scale copies and MMAs, in the peer the
+//                 news that the peer's scales of a stage are written (see the scales' role).
 //   warps 2..9    epilogue, two per TMEM lane quadrant taking every second 32-row chunk.
 //   warps 10..12  scales: the weight rows' block, and the tokens' two.
 //   warp 13       scheduler: decodes the CTA's tiles into a queue that every role reads.
@@ -135,10 +136,11 @@ template <bool kMx>
 __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_constant__ F4Params p) {
   using G = F4Geom<kMx>;
   using S = F4Scale<kMx>;
-  constexpr uint32_t kFullArrivals = 1 + 2 * kF4ScaleWarps;   // the values, both CTAs' scale warps
+  constexpr uint32_t kFullArrivals = 1 + kF4ScaleWarps + 1;   // the values, the leader's scale warps, the peer's forwarder
   constexpr uint32_t kEpiArrivals = 2 * kF4EpiWarps;
   __shared__ Ctrl ctl;
   __shared__ uint64_t peer_free[kF4Queue];   // leader: the peer's readers have taken a queue entry
+  __shared__ uint64_t scales_in[kMaxStages];   // peer: its scale warps have written a stage's atoms
   extern __shared__ uint8_t dyn_smem[];
 
   // Warp-uniform values that steer the roles are broadcast from lane 0: the compiler then knows
@@ -161,6 +163,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
     for (uint32_t s = 0; s < ST; ++s) {
       mbar_init(smem_addr(&ctl.full[s]), kFullArrivals);
       mbar_init(smem_addr(&ctl.empty[s]), 1);
+      mbar_init(smem_addr(&scales_in[s]), kF4ScaleWarps);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_addr(&ctl.acc_full[a]), 1);
@@ -170,7 +173,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
     for (uint32_t q = 0; q < kF4Queue; ++q) {
       mbar_init(smem_addr(&peer_free[q]), 1);
       mbar_init(smem_addr(&ctl.tq_full[q]), 1);
-      mbar_init(smem_addr(&ctl.tq_empty[q]), 1 + (rank == 0) + kF4EpiWarps + kF4ScaleWarps);
+      mbar_init(smem_addr(&ctl.tq_empty[q]), 2 + kF4EpiWarps + kF4ScaleWarps);   // warps 0 and 1 too
     }
     ctl.abort = 0;
     ctl.active = 0;
@@ -300,7 +303,28 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
         if (acc == 0) acc_phase ^= 1u;
       }
       if ((!ok || got < 0) && lane == 0) atomicOr(p.status, kStatusTimeout);
+    } else if (lane == 0) {
+      // The peer's scales to the leader, whose MMA warp issues the copies that read them: acquired
+      // in this CTA, released at cluster scope.
+      const uint32_t full0 = map_to_rank(smem_addr(&ctl.full[0]), 0);
+      Ring rt;
+      bool ok = true;
+      F4Feed feed;
+      for (Tile ti; ok;) {
+        const int got = feed.next<false>(ctl, abort, &ti);
+        if (got <= 0) {
+          ok = got == 0;
+          break;
+        }
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!wait_phase(smem_addr(&scales_in[rt.slot]), rt.phase, abort)) { ok = false; break; }
+          mbar_arrive_cluster_shared(full0 + rt.slot * 8u);
+          rt.next(ST);
+        }
+      }
+      if (!ok) atomicOr(p.status, kStatusTimeout);
     }
+    __syncwarp();
   } else if (warp < static_cast<int>(kF4FirstScaleWarp)) {
     // ------------------------------------------------------------ epilogue
     if (warp == 2) {
@@ -438,11 +462,17 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
     // load: two loads of 16 bytes fetch a sector twice when the line has left L1 in between
     // (prefill shapes: 0.93 ms instead of 0.71; rows an odd number of 16 bytes apart, which have
     // no other way, pay it: K = 5888 63.6 us, K = 5632 49.8 for 6231 rows, N = 1280).
+    // The copies that read a stage's atoms are issued in the leader.  Its own scale warps arrive
+    // on the stage's barrier; the peer's arrive on a barrier of their CTA, and its warp 1 passes
+    // the news on, for a release at CTA scope does not order the atoms for a thread of the other
+    // CTA.  That release is restricted to shared memory: an unrestricted one takes 0.95 us a stage
+    // (prefill shapes 1.5 ms).  The same fence in the scale warps themselves holds them up
+    // (0.648 ms; with the forwarder 0.627, one token's product 13.1 us for 13.0).
     constexpr uint32_t kRowStage = kF4StageK / S::kBlock;   // scale bytes per row and stage
     constexpr int kStages = static_cast<int>(32 / kRowStage);
     const int chunks = (KB + kStages - 1) / kStages;
     const uint32_t role = static_cast<uint32_t>(warp) - kF4FirstScaleWarp;
-    const uint32_t full0 = map_to_rank(smem_addr(&ctl.full[0]), 0);
+    const uint32_t written0 = smem_addr(rank == 0 ? &ctl.full[0] : &scales_in[0]);
     const int row_bytes = 4 * p.K / static_cast<int>(S::kBlock);
     const uint32_t atom0 = s_ring + static_cast<uint32_t>(lane) * 16u + (role == 0 ? 0u : (S::kWords + role - 1u) * kF4Atom);
     const uint32_t atom_step = role == 0 ? kF4Atom : 2u * kF4Atom;
@@ -534,7 +564,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
                   }
                   fence_async_smem();   // these writes, before the tensor-memory copies read them
                   __syncwarp();
-                  if (lane == 0) mbar_arrive_cluster_shared(full0 + rt.slot * 8u);
+                  if (lane == 0) mbar_arrive(written0 + rt.slot * 8u);
                   rt.next(ST);
                 }
               }
