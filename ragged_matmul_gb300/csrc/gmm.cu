@@ -577,8 +577,8 @@ int launch_dispatch(gmm_ctx *h, gmm::DispatchParams &p, cudaStream_t stream) {
 template <class T, int VN, int kRows, int kUnits>
 void launch_grad(gmm_ctx *h, gmm::CombineParams &p, long long nvec, cudaStream_t stream) {
   // One warp a token when that fills the SMs (32 resident warps each; 24 for single elements,
-  // whose pieces are shorter: 1003 tokens of 1411 fp32, top-6, 16.0 us with four warps a token,
-  // 16.5 with eight), else more.
+  // whose pieces are shorter: 1003 tokens of 1411 fp32, top-6, 15.2 us with four warps a token,
+  // 0.5 more with eight), else more.
   constexpr long long kFill = VN == 1 ? 24 : 32;
   const long long pieces = (nvec + 32 * kUnits - 1) / (32 * kUnits);
   int wpt = 1;

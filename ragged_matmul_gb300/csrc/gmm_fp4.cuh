@@ -33,13 +33,14 @@
 //   warps 10..12  scales: the weight rows' block, and the tokens' two.
 //   warp 13       scheduler: decodes the CTA's tiles into a queue that every role reads.
 //
-// Measured: 32768 rows over 8 experts, K = 4096, N = 14336, nvfp4: 0.64 ms, 6.0 PFLOP/s.  What
-// bounds it is what enters an SM: 37 KB a stage (31 KB of values, 6 KB of scales), which without
-// the MMAs and the epilogue takes 0.518 ms (18.4 TB/s, 64 bytes a clock and SM; multicast to
-// clusters of 2, 4 or 8 does not raise that rate), with the epilogue 0.574 ms; the MMAs alone
-// 0.42 ms.  So a tile holds as many tokens as tensor memory allows beside a second accumulator
-// (224 instead of 240: 0.693 ms).  2048 rows over 64 experts, K = 2048, N = 2816: 45 us with cold
-// weights, 4.9 TB/s.
+// Measured: 32768 rows over 8 experts, K = 4096, N = 14336, nvfp4: 0.63 ms, 6.1 PFLOP/s (0.70 to
+// 0.73 back to back, at the power cap).  Measured by parts, of 0.64 ms: the MMAs alone 0.42; without
+// them 0.574, without the epilogue too 0.518, which is 37 KB a stage and CTA (31 KB of values, 6 KB
+// of scales) entering the SMs at 18.4 TB/s, 64 bytes a clock and SM.  So a tile holds as many tokens
+// as tensor memory allows beside a second accumulator (224 instead of 240: 0.693 ms).  Whether
+// multicast would shorten that part is open: a program of copies alone gained nothing from it, but it
+// brought only 45 to 48 bytes a clock into an SM with it or without.  2048 rows over 64 experts,
+// K = 2048, N = 2816: 46 us with cold weights, 4.8 TB/s.
 //
 // Tiles are claimed by the pair as the grouped kernel's are (a static share where there are
 // few).  Every wait is bounded as in the grouped kernel.
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(kF4Threads, 1) gmm_fp4_kernel(const __grid_con
     // L2 sector, kStages stages) at a time, one chunk ahead of its use in registers, by one
     // load: two loads of 16 bytes fetch a sector twice when the line has left L1 in between
     // (prefill shapes: 0.93 ms instead of 0.71; rows an odd number of 16 bytes apart, which have
-    // no other way, pay it: K = 5888 63.6 us, K = 5632 49.8 for 6231 rows, N = 1280).
+    // no other way, pay it: K = 5888 57 us, K = 5632 44 for 6231 rows, N = 1280).
     // The copies that read a stage's atoms are issued in the leader.  Its own scale warps arrive
     // on the stage's barrier; the peer's arrive on a barrier of their CTA, and its warp 1 passes
     // the news on, for a release at CTA scope does not order the atoms for a thread of the other

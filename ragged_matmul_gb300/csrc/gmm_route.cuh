@@ -62,7 +62,7 @@ struct DispatchParams {
 // the same expert in that share; cnt[e] ends as the share's count of expert e.  Thirty-two
 // slots a step: lanes with the same expert find one another by a ballot on every bit of the
 // expert's number (a warp match takes a turn for every different one: 256 tokens, top-8 of 64
-// experts, 6.9 us in all, now 6.1), the lowest of them advances the count.  `emit(s, e, rank)`
+// experts, 0.8 us more than the 5.8 in all), the lowest of them advances the count.  `emit(s, e, rank)`
 // is called for every slot (rank -1 when its expert id is out of range).
 template <class Emit>
 __device__ __forceinline__ uint32_t route_rank_share(const int32_t *ids, int begin, int end, int E, uint32_t *cnt,
@@ -167,7 +167,7 @@ __device__ __forceinline__ void route_copy(const DispatchParams &p, const int *r
 // One launch for few slots: every CTA sorts all of them (a read of at most 16 KB that sits
 // in L2, about a microsecond) and copies its share, which saves the second launch that a
 // count before the copy would need.  CTA 0 writes the maps.  Bound by its latency: 256
-// tokens of 2048 bf16 to 8 of 64 experts take 6.1 us (9 with 2 KB copy units, which only
+// tokens of 2048 bf16 to 8 of 64 experts take 5.8 us (3 more with 2 KB copy units, which only
 // 32 CTAs shared).
 template <int VB, bool kFew>
 __global__ void __launch_bounds__(kRouteThreads) gmm_dispatch_small_kernel(const __grid_constant__ DispatchParams p) {
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kRouteThreads) gmm_dispatch_count_kernel(const
 
 // Second launch, started while the first one runs: a CTA sums the chunk counts (at most 128 KB, from L2) into the first row of
 // every expert's slots in its chunk, then places and copies its tokens, kRouteBatch at a time.
-// Bound by the copy's bytes: 16384 tokens of 8 KB to two rows each take 69.9 us with the
+// Bound by the copy's bytes: 16384 tokens of 8 KB to two rows each take 69 us with the
 // count, 5.8 TB/s.
 template <int VB>
 __global__ void __launch_bounds__(kRouteThreads) gmm_dispatch_place_kernel(const __grid_constant__ DispatchParams p) {
@@ -466,7 +466,7 @@ constexpr int kCombineWarps = 8;
 // (kBatch by top_k, so that few of the unrolled rows are idle: top-2 with batches of 8 took twice
 // as long; single elements, for rows that are not 16-byte aligned, in larger units).  At 64
 // registers a thread half of an SM's warps are resident, which keeps enough loads in flight
-// (with 100 registers and a quarter, 32768 rows of 8 KB to 4096 tokens took 73 us, now 48: 6.2 TB/s).
+// (with 100 registers and a quarter, 32768 rows of 8 KB to 4096 tokens took 73 us, now 47: 6.4 TB/s).
 template <class T, int VN, int kBatch, int kSeq, int kUnits>
 __global__ void __launch_bounds__(32 * kCombineWarps, 4) gmm_combine_kernel(const __grid_constant__ CombineParams p) {
   const int lane = threadIdx.x & 31;
@@ -522,9 +522,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 4) gmm_combine_kernel(cons
 // up to kCombineWarps, more than one where there are few tokens): they take the token's
 // 32 kUnits-vector pieces in turn, kRows rows at a time, and join their dot products through
 // shared memory in warp order.  The loads of a piece's kUnits (kRows + 1) vectors are in flight
-// together.  16384 tokens of 8 KB, top-2: 101.5 us, 6.6 TB/s (118 with a third of the warps
-// resident and four rows' code for two); 1003 tokens of 1411 fp32, top-6: 16.0 us with six
-// rows' code, 17.5 with four's.
+// together.  16384 tokens of 8 KB, top-2: 101 us, 6.6 TB/s (118 with a third of the warps
+// resident and four rows' code for two); 1003 tokens of 1411 fp32, top-6: 15.2 us with six
+// rows' code, 1.5 more with four's.
 template <class T, int VN, int kRows, int kUnits>
 __global__ void __launch_bounds__(32 * kCombineWarps, kRows == 8 ? 3 : 4)
     gmm_combine_grad_kernel(const __grid_constant__ CombineParams p) {
