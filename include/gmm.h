@@ -215,17 +215,80 @@ int gmm_run_fp8(gmm_handle_t h, void *c, const void *a, const uint32_t *a_offset
                 const float *input_scale, const float *weight_scale, const int *scales_granularity_mnk,
                 const gmm_epilogue *epilogue, cudaStream_t stream);
 
+/* Element types of logits, tokens and rows. */
+#define GMM_DTYPE_BF16 0
+#define GMM_DTYPE_FP16 1
+#define GMM_DTYPE_FP32 2
+
+/*
+ * A router's choice: the experts of each token and their weights, from its logits x.
+ *   score       s_e = softmax(x)_e, or 1 / (1 + exp(-x_e));
+ *   key         y_e = s_e + bias[e]: what the choice goes by (bias: fp32 [num_experts] or NULL;
+ *               it moves load between experts and does not enter the weights);
+ *   groups      expert_groups equal runs of experts (1: none).  A group's key is the sum of its
+ *               group_top (1 or 2) largest y_e; the top_groups groups with the largest keys stay;
+ *   choice      the top_k largest y_e of the groups that stay, in descending order;
+ *   weights     scale * s_j, or with renormalise scale * s_j / (the sum of the chosen s_j).
+ * Equal keys, of experts or of groups, go to the lowest index.  Keys are compared to 64-bit
+ * accuracy; equal logits of equal bias are equal keys.  Scores and weights are fp32.
+ * An expert whose key is -infinity or NaN (a masked logit or bias) is never chosen; a group's key
+ * leaves such experts out.  A slot that finds no expert gets id -1 and weight 0, which
+ * gmm_dispatch drops.  A token with a NaN logit (softmax: or one of +infinity) gets no expert and
+ * is reported as GMM_ERR_BAD_INPUT by gmm_query_status.
+ */
+#define GMM_SCORE_SOFTMAX 0
+#define GMM_SCORE_SIGMOID 1
+
+typedef struct gmm_route_options {
+  int scoring;          /* GMM_SCORE_* */
+  int expert_groups;
+  int top_groups;
+  int group_top;
+  int renormalise;      /* 0 or 1 */
+  float scale;          /* finite, above zero */
+} gmm_route_options;
+
+/*
+ *   slot_experts : int32 [num_tokens, top_k], written;  weights: fp32 [num_tokens, top_k], written
+ *                  (gmm_dispatch's and gmm_combine's operands);
+ *   logits       : [num_tokens, num_experts] of `dtype`, num_experts the handle's, rows
+ *                  logits_stride elements apart (0: one row for all).
+ * num_tokens == 0 launches nothing.
+ * Errors (nothing is launched): GMM_ERR_INVALID_ARG (NULL or misaligned for its element type,
+ * negative size, unknown dtype or option, expert_groups that does not divide num_experts,
+ * top_groups above expert_groups, group_top above a group's experts, top_k above the experts
+ * that can stay), GMM_ERR_UNSUPPORTED (top_k > 32, more than 2^30 slots, more than 4096 experts,
+ * 32 groups, or 128 experts a group and lane: a group has 32 / expert_groups lanes, rounded down
+ * to a power of two), GMM_ERR_CUDA.
+ */
+int gmm_route(gmm_handle_t h, int32_t *slot_experts, float *weights, const void *logits, long long logits_stride,
+              const float *bias, int num_tokens, int top_k, int dtype, const gmm_route_options *options,
+              cudaStream_t stream);
+
+/*
+ * The gradient of the weights for the logits, the choice held fixed: d_logits = sum over a token's
+ * slots of d_weights * d weight / d logit, zero for logits that do not enter (fp32, rounded once).
+ *   d_logits     : [num_tokens, num_experts] of `dtype`, rows d_logits_stride (>= num_experts)
+ *                  elements apart, written whole;
+ *   d_weights    : fp32 [num_tokens, top_k]; a slot with a negative id or a logit of -infinity is
+ *                  left out, an id >= num_experts too and is reported as GMM_ERR_BAD_INPUT; slots
+ *                  of a token that name an expert twice both count;
+ *   slot_experts, logits: as gmm_route wrote and took them; options: its scoring, renormalise and
+ *   scale (the others are not read).  A token that gmm_route reports gets zeros.
+ * Errors: as gmm_route.
+ */
+int gmm_route_grad(gmm_handle_t h, void *d_logits, long long d_logits_stride, const float *d_weights,
+                   const int32_t *slot_experts, const void *logits, long long logits_stride, int num_tokens, int top_k,
+                   int dtype, const gmm_route_options *options, cudaStream_t stream);
+
 /*
  * Tokens sorted by expert and back.  A router gives token t its top_k experts; slot
  * s = t * top_k + j is its j-th.  Rows (the grouped calls' A and C) hold one slot each, all
  * slots of expert 0 first, then expert 1, ..., each expert's in ascending slot order.
  * The calls below are asynchronous on `stream`, allocate nothing, can be captured in a CUDA
  * graph, and give the same bits every time (gmm_combine_grad for distinct rows, which it
- * requires).  Element types of the moved rows:
+ * requires).
  */
-#define GMM_DTYPE_BF16 0
-#define GMM_DTYPE_FP16 1
-#define GMM_DTYPE_FP32 2
 
 /*
  * Sort the slots by expert and copy the tokens to their rows.
@@ -283,6 +346,81 @@ int gmm_combine(gmm_handle_t h, void *out, long long out_stride, const void *row
 int gmm_combine_grad(gmm_handle_t h, void *d_rows, float *d_weights, const void *d_out, long long d_out_stride,
                      const void *rows, int num_rows, const int32_t *slot_rows, const float *weights, int num_tokens,
                      int top_k, int width, int dtype, cudaStream_t stream);
+
+/*
+ * 8-bit floating point (e4m3) with a scale for each block of 128:
+ *     q = e4m3(x / s),  s = amax / 448  (amax: the block's largest magnitude)
+ * every step rounded to nearest even in fp32, s = 0 giving q = 0; with pow2 = 1, s is the smallest
+ * power of two that is at least amax / 448 (2^-127 at least; 0 for a block of zeros).  A block that
+ * holds an infinity or a NaN gets a NaN scale and zero codes.
+ *
+ * Rows, a scale for each 128 elements of a row: gmm_run_fp8's a and input_scale of granularity
+ * (1, ., 128), optionally gathered.
+ *   q: e4m3 [rows, K] (16-byte aligned); scales: fp32 [rows, ceil(K / 128)];
+ *   x: [src_rows, K] of `dtype`, rows x_stride elements apart (0: one row for all);
+ *   row_slots: int32 [rows] (gmm_dispatch's row_slots) or NULL: row r is quantised from
+ *   x[row_slots[r] / top_k]; a row with a negative entry stays untouched, one whose source row is
+ *   past src_rows too and is reported as GMM_ERR_BAD_INPUT.
+ * Requirements: K a multiple of 16, up to 2^24; rows up to 2^30.  rows == 0 launches nothing.
+ * Errors (nothing is launched): GMM_ERR_INVALID_ARG, GMM_ERR_UNSUPPORTED, GMM_ERR_CUDA.
+ */
+int gmm_quantize_fp8(gmm_handle_t h, void *q, float *scales, const void *x, long long x_stride, int src_rows,
+                     const int32_t *row_slots, int top_k, int rows, int K, int dtype, int pow2, cudaStream_t stream);
+
+/*
+ * Weights, a scale for each 128 x 128 of a matrix: gmm_run_fp8's b and weight_scale of granularity
+ * (., 128, 128).  The codes of the transposed weights, for the product that takes gradients back
+ * through the layer, are these transposed, with the scales transposed.
+ *   q: e4m3 [batch, N, K] (16-byte aligned); scales: fp32 [batch, ceil(N / 128), ceil(K / 128)];
+ *   x: [batch, N, K] of `dtype`, contiguous.
+ * Requirements and errors: as gmm_quantize_fp8, and up to 2^31 - 1 tiles.
+ */
+int gmm_quantize_fp8_tiles(gmm_handle_t h, void *q, float *scales, const void *x, int batch, int N, int K, int dtype,
+                           int pow2, cudaStream_t stream);
+
+/*
+ * Along the rows of each group, a scale for each 128 rows and column: the operands of
+ * gmm_weight_grad_fp8.  The codes are stored transposed, and each group's rows start a block:
+ *     q_t[c, at(r)] for r in [a_offsets[g], a_offsets[g+1]),
+ *     at(r) = (a_offsets[g] / 128 + g) * 128 + (r - a_offsets[g])
+ * with zeros behind a group's last row up to the end of its block.  Scales are powers of two, as
+ * their exponent codes (2^(code - 127); 0 for a block of zeros, 255 for NaN).
+ *   q_t: e4m3 [width, pitch], pitch = GMM_FP8_COLS_PITCH(rows, num_groups) (16-byte aligned);
+ *   t_scales: uint8 [pitch / 128, width]; blocks that no group uses stay untouched in both;
+ *   q, scales: both NULL, or written too, of the rows that a group covers, as gmm_quantize_fp8
+ *   with pow2 = 0 writes them (the rows are read once for both forms);
+ *   x, row_slots, top_k: as gmm_quantize_fp8; a row without a source counts as zeros in q_t;
+ *   a_offsets: uint32 [num_groups + 1], non-decreasing, at most rows; else nothing is written, and
+ *   GMM_ERR_BAD_INPUT is reported by gmm_query_status.
+ * Requirements: width a multiple of 16, up to 2^24; num_groups up to 4096.  rows == 0 or
+ * num_groups == 0 launches nothing.  Errors: as gmm_quantize_fp8, plus GMM_ERR_INVALID_ARG for only
+ * one of q and scales.
+ */
+#define GMM_FP8_COLS_PITCH(rows, num_groups) (((rows) / 128 + (num_groups)) * 128)
+int gmm_quantize_fp8_cols(gmm_handle_t h, void *q_t, void *t_scales, void *q, float *scales, const void *x,
+                          long long x_stride, int src_rows, const int32_t *row_slots, int top_k, const uint32_t *a_offsets,
+                          int num_groups, int rows, int width, int dtype, cudaStream_t stream);
+
+/*
+ * The gradient of the expert weights, C = A . B[g]^T for the rows of group g:
+ *     d_b[g, n, k] (+)= sum over r in [a_offsets[g], a_offsets[g+1]) of d_c[r, n] * a[r, k]
+ * on operands that gmm_quantize_fp8_cols wrote, the scales applied in the tensor core, sums in fp32,
+ * one rounding.  Each group has a gradient of its own; a group without rows gets zeros.
+ *   d_b: [num_groups, N, K] of `dtype` (GMM_DTYPE_FP32 or GMM_DTYPE_BF16), 16-byte aligned;
+ *   accumulate: 1 adds to what d_b holds (GMM_DTYPE_FP32 only), groups without rows untouched;
+ *   d_t, d_t_scales: the gradient of C, e4m3 [N, pitch] and uint8 [pitch / 128, N];
+ *   a_t, a_t_scales: A, e4m3 [K, pitch] and uint8 [pitch / 128, K], both of
+ *   pitch = GMM_FP8_COLS_PITCH(rows, num_groups) and 16-byte aligned (the scales of any);
+ *   a_offsets: as gmm_quantize_fp8_cols took them, with the same meaning of bad ones.
+ * Requirements: N and K multiples of 16, up to 2^24; num_groups up to 4096.
+ * Without rows (rows == 0) the operands and a_offsets may be NULL and are not read.
+ * num_groups == 0 launches nothing.
+ * Errors (nothing is launched): GMM_ERR_INVALID_ARG, GMM_ERR_UNSUPPORTED (a size above its limit,
+ * GMM_DTYPE_FP16, 2^31 tiles of 256 x 240, or a device that cannot run CTA pairs), GMM_ERR_CUDA.
+ */
+int gmm_weight_grad_fp8(gmm_handle_t h, void *d_b, const void *d_t, const void *d_t_scales, const void *a_t,
+                        const void *a_t_scales, const uint32_t *a_offsets, int num_groups, int rows, int N, int K,
+                        int dtype, int accumulate, cudaStream_t stream);
 
 /*
  * Microscaled 4-bit floating point.  A value is e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their

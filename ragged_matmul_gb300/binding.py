@@ -33,7 +33,9 @@ GMM_ERR_NO_DEVICE = -6
 
 EXPORTED = ("gmm_create", "gmm_run", "gmm_run_ex", "gmm_run_int4", "gmm_run_int4_ex", "gmm_matmul_int4",
             "gmm_run_fp8", "gmm_run_planes", "gmm_run_noalloc", "gmm_query_status", "gmm_error_string", "gmm_destroy",
-            "gmm_dispatch", "gmm_combine", "gmm_combine_grad", "gmm_quantize_fp4", "gmm_dequantize_fp4", "gmm_run_fp4")
+            "gmm_dispatch", "gmm_combine", "gmm_combine_grad", "gmm_quantize_fp4", "gmm_dequantize_fp4", "gmm_run_fp4",
+            "gmm_route", "gmm_route_grad", "gmm_quantize_fp8", "gmm_quantize_fp8_tiles", "gmm_quantize_fp8_cols",
+            "gmm_weight_grad_fp8")
 
 # Activations of the optional epilogue (GMM_ACT_* in gmm.h).
 GMM_ACT_NONE = 0
@@ -51,10 +53,24 @@ GMM_FP4_MX = 1
 FP4_FORMATS = {"nvfp4": GMM_FP4_NV, "mxfp4": GMM_FP4_MX}
 FP4_BLOCKS = {GMM_FP4_NV: 16, GMM_FP4_MX: 32}
 
+# Score functions of the router's choice (GMM_SCORE_*), and the block of the 8-bit quantisers.
+GMM_SCORE_SOFTMAX = 0
+GMM_SCORE_SIGMOID = 1
+SCORINGS = {"softmax": GMM_SCORE_SOFTMAX, "sigmoid": GMM_SCORE_SIGMOID}
+FP8_BLOCK = 128
+
 
 class GmmEpilogue(ctypes.Structure):
     """gmm_epilogue: y = act(acc + bias[e, n]) * row_scale[r] before the bf16 store."""
     _fields_ = [("bias", ctypes.c_void_p), ("row_scale", ctypes.c_void_p), ("activation", ctypes.c_int)]
+
+
+
+class GmmRouteOptions(ctypes.Structure):
+    """gmm_route_options: how experts are scored, chosen and weighted."""
+    _fields_ = [("scoring", ctypes.c_int), ("expert_groups", ctypes.c_int), ("top_groups", ctypes.c_int),
+                ("group_top", ctypes.c_int), ("renormalise", ctypes.c_int), ("scale", ctypes.c_float)]
+
 
 _lib = None
 
@@ -111,6 +127,19 @@ def load_library(path: str | None = None):
     lib.gmm_dequantize_fp4.restype = I
     lib.gmm_run_fp4.argtypes = [P, P, P, P, P, P, P, I, I, I, P, P, I, P, P, EP, P]
     lib.gmm_run_fp4.restype = I
+    RO = ctypes.POINTER(GmmRouteOptions)
+    lib.gmm_route.argtypes = [P, P, P, P, L, P, I, I, I, RO, P]
+    lib.gmm_route.restype = I
+    lib.gmm_route_grad.argtypes = [P, P, L, P, P, P, L, I, I, I, RO, P]
+    lib.gmm_route_grad.restype = I
+    lib.gmm_quantize_fp8.argtypes = [P, P, P, P, L, I, P, I, I, I, I, I, P]
+    lib.gmm_quantize_fp8.restype = I
+    lib.gmm_quantize_fp8_tiles.argtypes = [P, P, P, P, I, I, I, I, I, P]
+    lib.gmm_quantize_fp8_tiles.restype = I
+    lib.gmm_quantize_fp8_cols.argtypes = [P, P, P, P, P, P, L, I, P, I, P, I, I, I, I, P]
+    lib.gmm_quantize_fp8_cols.restype = I
+    lib.gmm_weight_grad_fp8.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, P]
+    lib.gmm_weight_grad_fp8.restype = I
     lib.gmm_query_status.argtypes = [P, P]
     lib.gmm_query_status.restype = I
     lib.gmm_error_string.argtypes = [I]
@@ -659,6 +688,196 @@ def gmm_run_fp4(h: Handle, c, a, a_offsets, b, expert_ids, expert_usage_stats, a
                                     stream_handle(dev, stream))
     if check and rc != GMM_OK:
         raise GmmError(rc, "gmm_run_fp4")
+    return rc
+
+
+# ---------------------------------------------------------------- a router's choice
+
+_ROUTE_OPTIONS = {}
+
+
+def _route_options(scoring, renormalise, scale, groups=1, top_groups=1, group_top=1):
+    """gmm_route_options by reference; one structure for each combination of settings."""
+    key = (scoring, groups, top_groups, group_top, renormalise, scale)
+    o = _ROUTE_OPTIONS.get(key)
+    if o is None:
+        s = SCORINGS.get(scoring, scoring)
+        if s not in (GMM_SCORE_SOFTMAX, GMM_SCORE_SIGMOID):
+            raise ValueError(f"unknown scoring {scoring!r}: one of {tuple(SCORINGS)}")
+        o = ctypes.byref(GmmRouteOptions(s, int(groups), int(top_groups), int(group_top), int(bool(renormalise)),
+                                         float(scale)))
+        if len(_ROUTE_OPTIONS) >= 64:
+            _ROUTE_OPTIONS.clear()
+        _ROUTE_OPTIONS[key] = o
+    return o
+
+
+def _check_logits(t, name, h, types, out=False):
+    """Pointer, row stride and number of rows of [tokens, E]."""
+    p, stride, shape = _check_strided(t, name, types, h.device, out)
+    if shape[1] != h.num_experts:
+        raise ValueError(f"{name} must be [tokens, {h.num_experts}], got {tuple(shape)}")
+    return p, stride, shape[0]
+
+
+def gmm_route(h: Handle, slot_experts, weights, logits, scoring="softmax", bias=None, expert_groups: int = 1,
+              top_groups: int | None = None, group_top: int = 1, renormalise: bool = True, scale: float = 1.0,
+              stream=None, check: bool = True) -> int:
+    """The top_k experts of each token and their weights, from its logits [tokens, E] (bf16, fp16 or fp32):
+    writes slot_experts int32 [tokens, top_k] and weights fp32 [tokens, top_k].  Chosen by score + bias
+    (scoring "softmax" or "sigmoid"; bias fp32 [E]) among the top_groups of expert_groups groups with the
+    largest sums of their group_top best, equal keys to the lowest index; weights are scale * score, divided by
+    the chosen scores' sum if renormalise.  A masked expert (-infinity) is never chosen; a slot without an
+    expert gets -1 and 0."""
+    types, dev = _row_types(), h.device
+    pl, stride, T = _check_logits(logits, "logits", h, types)
+    pe, shape = _slots(slot_experts, "slot_experts", dev)
+    if shape[0] != T:
+        raise ValueError(f"slot_experts must be [{T}, top_k], got {tuple(shape)}")
+    pw = _shaped(weights, "weights", _F32, dev, shape)
+    pb = None if bias is None else _shaped(bias, "bias", _F32, dev, (h.num_experts,))
+    o = _route_options(scoring, renormalise, scale, expert_groups, expert_groups if top_groups is None else top_groups,
+                       group_top)
+    rc = load_library().gmm_route(h.ptr, pe, pw, pl, stride, pb, T, shape[1], types[logits.dtype], o,
+                                  stream_handle(dev, stream))
+    if check and rc != GMM_OK:
+        raise GmmError(rc, "gmm_route")
+    return rc
+
+
+def gmm_route_grad(h: Handle, d_logits, d_weights, slot_experts, logits, scoring="softmax", renormalise: bool = True,
+                   scale: float = 1.0, stream=None, check: bool = True) -> int:
+    """The gradient of gmm_route's weights for its logits, the choice held fixed: writes d_logits [tokens, E]
+    (the logits' dtype) from d_weights fp32 [tokens, top_k]; slots with a negative id are left out."""
+    types, dev = _row_types(), h.device
+    pl, stride, T = _check_logits(logits, "logits", h, types)
+    pd, d_stride, n = _check_logits(d_logits, "d_logits", h, (logits.dtype,), out=True)
+    pe, shape = _slots(slot_experts, "slot_experts", dev)
+    if shape[0] != T or n != T:
+        raise ValueError(f"slot_experts must be [{T}, top_k] and d_logits [{T}, {h.num_experts}], got {tuple(shape)} and "
+                         f"{tuple(d_logits.shape)}")
+    pw = _shaped(d_weights, "d_weights", _F32, dev, shape)
+    rc = load_library().gmm_route_grad(h.ptr, pd, d_stride, pw, pe, pl, stride, T, shape[1], types[logits.dtype],
+                                       _route_options(scoring, renormalise, scale), stream_handle(dev, stream))
+    if check and rc != GMM_OK:
+        raise GmmError(rc, "gmm_route_grad")
+    return rc
+
+
+# ---------------------------------------------------------------- 8-bit floating point, blocks of 128
+
+_E4M3 = None
+
+
+def _e4m3_types():
+    global _E4M3
+    if _E4M3 is None:
+        _E4M3 = _fp8_types()
+    return _E4M3
+
+
+def fp8_cols_pitch(rows: int, num_groups: int) -> int:
+    """Columns of a matrix that gmm_quantize_fp8_cols writes: every group starts a block of 128."""
+    return (rows // FP8_BLOCK + num_groups) * FP8_BLOCK
+
+
+def _gather(x, row_slots, types, device):
+    """x's pointer, stride and shape, row_slots' pointer, and the rows that are quantised."""
+    px, stride, (src_rows, width) = _check_strided(x, "x", types, device)
+    if row_slots is None:
+        return px, stride, src_rows, width, None, src_rows
+    return px, stride, src_rows, width, _ptr(row_slots, "row_slots", _I32, device), row_slots.numel()
+
+
+def gmm_quantize_fp8(h: Handle, q, scales, x, row_slots=None, top_k: int = 1, pow2: bool = False, stream=None,
+                     check: bool = True) -> int:
+    """Quantise the rows of x [src_rows, K] to e4m3 with an fp32 scale for each 128 of K: q [rows, K] (uint8 or
+    float8_e4m3fn), scales [rows, ceil(K / 128)], as gmm_run_fp8 takes them at granularity (1, ., 128).  With
+    row_slots (int32 [rows], gmm_dispatch's) row r is quantised from x[row_slots[r] // top_k]; a negative entry
+    leaves it untouched.  pow2: scales are powers of two."""
+    types, dev = _row_types(), h.device
+    px, stride, src_rows, K, ps, rows = _gather(x, row_slots, types, dev)
+    pq = _shaped(q, "q", _e4m3_types(), dev, (rows, K))
+    psc = _shaped(scales, "scales", _F32, dev, (rows, -(-K // FP8_BLOCK)))
+    rc = load_library().gmm_quantize_fp8(h.ptr, pq, psc, px, stride, src_rows, ps, int(top_k), rows, K, types[x.dtype],
+                                         int(bool(pow2)), stream_handle(dev, stream))
+    if check and rc != GMM_OK:
+        raise GmmError(rc, "gmm_quantize_fp8")
+    return rc
+
+
+def gmm_quantize_fp8_tiles(h: Handle, q, scales, w, pow2: bool = False, stream=None, check: bool = True) -> int:
+    """Quantise weights w [E, N, K] to e4m3 with an fp32 scale for each 128 x 128: q [E, N, K], scales
+    [E, ceil(N / 128), ceil(K / 128)], as gmm_run_fp8 takes them at granularity (., 128, 128)."""
+    types, dev = _row_types(), h.device
+    pw = _ptr(w, "w", types, dev)
+    shape = w.shape
+    if len(shape) != 3:
+        raise ValueError(f"w must be [E, N, K], got {tuple(shape)}")
+    E, N, K = shape
+    pq = _shaped(q, "q", _e4m3_types(), dev, shape)
+    psc = _shaped(scales, "scales", _F32, dev, (E, -(-N // FP8_BLOCK), -(-K // FP8_BLOCK)))
+    rc = load_library().gmm_quantize_fp8_tiles(h.ptr, pq, psc, pw, E, N, K, types[w.dtype], int(bool(pow2)),
+                                               stream_handle(dev, stream))
+    if check and rc != GMM_OK:
+        raise GmmError(rc, "gmm_quantize_fp8_tiles")
+    return rc
+
+
+def gmm_quantize_fp8_cols(h: Handle, q_t, t_scales, x, a_offsets, row_slots=None, top_k: int = 1, q=None, scales=None,
+                          stream=None, check: bool = True) -> int:
+    """Quantise x [src_rows, width] along the rows of each group of a_offsets [G + 1], transposed: q_t e4m3
+    [width, pitch] and t_scales uint8 [pitch / 128, width] (exponent codes) with pitch = fp8_cols_pitch(rows, G),
+    gmm_weight_grad_fp8's operands.  Row r stands in column (first / 128 + g) * 128 + r - first of its group g,
+    whose rows start at `first`.  row_slots as in gmm_quantize_fp8; with q and scales the rows' form is
+    written too, from the same read."""
+    types, dev = _row_types(), h.device
+    px, stride, src_rows, width, ps, rows = _gather(x, row_slots, types, dev)
+    po = _ptr(a_offsets, "a_offsets", _i32_types(), dev, 1)
+    G = a_offsets.numel() - 1
+    blocks = rows // FP8_BLOCK + G
+    pqt = _shaped(q_t, "q_t", _e4m3_types(), dev, (width, blocks * FP8_BLOCK))
+    pts = _shaped(t_scales, "t_scales", _U8, dev, (blocks, width))
+    pq = psc = None
+    if (q is None) != (scales is None):
+        raise ValueError("q and scales go together")
+    if q is not None:
+        pq = _shaped(q, "q", _e4m3_types(), dev, (rows, width))
+        psc = _shaped(scales, "scales", _F32, dev, (rows, -(-width // FP8_BLOCK)))
+    rc = load_library().gmm_quantize_fp8_cols(h.ptr, pqt, pts, pq, psc, px, stride, src_rows, ps, int(top_k), po, G, rows,
+                                              width, types[x.dtype], stream_handle(dev, stream))
+    if check and rc != GMM_OK:
+        raise GmmError(rc, "gmm_quantize_fp8_cols")
+    return rc
+
+
+def gmm_weight_grad_fp8(h: Handle, d_b, d_t, d_t_scales, a_t, a_t_scales, a_offsets, accumulate: bool = False, stream=None,
+                        check: bool = True) -> int:
+    """d_b[g, n, k] (+)= sum over the rows r of group g of d_c[r, n] * a[r, k]: d_b fp32 or bf16 [G, N, K], the
+    gradient of C (d_t [N, pitch]) and A (a_t [K, pitch]) as gmm_quantize_fp8_cols wrote them for a_offsets
+    [G + 1].  A group without rows gets zeros; accumulate (fp32 only) adds to d_b."""
+    types, dev = _row_types(), h.device
+    pd = _ptr(d_b, "d_b", (_F32[0], _BF16[0]), dev)
+    shape = d_b.shape
+    if len(shape) != 3:
+        raise ValueError(f"d_b must be [G, N, K], got {tuple(shape)}")
+    G, N, K = shape
+    po = _ptr(a_offsets, "a_offsets", _i32_types(), dev, G + 1)
+    if len(d_t.shape) != 2:
+        raise ValueError(f"d_t must be [N, pitch], got {tuple(d_t.shape)}")
+    pitch = d_t.shape[1]
+    blocks = pitch // FP8_BLOCK
+    rows = (blocks - G) * FP8_BLOCK + FP8_BLOCK - 1      # the most that this pitch holds
+    if pitch % FP8_BLOCK or rows < 0:
+        raise ValueError(f"d_t must have fp8_cols_pitch(rows, {G}) columns, got {pitch}")
+    pdt = _shaped(d_t, "d_t", _e4m3_types(), dev, (N, pitch))
+    pds = _shaped(d_t_scales, "d_t_scales", _U8, dev, (blocks, N))
+    pat = _shaped(a_t, "a_t", _e4m3_types(), dev, (K, pitch))
+    pas = _shaped(a_t_scales, "a_t_scales", _U8, dev, (blocks, K))
+    rc = load_library().gmm_weight_grad_fp8(h.ptr, pd, pdt, pds, pat, pas, po, G, rows if pitch else 0, N, K,
+                                            types[d_b.dtype], int(bool(accumulate)), stream_handle(dev, stream))
+    if check and rc != GMM_OK:
+        raise GmmError(rc, "gmm_weight_grad_fp8")
     return rc
 
 

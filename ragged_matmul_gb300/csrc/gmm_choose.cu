@@ -1,0 +1,159 @@
+// Host side of a router's choice and its gradient (gmm_route, gmm_route_grad): argument
+// checks, the kernel variant and the launch.
+#include <cmath>
+#include <type_traits>
+
+#include "gmm_choose.cuh"
+#include "gmm_host.h"
+
+namespace {
+
+using namespace gmm::host;
+
+// Warps a CTA: fewer where a warp's `smem` bytes (64-bit keys of every expert, rows of the
+// gradient) would not leave the default 48 KB.
+int choose_warps(size_t smem) {
+  return static_cast<int>(std::max<size_t>(1, std::min<size_t>(gmm::kChooseWarps, 48 * 1024 / std::max<size_t>(1, smem))));
+}
+
+template <class T, int L, int V>
+int launch_choose(const gmm::ChooseParams &p, bool vec, bool score, bool grad, cudaStream_t stream) {
+  const long long warps = (p.num_tokens + 32 / L - 1) / (32 / L);
+  const bool dense = p.scoring == GMM_SCORE_SOFTMAX && !p.renormalise;
+  const size_t per_warp = grad ? static_cast<size_t>(32) * V * 4 : (score ? static_cast<size_t>(p.num_experts) * 8 : 0);
+  const int wc = choose_warps(per_warp);
+  const unsigned grid = static_cast<unsigned>((warps + wc - 1) / wc), threads = 32u * wc;
+  const size_t smem = per_warp * wc;
+  auto go = [&](auto vec_c) {
+    constexpr bool kVec = decltype(vec_c)::value;
+    if (grad) {
+      if (dense) gmm::gmm_route_grad_kernel<T, L, V, kVec, true><<<grid, threads, smem, stream>>>(p);
+      else gmm::gmm_route_grad_kernel<T, L, V, kVec, false><<<grid, threads, smem, stream>>>(p);
+    } else if constexpr (L == 32) {
+      if (score) gmm::gmm_route_kernel<T, L, V, kVec, true><<<grid, threads, smem, stream>>>(p);
+      else gmm::gmm_route_kernel<T, L, V, kVec, false><<<grid, threads, smem, stream>>>(p);
+    } else {
+      gmm::gmm_route_kernel<T, L, V, kVec, false><<<grid, threads, smem, stream>>>(p);
+    }
+  };
+  if constexpr (V * sizeof(T) <= 128) {
+    if (vec) go(std::true_type()); else go(std::false_type());
+  } else {
+    go(std::false_type());
+  }
+  return launch_status(grad ? "launch of the route gradient kernel" : "launch of the route kernel");
+}
+
+template <class T>
+int run_choose(gmm_ctx *h, const gmm::ChooseParams &p, bool score, bool grad, cudaStream_t stream) {
+  // Lanes a token: a whole warp has the shortest way through one token; with many tokens fewer
+  // lanes leave fewer of them idle.
+  const int run = p.groups > 1 ? p.group_size : p.num_experts;           // consecutive experts
+  const int need = (run + p.group_lanes - 1) / p.group_lanes;            // a lane's share in a whole warp
+  const bool many = p.groups == 1 && !score && p.num_tokens > 16 * h->num_sms;
+  const unsigned long long at = reinterpret_cast<uintptr_t>(p.logits) | static_cast<unsigned long long>(p.logits_pitch) |
+                                reinterpret_cast<uintptr_t>(p.d_logits) | static_cast<unsigned long long>(p.d_pitch);
+  auto vec = [&](int v) { return run % v == 0 && at % std::min<size_t>(16, v * sizeof(T)) == 0; };
+  if (many && p.num_experts <= 64 && p.top_k <= 8) return launch_choose<T, 8, 8>(p, vec(8), score, grad, stream);
+  if (many && p.num_experts <= 128 && p.top_k <= 16) return launch_choose<T, 16, 8>(p, vec(8), score, grad, stream);
+  if (need <= 2) return launch_choose<T, 32, 2>(p, vec(2), score, grad, stream);
+  if (need <= 4) return launch_choose<T, 32, 4>(p, vec(4), score, grad, stream);
+  if (need <= 8) return launch_choose<T, 32, 8>(p, vec(8), score, grad, stream);
+  if (need <= 16) return launch_choose<T, 32, 16>(p, vec(16), score, grad, stream);
+  if (need <= 32) return launch_choose<T, 32, 32>(p, vec(32), score, grad, stream);
+  return launch_choose<T, 32, gmm::kChooseMaxPerLane>(p, false, score, grad, stream);
+}
+
+int check_route(gmm_ctx *h, gmm::ChooseParams &p, const void *logits, long long logits_stride, int num_tokens, int top_k,
+                int dtype, const gmm_route_options *o) {
+  if (!h || !o || num_tokens < 0 || top_k < 1 || logits_stride < 0 || !dtype_bytes(dtype)) return GMM_ERR_INVALID_ARG;
+  const int E = h->num_experts, es = dtype_bytes(dtype);
+  if (top_k > E || (o->scoring != GMM_SCORE_SOFTMAX && o->scoring != GMM_SCORE_SIGMOID)) return GMM_ERR_INVALID_ARG;
+  if (!(o->scale > 0.0f) || !(o->scale < INFINITY)) return GMM_ERR_INVALID_ARG;
+  if (top_k > gmm::kRouteMaxTopK || E > gmm::kRouteMaxExperts || static_cast<long long>(num_tokens) * top_k > (1ll << 30))
+    return GMM_ERR_UNSUPPORTED;
+  if (num_tokens > 0 && (!logits || !aligned_to(logits, es))) return GMM_ERR_INVALID_ARG;
+  std::memset(&p, 0, sizeof(p));
+  p.logits = static_cast<const uint8_t *>(logits);
+  p.logits_pitch = logits_stride * es;
+  p.num_tokens = num_tokens;
+  p.num_experts = E;
+  p.top_k = top_k;
+  p.scoring = o->scoring;
+  p.groups = 1;
+  p.group_size = E;
+  p.group_lanes = 32;
+  p.top_groups = 1;
+  p.group_top = 1;
+  p.renormalise = o->renormalise != 0;
+  p.scale = o->scale;
+  p.status = reinterpret_cast<uint32_t *>(h->ws);
+  return GMM_OK;
+}
+
+int run_choose_dtype(gmm_ctx *h, const gmm::ChooseParams &p, int dtype, bool score, bool grad, cudaStream_t stream) {
+  DeviceGuard guard(h->device);
+  switch (dtype) {
+    case GMM_DTYPE_BF16: return run_choose<__nv_bfloat16>(h, p, score, grad, stream);
+    case GMM_DTYPE_FP16: return run_choose<__half>(h, p, score, grad, stream);
+    default: return run_choose<float>(h, p, score, grad, stream);
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+int gmm_route(gmm_handle_t h, int32_t *slot_experts, float *weights, const void *logits, long long logits_stride,
+              const float *bias, int num_tokens, int top_k, int dtype, const gmm_route_options *options,
+              cudaStream_t stream) {
+  static_assert(GMM_SCORE_SOFTMAX == gmm::kScoreSoftmax && GMM_SCORE_SIGMOID == gmm::kScoreSigmoid,
+                "score functions of the C ABI and the kernel agree");
+  gmm::ChooseParams p;
+  int rc = check_route(h, p, logits, logits_stride, num_tokens, top_k, dtype, options);
+  if (rc) return rc;
+  const int E = h->num_experts, groups = options->expert_groups;
+  if (groups < 1 || E % groups || options->top_groups < 1 || options->top_groups > groups ||
+      (options->group_top != 1 && options->group_top != 2) || options->group_top > E / groups ||
+      top_k > options->top_groups * (E / groups) || !aligned_to(bias, 4))
+    return GMM_ERR_INVALID_ARG;
+  if (groups > gmm::kChooseMaxGroups) return GMM_ERR_UNSUPPORTED;
+  if (num_tokens > 0 && (!slot_experts || !weights || !aligned_to(slot_experts, 4) || !aligned_to(weights, 4)))
+    return GMM_ERR_INVALID_ARG;
+  p.bias = bias;
+  p.ids = slot_experts;
+  p.weights = weights;
+  if (options->top_groups < groups) {   // else every group is kept
+    p.groups = groups;
+    p.group_size = E / groups;
+    p.group_lanes = 1;
+    while (2 * p.group_lanes * groups <= 32) p.group_lanes *= 2;
+    p.top_groups = options->top_groups;
+    p.group_top = options->group_top;
+    if ((p.group_size + p.group_lanes - 1) / p.group_lanes > gmm::kChooseMaxPerLane) return GMM_ERR_UNSUPPORTED;
+  }
+  if (num_tokens == 0) return GMM_OK;
+  const bool score = p.bias != nullptr || (p.groups > 1 && p.group_top == 2);
+  return run_choose_dtype(h, p, dtype, score, false, stream);
+}
+
+int gmm_route_grad(gmm_handle_t h, void *d_logits, long long d_logits_stride, const float *d_weights,
+                   const int32_t *slot_experts, const void *logits, long long logits_stride, int num_tokens, int top_k,
+                   int dtype, const gmm_route_options *options, cudaStream_t stream) {
+  gmm::ChooseParams p;
+  int rc = check_route(h, p, logits, logits_stride, num_tokens, top_k, dtype, options);
+  if (rc) return rc;
+  if (num_tokens == 0) return GMM_OK;
+  const int es = dtype_bytes(dtype);
+  if (!d_logits || !d_weights || !slot_experts || !aligned_to(d_logits, es) || !aligned_to(d_weights, 4) ||
+      !aligned_to(slot_experts, 4) || d_logits_stride < 0)
+    return GMM_ERR_INVALID_ARG;
+  if (d_logits_stride < h->num_experts && num_tokens > 1) return GMM_ERR_INVALID_ARG;   // rows of the output overlap
+  p.ids = const_cast<int32_t *>(slot_experts);
+  p.weights = const_cast<float *>(d_weights);
+  p.d_logits = static_cast<uint8_t *>(d_logits);
+  p.d_pitch = d_logits_stride * es;
+  return run_choose_dtype(h, p, dtype, false, true, stream);
+}
+
+}  // extern "C"

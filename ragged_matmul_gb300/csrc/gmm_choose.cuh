@@ -1,0 +1,580 @@
+// A router's choice of experts and its gradient, for sm_103a.
+//
+// For token t with logits x_e (E experts) and a score function
+//   softmax   s_e = exp(x_e) / sum_i exp(x_i)
+//   sigmoid   s_e = 1 / (1 + exp(-x_e))
+// the experts are chosen by the key y_e = s_e + b_e (b: an optional bias that only the choice
+// sees):
+//   groups    the experts are `groups` equal runs; a group's key is the sum of its group_top (1
+//             or 2) largest y_e, and only the top_groups groups with the largest keys are kept;
+//   choice    the top_k largest y_e of the kept groups, in descending order;
+//   weights   w_j = scale * s_j, or scale * s_j / sum_i s_i over the chosen (renormalise).
+// Equal keys go to the lowest index.  An expert whose key is -infinity or NaN (a masked logit or
+// bias) is never chosen; slots that find no expert get id -1 and weight 0.  A token with a NaN
+// logit (or, with softmax, one of +infinity) gets none at all and is reported.
+//
+// Gradient, with g_j = scale * d w_j and the chosen ids given:
+//   renormalised, u_j = s_j / sum_i s_i:
+//     softmax   d x_j = u_j (g_j - sum_i u_i g_i)
+//     sigmoid   d x_j = u_j (g_j - sum_i u_i g_i) (1 - s_j)
+//   not renormalised:
+//     softmax   d x_e = s_e (sum_{j: id_j = e} g_j - sum_j s_j g_j)        (every expert)
+//     sigmoid   d x_j = g_j s_j (1 - s_j)
+// and zero elsewhere; slots that name an expert twice add up.
+//
+// The choice is that of the keys to 64-bit accuracy.  Without a bias the scores stand in the
+// order of the logits, which are compared themselves.  With one, the keys are computed in fp32;
+// two keys (or group keys) nearer than their error bounds, of different logit or bias, send the
+// token to a path that computes the candidates in 64 bits (about one token in a hundred at 256
+// experts), because fp32 sums of near keys would otherwise choose by their rounding.
+//
+// Bound by latency and, with many tokens, by instruction issue: L lanes hold a token's logits in
+// registers, V consecutive experts each, and take the maximum top_k times.  Keys are unsigned
+// words in the order of the values, so that a maximum over 32 lanes is one redux instruction.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstdint>
+#include <type_traits>
+
+#include "gmm_common.cuh"
+
+namespace gmm {
+
+constexpr int kScoreSoftmax = 0;
+constexpr int kScoreSigmoid = 1;
+constexpr int kChooseWarps = 4;
+constexpr int kChooseMaxGroups = 32;    // one lane at least holds a group
+constexpr int kChooseMaxPerLane = 128;  // logits a lane holds, at most
+
+struct ChooseParams {
+  const uint8_t *logits;        // [tokens, E], row pitch logits_pitch
+  long long logits_pitch;       // bytes
+  const float *bias;            // [E] or null
+  int32_t *ids;                 // [tokens, top_k]; the gradient's input
+  float *weights;               // [tokens, top_k]; gradient: d_weights
+  uint8_t *d_logits;            // gradient: [tokens, E], row pitch d_pitch
+  long long d_pitch;            // bytes
+  int num_tokens;
+  int num_experts;
+  int top_k;
+  int scoring;
+  int groups;
+  int group_size;               // experts per group
+  int group_lanes;              // lanes per group: 32 / (groups rounded up to a power of two)
+  int top_groups;
+  int group_top;
+  int renormalise;
+  float scale;
+  uint32_t *status;
+};
+
+__device__ __forceinline__ uint32_t redux_max(uint32_t x) {
+  uint32_t r;
+  asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// Maximum over the L lanes of a token.
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
+  if constexpr (L == 32) {
+    return redux_max(x);
+  } else {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+  }
+}
+
+template <int L>
+__device__ __forceinline__ float lanes_sum(float x) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Words in the order of the values, 0 for -infinity and NaN (never chosen); -0 counts as +0.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  const uint32_t k = (b & 0x80000000u) ? ~b : b | 0x80000000u;
+  return x > -INFINITY ? k : 0u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {   // its inverse; -infinity for 0
+  return k == 0u ? -INFINITY : __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+__device__ __forceinline__ unsigned long long order_key(double x) {
+  const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(x + 0.0));
+  const unsigned long long k = (b >> 63) ? ~b : b | (1ull << 63);
+  return x > -static_cast<double>(INFINITY) ? k : 0ull;
+}
+
+template <class T>
+__device__ __forceinline__ float choose_float(T x) {
+  if constexpr (std::is_same_v<T, float>) return x;
+  else if constexpr (std::is_same_v<T, __half>) return __half2float(x);
+  else return __bfloat162float(x);
+}
+
+// V consecutive logits of one token as fp32; -infinity past the lane's `n`.  kVec: the lane's run
+// is whole and aligned to its size, 16 bytes at most.
+template <class T, int V, bool kVec>
+__device__ __forceinline__ void choose_load(const T *row, int first, int n, float (&x)[V]) {
+  constexpr int kBytes = V * static_cast<int>(sizeof(T));
+  if constexpr (kVec) {
+    alignas(16) T raw[V];
+    if (n > 0) {
+      if constexpr (kBytes >= 16) {
+#pragma unroll
+        for (int i = 0; i < kBytes / 16; ++i)
+          reinterpret_cast<uint4 *>(raw)[i] = __ldg(reinterpret_cast<const uint4 *>(row + first) + i);
+      } else if constexpr (kBytes == 8) {
+        *reinterpret_cast<uint2 *>(raw) = __ldg(reinterpret_cast<const uint2 *>(row + first));
+      } else if constexpr (kBytes == 4) {
+        *reinterpret_cast<uint32_t *>(raw) = __ldg(reinterpret_cast<const uint32_t *>(row + first));
+      } else {
+        raw[0] = row[first];
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = n > 0 ? choose_float<T>(raw[v]) : -INFINITY;
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = v < n ? choose_float<T>(row[first + v]) : -INFINITY;
+  }
+}
+
+__device__ __forceinline__ float sigmoid32(float x) { return 1.0f / (1.0f + expf(-x)); }
+__device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
+
+// The largest two of a run of lanes, each lane with its own two.
+__device__ __forceinline__ void merge_top2(float &a1, float &a2, float b1, float b2) {
+  a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+  a1 = fmaxf(a1, b1);
+}
+
+// The choice of one token by 64-bit keys, by a whole warp: ids[j] for lane j < top_k.  Only the
+// experts whose fp32 key reaches `least` are looked at (all of them and the groups again where
+// `all` is set); `kept`: bit g, group g is kept.
+template <class T>
+__device__ __noinline__ int choose_exact(const ChooseParams &p, const T *row, float top, float z, float least, bool all,
+                                         uint32_t kept, unsigned long long *keys) {
+  const int lane = static_cast<int>(threadIdx.x & 31u), E = p.num_experts;
+  double zd = 0.0;
+  if (p.scoring == kScoreSoftmax) {
+    for (int e = lane; e < E; e += 32) zd += exp(static_cast<double>(choose_float<T>(row[e])) - static_cast<double>(top));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) zd += __shfl_xor_sync(0xffffffffu, zd, o);
+  }
+  for (int e = lane; e < E; e += 32) {
+    const float x = choose_float<T>(row[e]);
+    unsigned long long k = 0ull;
+    const float s = p.scoring == kScoreSoftmax ? expf(x - top) / z : sigmoid32(x);
+    const float b = p.bias != nullptr ? __ldg(p.bias + e) : 0.0f;
+    if (x > -INFINITY && (all || s + b >= least))
+      k = order_key((p.scoring == kScoreSoftmax ? exp(static_cast<double>(x) - static_cast<double>(top)) / zd
+                                                : sigmoid64(static_cast<double>(x))) +
+                    static_cast<double>(b));
+    keys[e] = k;
+  }
+  __syncwarp();
+  if (all && p.groups > 1) {   // lane g: group g's key
+    unsigned long long gk = 0ull;
+    if (lane < p.groups) {
+      unsigned long long m1 = 0ull, m2 = 0ull;
+      for (int i = 0; i < p.group_size; ++i) {
+        const unsigned long long k = keys[lane * p.group_size + i];
+        if (k > m1) {
+          m2 = m1;
+          m1 = k;
+        } else if (k > m2) {
+          m2 = k;
+        }
+      }
+      gk = m1;
+      if (p.group_top == 2 && m2 != 0ull) {
+        auto value = [](unsigned long long k) {
+          return __longlong_as_double(static_cast<long long>((k >> 63) ? k & ~(1ull << 63) : ~k));
+        };
+        gk = order_key(value(m1) + value(m2));
+      }
+    }
+    int rank = 0;
+    for (int g = 0; g < p.groups; ++g) {
+      const unsigned long long o = __shfl_sync(0xffffffffu, gk, g);
+      rank += o > gk || (o == gk && g < lane) ? 1 : 0;
+    }
+    kept = __ballot_sync(0xffffffffu, lane < p.groups && rank < p.top_groups);
+  }
+  if (p.bias == nullptr) {   // the experts themselves by their logits, which are exact
+    __syncwarp();
+    for (int e = lane; e < E; e += 32) keys[e] = order_key(static_cast<double>(choose_float<T>(row[e])));
+    __syncwarp();
+  }
+  int id = -1;
+  for (int j = 0; j < p.top_k; ++j) {
+    unsigned long long m = 0ull;
+    int at = E;
+    for (int e = lane; e < E; e += 32)
+      if (((kept >> (e / p.group_size)) & 1u) && keys[e] > m) {
+        m = keys[e];
+        at = e;
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const unsigned long long mo = __shfl_xor_sync(0xffffffffu, m, o);
+      const int ao = __shfl_xor_sync(0xffffffffu, at, o);
+      if (mo > m || (mo == m && ao < at)) {
+        m = mo;
+        at = ao;
+      }
+    }
+    if (m == 0ull) break;
+    if (lane == j) id = at;
+    if (lane == (at & 31)) keys[at] = 0ull;
+    __syncwarp();
+  }
+  __syncwarp();
+  return id;
+}
+
+// One token per L lanes, 32 / L tokens a warp.  kScore: a key that is not the logit itself is
+// compared (a bias, or groups by two scores); then L = 32.  16-bit logits that are compared
+// themselves carry the expert's number in the key's low half, so that a maximum is also its place.
+template <class T, int L, int V, bool kVec, bool kScore>
+__global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __grid_constant__ ChooseParams p) {
+  static_assert(!kScore || L == 32, "a score's token has a whole warp");
+  constexpr bool kPacked = !kScore && sizeof(T) == 2;
+  extern __shared__ unsigned long long choose_smem[];
+  const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
+  const int sub = lane & (L - 1), seg = lane & ~(L - 1);
+  const uint32_t seg_mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << seg;
+  const long long w = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + warp;   // fewer warps where they need much shared memory
+  const long long t = w * (32 / L) + lane / L;
+  if (w * (32 / L) >= p.num_tokens) return;   // the whole warp
+  const bool live = t < p.num_tokens;
+  const T *row = reinterpret_cast<const T *>(p.logits + (live ? t : 0) * p.logits_pitch);
+
+  // This lane's run of experts: of group `mine`, from `first`, n of them.
+  int mine = 0, first, n;   // V at most
+  if (p.groups > 1) {
+    mine = sub / p.group_lanes;
+    const int at = (sub - mine * p.group_lanes) * V;
+    first = mine * p.group_size + at;
+    n = mine < p.groups ? max(0, min(V, p.group_size - at)) : 0;
+  } else {
+    first = sub * V;
+    n = max(0, min(V, p.num_experts - first));
+  }
+  float x[V];
+  choose_load<T, V, kVec>(row, first, n, x);
+
+  // NaN (and, for softmax, +infinity) anywhere: no expert at all.
+  bool bad = false;
+#pragma unroll
+  for (int v = 0; v < V; ++v) bad |= !(x[v] < INFINITY) && (p.scoring == kScoreSoftmax || x[v] != x[v]);
+  bad = (__ballot_sync(0xffffffffu, bad) & seg_mask) != 0u;
+
+  uint32_t key[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if constexpr (kPacked) {   // fp32's order on the type's own 16 bits, then the lowest expert first
+      const uint32_t k = order_key(x[v]);
+      const uint32_t k16 = std::is_same_v<T, __half> ? 0u : k >> 16;
+      if constexpr (std::is_same_v<T, __half>) {
+        const uint32_t h = __half_as_ushort(__float2half_rn(x[v] + 0.0f));
+        key[v] = k == 0u ? 0u : ((((h & 0x8000u) ? ~h : h | 0x8000u) & 0xffffu) << 16) | (0xffffu - static_cast<uint32_t>(first + v));
+      } else {
+        key[v] = k == 0u ? 0u : (k16 << 16) | (0xffffu - static_cast<uint32_t>(first + v));
+      }
+    } else {
+      key[v] = order_key(x[v]);
+    }
+  }
+
+  // Softmax's maximum and sum, where a score itself is needed.
+  float top = 0.0f, z = 1.0f;
+  if (p.scoring == kScoreSoftmax && (kScore || !p.renormalise)) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < V; ++v) m = fmaxf(m, x[v]);
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    top = m > -INFINITY ? m : 0.0f;
+    float sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) sum += expf(x[v] - top);
+    z = lanes_sum<L>(sum);
+  }
+
+  float score_tol = 0.0f;   // two fp32 keys (of magnitude up to 1) are this near at least to be unsure of
+  bool unsure = false, unsure_groups = false;
+  uint32_t kept = 0xffffffffu;
+  if constexpr (kScore) {
+    // expf, the sum and the quotient are each off by a few units in the last place of values up to
+    // 1; z by one a term and lane; the bias adds half of one of the key.  Two keys, so twice that.
+    score_tol = p.scoring == kScoreSoftmax ? 1.2e-7f * (V + 16) : 6e-7f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (key[v] != 0u) {
+        const float s = p.scoring == kScoreSoftmax ? expf(x[v] - top) / z : sigmoid32(x[v]);
+        key[v] = order_key(s + (p.bias != nullptr ? __ldg(p.bias + first + v) : 0.0f));
+      }
+  }
+  if (p.groups > 1) {
+    float g1 = -INFINITY, g2 = -INFINITY;
+    if constexpr (kPacked) {
+      uint32_t m = 0u;
+#pragma unroll
+      for (int v = 0; v < V; ++v) m = max(m, key[v] >> 16);
+      g1 = m == 0u ? -INFINITY : static_cast<float>(m);   // any value in the keys' order
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) merge_top2(g1, g2, key_value(key[v]), -INFINITY);
+    }
+    for (int o = p.group_lanes / 2; o > 0; o >>= 1)
+      merge_top2(g1, g2, __shfl_xor_sync(0xffffffffu, g1, o), __shfl_xor_sync(0xffffffffu, g2, o));
+    const float gv = p.group_top == 2 && kScore && g2 > -INFINITY ? g1 + g2 : g1;
+    const uint32_t gk = mine < p.groups ? order_key(gv) : 0u;
+    int rank = 0;
+    for (int g = 0; g < p.groups; ++g) {
+      const uint32_t o = __shfl_sync(0xffffffffu, gk, seg + g * p.group_lanes);
+      rank += o > gk || (o == gk && g < mine) ? 1 : 0;
+    }
+    const bool keep = mine < p.groups && rank < p.top_groups;
+    if constexpr (kScore) {
+      // The last group kept and the first one left out.
+      const uint32_t out = redux_max(keep || mine >= p.groups ? 0u : gk);
+      const uint32_t in = ~redux_max(keep ? ~gk : 0u);
+      const float a = key_value(in), b = key_value(out);
+      unsure_groups = out != 0u && in != 0u && !(a - b > 2.0f * (score_tol + 2.4e-7f * fmaxf(fabsf(a), fabsf(b))));
+      uint32_t k = 0u;
+      for (int g = 0; g < p.groups; ++g)
+        k |= (__shfl_sync(0xffffffffu, keep ? 1u : 0u, g * p.group_lanes)) << g;
+      kept = k;
+      if (p.bias == nullptr)
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = order_key(x[v]);   // the experts by their logits
+    }
+    if (!keep)
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = 0u;
+  }
+
+  // top_k maxima; lane j keeps the j-th expert's number.
+  int id = -1;
+  float kth = 0.0f;
+  auto take = [&](int &e) -> uint32_t {   // the largest key left, and its expert
+    uint32_t m = key[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) m = max(m, key[v]);
+    const uint32_t M = lanes_max<L>(m);
+    if constexpr (kPacked) {
+      e = static_cast<int>(0xffffu - (M & 0xffffu));
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = key[v] == M ? 0u : key[v];
+    } else {
+      const uint32_t holders = __ballot_sync(0xffffffffu, m == M) & seg_mask;
+      const int owner = __ffs(static_cast<int>(holders)) - 1;   // the lowest expert's lane
+      int at = 0;
+      if (lane == owner) {
+        bool done = false;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (!done && key[v] == M) {
+            at = first + v;
+            key[v] = 0u;
+            done = true;
+          }
+      }
+      e = __shfl_sync(0xffffffffu, at, owner);
+    }
+    return M;
+  };
+  float prev_key = 0.0f, prev_x = 0.0f, prev_b = 0.0f;
+  for (int j = 0; j < p.top_k; ++j) {
+    int e;
+    const uint32_t M = take(e);
+    if (sub == j && M != 0u) id = e;
+    if (__all_sync(0xffffffffu, M == 0u)) break;
+    if constexpr (kScore) {
+      if (p.bias != nullptr && M != 0u) {
+        const float k = key_value(M), xe = choose_float<T>(row[e]), be = __ldg(p.bias + e);
+        if (j > 0 && !(prev_key - k > score_tol + 2.4e-7f * fabsf(prev_key)) && !(prev_x == xe && prev_b == be)) unsure = true;
+        prev_key = k;
+        prev_x = xe;
+        prev_b = be;
+        kth = k;
+      }
+    }
+  }
+  if constexpr (kScore) {
+    if (p.bias != nullptr && __shfl_sync(0xffffffffu, id, p.top_k - 1) >= 0) {   // every slot is filled: who came next?
+      const float tol = score_tol + 2.4e-7f * fabsf(kth);
+      for (int i = 0; i < p.num_experts; ++i) {
+        int e;
+        const uint32_t M = take(e);
+        if (M == 0u || kth - key_value(M) > tol) break;
+        if (!(choose_float<T>(row[e]) == prev_x && __ldg(p.bias + e) == prev_b)) {
+          unsure = true;
+          break;
+        }
+      }
+    }
+    if ((unsure || unsure_groups) && !bad) {
+      // Every fp32 key that might belong among the chosen ones.
+      const bool full = __shfl_sync(0xffffffffu, id, p.top_k - 1) >= 0;
+      const float least = full && kth < INFINITY ? kth - 2.0f * (score_tol + 2.4e-7f * fabsf(kth)) : -INFINITY;
+      id = choose_exact<T>(p, row, top, z, least, unsure_groups || p.bias == nullptr, kept,
+                           choose_smem + static_cast<size_t>(warp) * p.num_experts);
+    }
+  }
+  if (bad) {
+    id = -1;
+    if (live && sub == 0) atomicOr(p.status, kStatusBadLogit);
+  }
+
+  // Weights.
+  const float xj = id >= 0 ? choose_float<T>(row[id]) : -INFINITY;
+  float wj;
+  if (p.renormalise) {
+    // Scores relative to the largest chosen logit's: the sum is not below 1 (softmax).  Sigmoids of
+    // logits below -80 are exp(x) to within their last bit, and taken so before they underflow.
+    float m = xj;
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (id < 0) wj = 0.0f;
+    else wj = p.scoring == kScoreSoftmax || m < -80.0f ? expf(xj - m) : sigmoid32(xj);
+    const float sum = lanes_sum<L>(wj);
+    if (id >= 0) wj = wj / sum;
+  } else {
+    wj = id < 0 ? 0.0f : (p.scoring == kScoreSoftmax ? expf(xj - top) / z : sigmoid32(xj));
+  }
+  if (live && sub < p.top_k) {
+    const long long s = t * p.top_k + sub;
+    p.ids[s] = id;
+    p.weights[s] = id < 0 ? 0.0f : wj * p.scale;
+  }
+}
+
+// The gradient.  L lanes a token; a token's row of d_logits is put together in shared memory (zeros,
+// then the chosen experts') and written V consecutive experts a lane; kDense (softmax, not
+// renormalised): every logit is read, and every expert's value is its score times a difference.
+template <class T, int L, int V, bool kVec, bool kDense>
+__global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_grad_kernel(const __grid_constant__ ChooseParams p) {
+  extern __shared__ __align__(16) float choose_row[];
+  const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
+  const int sub = lane & (L - 1), seg = lane & ~(L - 1);
+  const long long w = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + warp;   // fewer warps where they need much shared memory
+  const long long t = w * (32 / L) + lane / L;
+  if (w * (32 / L) >= p.num_tokens) return;
+  const bool live = t < p.num_tokens;
+  const T *row = reinterpret_cast<const T *>(p.logits + (live ? t : 0) * p.logits_pitch);
+  float *buf = choose_row + (static_cast<size_t>(warp) * (32 / L) + lane / L) * (L * V);
+  const int first = sub * V, n = max(0, min(V, p.num_experts - first));
+
+  int id = -1;
+  float g = 0.0f, xj = -INFINITY;
+  if (live && sub < p.top_k) {
+    id = __ldg(p.ids + t * p.top_k + sub);
+    if (id >= p.num_experts) {
+      atomicOr(p.status, kStatusBadExpert);
+      id = -1;
+    }
+    if (id >= 0) {
+      g = __ldg(p.weights + t * p.top_k + sub) * p.scale;
+      xj = choose_float<T>(row[id]);
+      if (xj == -INFINITY) id = -1;   // a score of zero: no gradient, and none through the others' sum
+    }
+  }
+  float x[V];
+  float top = 0.0f, z = 1.0f;
+  bool bad = id >= 0 && (!(xj < INFINITY) && (p.scoring == kScoreSoftmax || xj != xj));
+  if constexpr (kDense) {
+    choose_load<T, V, kVec>(row, first, n, x);
+    float m = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      bad |= !(x[v] < INFINITY);
+      m = fmaxf(m, x[v]);
+    }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    top = m > -INFINITY ? m : 0.0f;
+    float sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      x[v] = expf(x[v] - top);
+      sum += x[v];
+    }
+    z = lanes_sum<L>(sum);
+  }
+  const uint32_t bads = __ballot_sync(0xffffffffu, bad);
+  bad = ((L == 32 ? bads : (bads >> seg) & ((1u << (L & 31)) - 1u))) != 0u;
+  if (bad) {   // such a token has no experts: no gradient
+    id = -1;
+    if (live && sub == 0) atomicOr(p.status, kStatusBadLogit);
+  }
+  float dj = 0.0f, common = 0.0f;
+  if constexpr (kDense) {
+    dj = id >= 0 ? g : 0.0f;
+    common = lanes_sum<L>(id >= 0 ? g * (expf(xj - top) / z) : 0.0f);
+  } else if (p.renormalise) {
+    float m = id >= 0 ? xj : -INFINITY;
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const bool ratio = p.scoring == kScoreSoftmax || m < -80.0f;
+    const float s = id >= 0 ? (ratio ? expf(xj - m) : sigmoid32(xj)) : 0.0f;
+    const float sum = lanes_sum<L>(s);
+    const float u = id >= 0 ? s / sum : 0.0f;
+    const float mean = lanes_sum<L>(id >= 0 ? u * g : 0.0f);
+    dj = id >= 0 ? u * (g - mean) : 0.0f;
+    if (p.scoring == kScoreSigmoid) dj *= sigmoid32(-xj);
+  } else if (id >= 0) {
+    dj = g * sigmoid32(xj) * sigmoid32(-xj);
+  }
+  if (id < 0) dj = 0.0f;
+
+  if constexpr (V % 4 == 0) {
+#pragma unroll
+    for (int v = 0; v < V; v += 4) *reinterpret_cast<float4 *>(buf + first + v) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) buf[first + v] = 0.0f;
+  }
+  __syncwarp();
+  // A lane whose expert an earlier slot names too adds after it, in the slots' order.
+  for (int j = 0; j < p.top_k; ++j) {
+    if (sub == j && id >= 0) buf[id] += dj;
+    __syncwarp();
+  }
+  if (!live) return;
+  T *out = reinterpret_cast<T *>(p.d_logits + t * p.d_pitch) + first;
+  alignas(16) T y[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float d = buf[first + v];
+    if constexpr (kDense) d = bad || z == 0.0f ? 0.0f : x[v] / z * (d - common);   // z = 0: every logit is masked
+    y[v] = route_from_float<T>(d);
+  }
+  constexpr int kBytes = V * static_cast<int>(sizeof(T));
+  if (kVec && n > 0) {
+    if constexpr (kBytes >= 16) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i) reinterpret_cast<uint4 *>(out)[i] = reinterpret_cast<const uint4 *>(y)[i];
+    } else if constexpr (kBytes == 8) {
+      *reinterpret_cast<uint2 *>(out) = *reinterpret_cast<const uint2 *>(y);
+    } else if constexpr (kBytes == 4) {
+      *reinterpret_cast<uint32_t *>(out) = *reinterpret_cast<const uint32_t *>(y);
+    } else {
+      out[0] = y[0];
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (v < n) out[v] = y[v];
+  }
+}
+
+}  // namespace gmm

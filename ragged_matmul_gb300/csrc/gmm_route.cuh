@@ -21,19 +21,15 @@
 #include <cstdint>
 #include <type_traits>
 
-#include "gmm_kernel.cuh"
+#include "gmm_common.cuh"
 
 namespace gmm {
 
-constexpr uint32_t kStatusBadSlot = 16u;   // a slot_rows / row_slots value outside its range
-
 constexpr int kRouteThreads = 512;
 constexpr int kRouteWarps = kRouteThreads / 32;
-constexpr int kRouteMaxTopK = 32;          // a token's slots are held one per lane
 constexpr int kRouteMaxWidth = 0x7fffffff - 4095;   // columns are counted in 32 bits, by steps of up to 2048 past the last one
 constexpr int kRouteSmallSlots = 4096;     // up to here (and kRouteSmallExperts) one launch sorts and copies
 constexpr int kRouteSmallExperts = 1024;
-constexpr int kRouteMaxExperts = 4096;     // one group per expert: the grouped kernels' limit
 constexpr int kRouteMaxCounts = 32768;     // chunk counts (chunks x experts) in the workspace
 constexpr int kRouteMaxChunks = 152;
 constexpr long long kRoutePrefetch = 64 * 1024;   // bytes of its tokens that a CTA prefetches while the count runs
@@ -349,15 +345,6 @@ struct CombineParams {
   int warps_per_token;         // gradient
   uint32_t *status;
 };
-
-template <class T>
-__device__ __forceinline__ T route_from_float(float x);
-template <>
-__device__ __forceinline__ float route_from_float(float x) { return x; }
-template <>
-__device__ __forceinline__ __half route_from_float(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 route_from_float(float x) { return __float2bfloat16_rn(x); }
 
 // VN consecutive elements of type T as loaded: 16 bytes, or one element.
 template <class T, int VN>

@@ -757,6 +757,34 @@ __device__ __forceinline__ void mma_half_stage_e2m1_pair(uint32_t d_tmem, uint32
 #undef GMM_F4_MMA
 #undef GMM_F4_HEAD
 
+// One stage (128 of K) of the 8-bit block-scaled kernel: the copies of its scales to tensor memory,
+// as above (the first operand's 128 rows' atom, then the second's one or two), four pair MMAs of e4m3
+// operands (kind::mxf8f6f4, K = 32: 32 bytes of each 128-byte swizzled row; a scale word's four bytes
+// are the same, so scale id 0 serves all of them), and a commit to both CTAs' `empty`.  `two` = 0
+// leaves out the second operand's second atom (at most 128 rows).
+#define GMM_E4_MMA(K2, P)                                                                                  \
+  "add.u32 x, %1, " K2 ";\n\tmov.b64 a, {x, %3};\n\tadd.u32 x, %2, " K2 ";\n\tmov.b64 b, {x, %3};\n\t"       \
+  "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a, b, %4, [%7], [%8], " P ";\n\t"
+#define GMM_E4_CP(T, OFF, SOFF, P)                                                                         \
+  "add.u32 x, " T ", " OFF ";\n\tadd.u32 y, %5, " SOFF ";\n\tmov.b64 s, {y, %6};\n\t"                     \
+  "@" P " tcgen05.cp.cta_group::2.32x128b.warpx4 [x], s;\n\t"
+__device__ __forceinline__ void mma_stage_e4m3_mx_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t ab_hi,
+                                                       uint32_t idesc, uint32_t s_lo, uint32_t s_hi, uint32_t sfa,
+                                                       uint32_t sfb, uint32_t accumulate, uint32_t two, uint32_t empty) {
+  asm volatile(
+      "{\n\t.reg .pred e, p, t, q;\n\t.reg .b32 l, x, y;\n\t.reg .b64 a, b, s;\n\t"
+      "elect.sync l|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %9, 0;\n\tsetp.eq.b32 t, %9, %9;\n\tsetp.ne.b32 q, %10, 0;\n\tand.pred q, q, e;\n\t"
+      GMM_E4_CP("%7", "0", "0", "e") GMM_E4_CP("%8", "0", "32", "e") GMM_E4_CP("%8", "4", "64", "q")
+      GMM_E4_MMA("0", "p") GMM_E4_MMA("2", "t") GMM_E4_MMA("4", "t") GMM_E4_MMA("6", "t")
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%11], %12;\n\t}"
+      ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(ab_hi), "r"(idesc), "r"(s_lo), "r"(s_hi), "r"(sfa), "r"(sfb),
+      "r"(accumulate), "r"(two), "r"(empty), "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+#undef GMM_E4_CP
+#undef GMM_E4_MMA
+
 // ----------------------------------------------------------------- descriptors
 
 // Shared-memory descriptor of 32 rows x 16 bytes for the copy above: no swizzle, 8-row core
@@ -814,6 +842,16 @@ __host__ __device__ constexpr uint32_t idesc_e2m1_f32(uint32_t M, uint32_t N, bo
          | ((e8m0 ? 1u : 0u) << 23)      // scale format
          | ((M >> 4) << 24)              // M / 16
          | (sf_id << 29);                // A scale id
+}
+
+// Instruction descriptor, kind::mxf8f6f4: e4m3 A and B (both K-major), fp32 D, shape M x N, e8m0
+// block scales, the scale words' byte 0 for both operands.
+__host__ __device__ constexpr uint32_t idesc_e4m3_mx_f32(uint32_t M, uint32_t N) {
+  return (0u << 7)              // A format: e4m3
+         | (0u << 10)           // B format: e4m3
+         | ((N >> 3) << 17)     // N / 8
+         | (1u << 23)           // scale format: e8m0
+         | ((M >> 4) << 24);    // M / 16
 }
 
 }  // namespace gmm
