@@ -243,6 +243,15 @@ __device__ __forceinline__ float quant_value8(const QuantRaw8<T> &r, int i) {
   else return __uint_as_float((i & 1) ? r.w[i / 2] & 0xffff0000u : r.w[i / 2] << 16);
 }
 
+// The element negated, its sign flipped in the word so that -0 keeps it.
+template <class T>
+__device__ __forceinline__ float quant_negated8(const QuantRaw8<T> &r, int i) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(r.w[i] ^ 0x80000000u);
+  const uint32_t w = r.w[i / 2] ^ 0x80008000u;
+  if constexpr (std::is_same_v<T, __half>) return __half2float(__ushort_as_half(static_cast<unsigned short>(w >> (16 * (i & 1)))));
+  else return __uint_as_float((i & 1) ? w & 0xffff0000u : w << 16);
+}
+
 // Magnitudes in the order of fp32's bits: of 16-bit types two to a word, compared as they stand.
 template <class T>
 struct QuantMax8 { uint32_t w[sizeof(T) * 2]; };
@@ -269,11 +278,12 @@ __device__ __forceinline__ uint32_t quant_bits(uint32_t m) {
 // of 8 rows from 8 rg, so that a warp's load is two whole row pieces, a column's codes of 8 rows are
 // 8 bytes of the transposed tile in shared memory, and a row's codes of 8 columns 8 bytes of q.
 template <class T, bool kVec, bool kBoth>
-__global__ void __launch_bounds__(kQ8Threads) gmm_quantize_fp8_cols_kernel(const __grid_constant__ Quant8Params p) {
+__global__ void __launch_bounds__(kQ8Threads, sizeof(T) == 2 ? 4 : 2) gmm_quantize_fp8_cols_kernel(const __grid_constant__ Quant8Params p) {
   constexpr int kWords = sizeof(T) * 2, kWarps = kQ8Threads / 32;
   __shared__ __align__(16) uint8_t tile[kQ8Block * kQ8Block];
   __shared__ uint32_t part[kWarps][kWords * 16];
   __shared__ __align__(16) float inv[kQ8Block];
+  __shared__ float2 row_scale[kQ8Block];
   __shared__ int source[kQ8Block];
   __shared__ uint32_t s_first, s_rows;
   const int tid = threadIdx.x, cv = tid & 15, rg = tid >> 4, lane = tid & 31, warp = tid >> 5;
@@ -331,34 +341,56 @@ __global__ void __launch_bounds__(kQ8Threads) gmm_quantize_fp8_cols_kernel(const
     for (int k = 0; k < kWords; ++k) part[warp][cv * kWords + k] = m[k];
 
   if constexpr (kBoth) {
+    // Largest magnitudes of the rows, over 16 lanes: every step halves the rows that a lane has left,
+    // so that two lanes end with each row, and its division is made once instead of in every lane.
+    uint32_t a[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      uint32_t a = 0;
+      a[i] = 0;
 #pragma unroll
-      for (int k = 0; k < kWords; ++k) a = quant_mag<T>(a, raw[i].w[k]);
-      if constexpr (sizeof(T) == 2) a = max(a & 0xffffu, a >> 16);
+      for (int k = 0; k < kWords; ++k) a[i] = quant_mag<T>(a[i], raw[i].w[k]);
+      if constexpr (sizeof(T) == 2) a[i] = max(a[i] & 0xffffu, a[i] >> 16);
+    }
+    int mine = 0;   // this lane's row of the eight
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-      const Quant8Scale c = quant8_scale<false>(quant_bits<T>(a));
-      if (!live[i]) continue;
-      const size_t row = first + static_cast<uint32_t>(rg * 8 + i);
-      if (cv == 0) p.scales[row * p.blocks + cb] = c.s;
-      if (!in) continue;
-      float y[8];
-      if (c.how == 2) {
+    for (int half = 4; half > 0; half >>= 1) {
+      const bool up = (lane & (2 * half)) != 0;
+      mine += up ? half : 0;
+#pragma unroll
+      for (int i = 0; i < half; ++i) {
+        const uint32_t sent = up ? a[i] : a[i + half], kept = up ? a[i + half] : a[i];
+        a[i] = max(kept, __shfl_xor_sync(0xffffffffu, sent, 2 * half));
+      }
+    }
+    a[0] = max(a[0], __shfl_xor_sync(0xffffffffu, a[0], 1));
+    const Quant8Scale c = quant8_scale<false>(quant_bits<T>(a[0]));
+    const int r = rg * 8 + mine;
+    if ((lane & 1) == 0) {
+      row_scale[r] = make_float2(c.s, c.how == 3 ? -1.0f : c.r);   // -1: divide; 0: all codes are zero
+      if (static_cast<uint32_t>(r) < n && (p.row_slots == nullptr || source[r] >= 0))
+        p.scales[static_cast<size_t>(first + static_cast<uint32_t>(r)) * p.blocks + cb] = c.s;
+    }
+    __syncwarp();
+    uint8_t *out = p.q + static_cast<size_t>(first + static_cast<uint32_t>(rg * 8)) * p.width + col;
+#pragma unroll
+    for (int i = 0; i < 8; ++i, out += p.width) {
+      if (!live[i] || !in) continue;
+      const float2 f = row_scale[rg * 8 + i];
+      float v[8], y[8];   // -x, and x / s
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = quant_negated8<T>(raw[i], j);
+      if (f.y > 0.0f) {
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-          float v0 = -quant_value8<T>(raw[i], j), v1 = -quant_value8<T>(raw[i], j + 1);
-          mul_f32x2(y[j], y[j + 1], -c.r, v0, v1);
-          fma_f32x2(v0, v1, c.s, y[j], y[j + 1]);
-          fma_f32x2(y[j], y[j + 1], -c.r, v0, v1);
+          mul_f32x2(y[j], y[j + 1], -f.y, v[j], v[j + 1]);
+          fma_f32x2(v[j], v[j + 1], f.x, y[j], y[j + 1]);
+          fma_f32x2(y[j], y[j + 1], -f.y, v[j], v[j + 1]);
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = c.how == 3 ? __fdiv_rn(quant_value8<T>(raw[i], j), c.s) : 0.0f;
+        for (int j = 0; j < 8; ++j) y[j] = f.y < 0.0f ? __fdiv_rn(-v[j], f.x) : 0.0f;
       }
-      *reinterpret_cast<uint2 *>(p.q + row * p.width + col) =
-          make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
+      *reinterpret_cast<uint2 *>(out) = make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
     }
   }
   __syncthreads();
