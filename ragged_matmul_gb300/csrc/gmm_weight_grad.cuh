@@ -13,9 +13,11 @@
 //
 // Scales.  A stage needs one byte per operand row; the MMA takes a 32-bit word per row (four scales,
 // here the same byte) from tensor memory, row m in lane m % 32 and column m / 32.  Warps load the
-// bytes a few stages ahead, and write each 128 rows' words as a 512-byte atom that tcgen05.cp
-// spreads over the lane quadrants, in order with the MMAs.  Both CTAs hold the scales of all of
-// the tile's k and of their own 128 n.
+// bytes ahead, four stages at a time, and write each 128 rows' words as a 512-byte atom that
+// tcgen05.cp spreads over the lane quadrants, in order with the MMAs.  Both CTAs hold the scales of
+// all of the tile's k and of their own 128 n.  They have a ring of their own, of entries of four
+// stages: the way of a scale (a freed entry, the peer's warps, its forwarder, the leader) takes
+// longer than the values' ring is deep.
 //
 // Roles (288 threads per CTA):
 //   warp 0       TMA producer of both operands' codes;
@@ -43,15 +45,17 @@ constexpr uint32_t kWgUnit = 16;                             // widths are multi
 constexpr uint32_t kWgABytes = kBlockN * kWgBlock;           // a CTA's 128 n
 constexpr uint32_t kWgBBytes = kWgMaxK / 2 * kWgBlock;       // a CTA's half of the k
 constexpr uint32_t kWgAtom = 512;                            // scale words of 128 rows
-constexpr uint32_t kWgScaleBytes = 3 * kWgAtom;
-constexpr uint32_t kWgStageBytes = kWgABytes + kWgBBytes + kWgScaleBytes;
+constexpr uint32_t kWgScaleBytes = 3 * kWgAtom;              // a stage's
+constexpr int kWgAhead = 4;                                  // stages of an entry of the scales' ring
+constexpr uint32_t kWgEntryBytes = kWgAhead * kWgScaleBytes;
+constexpr uint32_t kWgEntries = 4;
+constexpr uint32_t kWgStageBytes = kWgABytes + kWgBBytes;
 constexpr uint32_t kWgAccCols = kWgMaxK;
 constexpr uint32_t kWgScaleCol = 2 * kWgAccCols;
 constexpr uint32_t kWgStgBytes = 32 * 32 * 4;                // one staging buffer: 32 n x 32 k in fp32
 constexpr uint32_t kWgStgBufs = 2;                           // per epilogue warp
 constexpr int kWgMaxStages = 8;
-constexpr int kWgAhead = 4;                                  // stages of scales in registers
-constexpr size_t kWgFixedBytes = 1024 + kWgEpiWarps * kWgStgBufs * kWgStgBytes;
+constexpr size_t kWgFixedBytes = 1024 + kWgEpiWarps * kWgStgBufs * kWgStgBytes + kWgEntries * kWgEntryBytes;
 static_assert(kWgScaleCol + 12 <= kTmemCols, "scales beside the accumulators");
 static_assert(kWgABytes % 1024 == 0 && kWgBBytes % 1024 == 0 && kWgStgBytes % 1024 == 0, "swizzled tiles start at 1024 bytes");
 
@@ -103,9 +107,11 @@ __device__ __forceinline__ WgTile wg_tile(const WeightGradParams &p, const uint3
 }
 
 struct __align__(16) WgCtrl {
-  uint64_t full[kWgMaxStages];       // leader: both CTAs' bytes, its scale warps, the peer's forwarder
+  uint64_t full[kWgMaxStages];       // leader: both CTAs' bytes
   uint64_t empty[kWgMaxStages];      // the MMAs that read the stage completed (both CTAs)
-  uint64_t scales_in[kWgMaxStages];  // peer: its scale warps have written a stage's atoms
+  uint64_t scales_full[kWgEntries];  // leader: its scale warps, the peer's forwarder
+  uint64_t scales_empty[kWgEntries]; // the copies that read the entry completed (both CTAs)
+  uint64_t scales_in[kWgEntries];    // peer: its scale warps have written an entry
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
   uint32_t tmem_base;
@@ -151,7 +157,6 @@ __device__ __forceinline__ void wg_stage_row(uint32_t stg, uint32_t r, const uin
 
 template <bool kBf16>
 __global__ void __launch_bounds__(kWgThreads, 1) gmm_weight_grad_fp8_kernel(const __grid_constant__ WeightGradParams p) {
-  constexpr uint32_t kFullArrivals = 1 + kWgScaleWarps + 1;
   __shared__ WgCtrl ctl;
   extern __shared__ uint8_t dyn_smem[];
   const int tid = threadIdx.x, lane = tid & 31;
@@ -164,13 +169,17 @@ __global__ void __launch_bounds__(kWgThreads, 1) gmm_weight_grad_fp8_kernel(cons
   const uint32_t b_ring = a_ring + ST * kWgABytes;
   const uint32_t stg_ring = b_ring + ST * kWgBBytes;
   const uint32_t s_ring = stg_ring + kWgEpiWarps * kWgStgBufs * kWgStgBytes;
-  uint32_t *off = reinterpret_cast<uint32_t *>(dyn_smem + (s_ring + ST * kWgScaleBytes - dyn_base));
+  uint32_t *off = reinterpret_cast<uint32_t *>(dyn_smem + (s_ring + kWgEntries * kWgEntryBytes - dyn_base));
 
   if (tid == 0) {
     set_wait_limit(p.wait_limit_ns);
     for (uint32_t s = 0; s < ST; ++s) {
-      mbar_init(smem_addr(&ctl.full[s]), kFullArrivals);
+      mbar_init(smem_addr(&ctl.full[s]), 1);
       mbar_init(smem_addr(&ctl.empty[s]), 1);
+    }
+    for (uint32_t s = 0; s < kWgEntries; ++s) {
+      mbar_init(smem_addr(&ctl.scales_full[s]), kWgScaleWarps + 1);
+      mbar_init(smem_addr(&ctl.scales_empty[s]), 1);
       mbar_init(smem_addr(&ctl.scales_in[s]), kWgScaleWarps);
     }
     for (int a = 0; a < 2; ++a) {
@@ -243,7 +252,7 @@ __global__ void __launch_bounds__(kWgThreads, 1) gmm_weight_grad_fp8_kernel(cons
   } else if (warp == 1) {
     if (rank == 0) {
       // ---------------------------------------------------------- scale copies and MMAs (leader)
-      Ring rt;
+      Ring rt, rs;
       uint32_t acc = 0, acc_phase = 0;
       bool ok = true;
       const uint64_t a_desc = smem_desc_k_sw128(a_ring), b_desc = smem_desc_k_sw128(b_ring);
@@ -252,6 +261,7 @@ __global__ void __launch_bounds__(kWgThreads, 1) gmm_weight_grad_fp8_kernel(cons
       const uint32_t v_hi = static_cast<uint32_t>(a_desc >> 32);
       const uint32_t s_lo = static_cast<uint32_t>(s_desc), s_hi = static_cast<uint32_t>(s_desc >> 32);
       const uint32_t full0 = smem_addr(&ctl.full[0]), empty0 = smem_addr(&ctl.empty[0]);
+      const uint32_t s_full0 = smem_addr(&ctl.scales_full[0]), s_empty0 = smem_addr(&ctl.scales_empty[0]);
       const uint32_t sfa = tmem_base + kWgScaleCol, sfb = sfa + 4u;
       for (uint32_t t = unit0; t < total && ok; t += units) {
         const WgTile x = wg_tile(p, off, t);
@@ -264,11 +274,20 @@ __global__ void __launch_bounds__(kWgThreads, 1) gmm_weight_grad_fp8_kernel(cons
         const uint32_t d_tmem = tmem_base + acc * kWgAccCols;
         const uint32_t idesc = idesc_e4m3_mx_f32(kWgTileN, x.width), two = x.width > 128u;
         for (uint32_t kb = 0; kb < x.stages; ++kb) {
-          if (!__all_sync(0xffffffffu, wait_phase_cluster(full0 + rt.slot * 8u, rt.phase, abort))) { ok = false; break; }
+          const uint32_t in = kb % kWgAhead;
+          bool there = true;
+          if (in == 0) there = wait_phase_cluster(s_full0 + rs.slot * 8u, rs.phase, abort);
+          there = there && wait_phase_cluster<true>(full0 + rt.slot * 8u, rt.phase, abort);
+          if (!__all_sync(0xffffffffu, there)) { ok = false; break; }
           tc_fence_after_sync();
           mma_stage_e4m3_mx_pair(d_tmem, a_lo + rt.slot * (kWgABytes >> 4), b_lo + rt.slot * (kWgBBytes >> 4), v_hi, idesc,
-                                 s_lo + rt.slot * (kWgScaleBytes >> 4), s_hi, sfa, sfb, kb != 0, two, empty0 + rt.slot * 8u);
+                                 s_lo + ((rs.slot * kWgEntryBytes + in * kWgScaleBytes) >> 4), s_hi, sfa, sfb, kb != 0, two,
+                                 empty0 + rt.slot * 8u);
           rt.next(ST);
+          if (in == kWgAhead - 1 || kb + 1 == x.stages) {
+            mma_commit_pair(s_empty0 + rs.slot * 8u, 0x3);
+            rs.next(kWgEntries);
+          }
         }
         if (!ok) break;
         mma_commit_pair(smem_addr(&ctl.acc_full[acc]), 0x3);
@@ -279,15 +298,15 @@ __global__ void __launch_bounds__(kWgThreads, 1) gmm_weight_grad_fp8_kernel(cons
     } else if (lane == 0) {
       // The peer's scales to the leader, whose MMA warp issues the copies that read them: acquired
       // in this CTA, released at cluster scope.
-      const uint32_t full0 = map_to_rank(smem_addr(&ctl.full[0]), 0);
-      Ring rt;
+      const uint32_t full0 = map_to_rank(smem_addr(&ctl.scales_full[0]), 0);
+      Ring rs;
       bool ok = true;
       for (uint32_t t = unit0; t < total && ok; t += units) {
         const uint32_t stages = wg_tile(p, off, t).stages;
-        for (uint32_t kb = 0; kb < stages; ++kb) {
-          if (!wait_phase(smem_addr(&ctl.scales_in[rt.slot]), rt.phase, abort)) { ok = false; break; }
-          mbar_arrive_cluster_shared(full0 + rt.slot * 8u);
-          rt.next(ST);
+        for (uint32_t kb = 0; kb < stages; kb += kWgAhead) {
+          if (!wait_phase(smem_addr(&ctl.scales_in[rs.slot]), rs.phase, abort)) { ok = false; break; }
+          mbar_arrive_cluster_shared(full0 + rs.slot * 8u);
+          rs.next(kWgEntries);
         }
       }
       if (!ok) atomicOr(p.status, kStatusTimeout);
@@ -361,11 +380,11 @@ __global__ void __launch_bounds__(kWgThreads, 1) gmm_weight_grad_fp8_kernel(cons
     // ------------------------------------------------------------ scales
     // Rows past the matrix repeat its last one (their results are not stored).
     const uint32_t role = static_cast<uint32_t>(warp) - kWgFirstScaleWarp;
-    const uint32_t written0 = smem_addr(rank == 0 ? &ctl.full[0] : &ctl.scales_in[0]);
+    const uint32_t written0 = smem_addr(rank == 0 ? &ctl.scales_full[0] : &ctl.scales_in[0]);
     const uint8_t *base = role == 0 ? p.d_scales : p.a_scales;
     const uint32_t width = static_cast<uint32_t>(role == 0 ? p.N : p.K);
     const uint32_t dst0 = s_ring + role * kWgAtom + static_cast<uint32_t>(lane) * 16u;
-    Ring rt;
+    Ring rs;
     bool ok = true;
     uint32_t t = unit0, kb = 0;   // the next chunk of kWgAhead stages
     WgTile x{};
@@ -401,20 +420,21 @@ __global__ void __launch_bounds__(kWgThreads, 1) gmm_weight_grad_fp8_kernel(cons
       return n;
     };
     auto put = [&](const uint32_t (&v)[kWgAhead][4], uint32_t n) {
+      if (!ok) return;
+      if (!__all_sync(0xffffffffu, wait_phase(smem_addr(&ctl.scales_empty[rs.slot]), rs.phase ^ 1u, abort))) {
+        ok = false;
+        return;
+      }
+      const uint32_t dst = dst0 + rs.slot * kWgEntryBytes;
 #pragma unroll
       for (uint32_t i = 0; i < kWgAhead; ++i)
-        if (i < n && ok) {
-          if (!__all_sync(0xffffffffu, wait_phase(smem_addr(&ctl.empty[rt.slot]), rt.phase ^ 1u, abort))) {
-            ok = false;
-          } else {
-            st_shared_v4(dst0 + rt.slot * kWgScaleBytes, v[i][0] * 0x01010101u, v[i][1] * 0x01010101u, v[i][2] * 0x01010101u,
-                         v[i][3] * 0x01010101u);
-            fence_async_smem();   // these writes, before the tensor-memory copies read them
-            __syncwarp();
-            if (lane == 0) mbar_arrive(written0 + rt.slot * 8u);
-            rt.next(ST);
-          }
-        }
+        if (i < n)
+          st_shared_v4(dst + i * kWgScaleBytes, v[i][0] * 0x01010101u, v[i][1] * 0x01010101u, v[i][2] * 0x01010101u,
+                       v[i][3] * 0x01010101u);
+      fence_async_smem();   // these writes, before the tensor-memory copies read them
+      __syncwarp();
+      if (lane == 0) mbar_arrive(written0 + rs.slot * 8u);
+      rs.next(kWgEntries);
     };
     uint32_t v0[kWgAhead][4], v1[kWgAhead][4];
     enter();
