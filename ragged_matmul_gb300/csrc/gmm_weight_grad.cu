@@ -31,8 +31,12 @@ cudaLaunchConfig_t pair_config(unsigned grid, size_t smem, cudaStream_t stream, 
   return cfg;
 }
 
-int stages_of(const gmm_variant &v, int groups) {
-  const size_t fixed = gmm::kWgFixedBytes + offsets_bytes(groups);
+size_t staging_bytes(bool bf16, int bufs) {
+  return static_cast<size_t>(bufs) * gmm::kWgEpiWarps * (bf16 ? gmm::kWgStgBytes<true> : gmm::kWgStgBytes<false>);
+}
+
+int stages_of(const gmm_variant &v, int groups, bool bf16, int bufs) {
+  const size_t fixed = gmm::kWgFixedBytes + staging_bytes(bf16, bufs) + offsets_bytes(groups);
   if (v.budget < fixed) return 0;
   return static_cast<int>(std::min<size_t>(gmm::kWgMaxStages, (v.budget - fixed) / gmm::kWgStageBytes));
 }
@@ -61,7 +65,7 @@ void configure_weight_grad(gmm_variant (&vars)[2], int optin, int sm_smem, int d
     const long avail = static_cast<long>(optin) - static_cast<long>(attr.sharedSizeBytes);
     if (avail <= 0 || num_sms < 2) return;
     v.budget = static_cast<size_t>(avail);
-    v.stages = stages_of(v, 1);
+    v.stages = stages_of(v, 1, bf16, 2);
     if (v.stages < v.min_stages) return;
     const long reserve = static_cast<long>(sm_smem) / 2 + 1024;   // more than half an SM: one CTA per SM
     const long cap = static_cast<long>(device_optin) - static_cast<long>(attr.sharedSizeBytes);
@@ -100,8 +104,6 @@ extern "C" int gmm_weight_grad_fp8(gmm_handle_t h, void *d_b, const void *d_t, c
 
   WeightGradParams p;
   std::memset(&p, 0, sizeof(p));
-  p.num_stages = stages_of(v, num_groups);
-  if (p.num_stages < v.min_stages) return GMM_ERR_UNSUPPORTED;   // the offsets leave no room for the ring
   const uint32_t units = static_cast<uint32_t>(K) / gmm::kWgUnit, most = gmm::kWgMaxK / gmm::kWgUnit;
   p.k_tiles = (units + most - 1) / most;
   p.width = units / p.k_tiles * gmm::kWgUnit;
@@ -111,6 +113,13 @@ extern "C" int gmm_weight_grad_fp8(gmm_handle_t h, void *d_b, const void *d_t, c
   if (total > 0x7fffffffull) return GMM_ERR_UNSUPPORTED;
   p.per_group = p.k_tiles * p.n_tiles;
   p.total = static_cast<uint32_t>(total);
+  // Two staging buffers where a CTA has a tile or three, whose last stores are then waited for side by
+  // side (fp32, 16 groups, N = 1024, K = 512: 12.8 us, with one 15.5); with more tiles one, for a deeper
+  // ring of operands (64 groups, N = 2816, K = 2048: 273 us, with two 297).  In bf16 the ring is as deep
+  // with two.
+  p.stg_bufs = bf16 || p.total <= 3u * static_cast<uint32_t>(v.grid / 2) ? 2 : 1;
+  p.num_stages = stages_of(v, num_groups, bf16, p.stg_bufs);
+  if (p.num_stages < v.min_stages) return GMM_ERR_UNSUPPORTED;   // the offsets leave no room for the ring
   // As many n tiles a band as make the tiles that run side by side about as deep as they are wide.
   p.band = 8;
   p.d_scales = static_cast<const uint8_t *>(d_t_scales);

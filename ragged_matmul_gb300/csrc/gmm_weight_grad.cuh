@@ -30,6 +30,8 @@
 // memory: each role finds its tiles itself.  Every wait is bounded as in the grouped kernel.
 #pragma once
 
+#include <type_traits>
+
 #include "gmm_kernel.cuh"
 
 namespace gmm {
@@ -48,16 +50,16 @@ constexpr uint32_t kWgAtom = 512;                            // scale words of 1
 constexpr uint32_t kWgScaleBytes = 3 * kWgAtom;              // a stage's
 constexpr int kWgAhead = 4;                                  // stages of an entry of the scales' ring
 constexpr uint32_t kWgEntryBytes = kWgAhead * kWgScaleBytes;
-constexpr uint32_t kWgEntries = 4;
+constexpr uint32_t kWgEntries = 3;
 constexpr uint32_t kWgStageBytes = kWgABytes + kWgBBytes;
 constexpr uint32_t kWgAccCols = kWgMaxK;
 constexpr uint32_t kWgScaleCol = 2 * kWgAccCols;
-constexpr uint32_t kWgStgBytes = 32 * 32 * 4;                // one staging buffer: 32 n x 32 k in fp32
-constexpr uint32_t kWgStgBufs = 2;                           // per epilogue warp
+template <bool kBf16>
+constexpr uint32_t kWgStgBytes = 32 * 32 * (kBf16 ? 2 : 4);  // one staging buffer: 32 n x 32 k
 constexpr int kWgMaxStages = 8;
-constexpr size_t kWgFixedBytes = 1024 + kWgEpiWarps * kWgStgBufs * kWgStgBytes + kWgEntries * kWgEntryBytes;
+constexpr size_t kWgFixedBytes = 1024 + kWgEntries * kWgEntryBytes;   // and the staging buffers
 static_assert(kWgScaleCol + 12 <= kTmemCols, "scales beside the accumulators");
-static_assert(kWgABytes % 1024 == 0 && kWgBBytes % 1024 == 0 && kWgStgBytes % 1024 == 0, "swizzled tiles start at 1024 bytes");
+static_assert(kWgABytes % 1024 == 0 && kWgBBytes % 1024 == 0 && kWgStgBytes<true> % 1024 == 0, "swizzled tiles start at 1024 bytes");
 
 struct alignas(128) WeightGradParams {
   CUtensorMap d_map;        // codes of dc {pitch, N}, box {128, 128}, 128-byte swizzle
@@ -72,6 +74,7 @@ struct alignas(128) WeightGradParams {
   int N;
   int K;
   int num_stages;
+  int stg_bufs;             // staging buffers per epilogue warp: 1 or 2
   int accumulate;
   uint32_t k_tiles;         // tiles along K, of which the first `wide` are 16 wider than `width`
   uint32_t wide;
@@ -124,22 +127,22 @@ __device__ __forceinline__ void wg_store_3d(const CUtensorMap *map, uint32_t src
                  "r"(src), "r"(x), "r"(y), "r"(z)
                  : "memory");
   else
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map), "r"(src),
-                 "r"(x), "r"(y), "r"(z)
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%2, %3, %4}], [%1], %5;" ::"l"(map),
+                 "r"(src), "r"(x), "r"(y), "r"(z), "l"(l2_policy_evict_first())
                  : "memory");
 }
 
-// A staging buffer's swizzle as the store's tensor map has it: 16-byte chunk j of row r of
-// kRowBytes (32, 64 or 128).
+// 16-byte chunk j of row r in a staging buffer, as the store's tensor map has it swizzled over its
+// rows of 32, 64 or 128 bytes.
 template <uint32_t kRowBytes>
 __device__ __forceinline__ uint32_t wg_chunk(uint32_t r, uint32_t j) {
   return r * kRowBytes + ((j ^ (r / (128 / kRowBytes) & (kRowBytes / 16 - 1))) << 4);
 }
 
-// 16 kHalves columns of the thread's row to the staging buffer.
-template <bool kBf16, int kHalves>
-__device__ __forceinline__ void wg_stage_row(uint32_t stg, uint32_t r, const uint32_t (&v)[32]) {
-  constexpr uint32_t kRow = 16u * kHalves * (kBf16 ? 2 : 4);
+// kCols fp32 columns of the thread's row to a staging buffer.
+template <bool kBf16, int kCols>
+__device__ __forceinline__ void wg_stage_row(uint32_t stg, uint32_t r, const uint32_t (&v)[kCols]) {
+  constexpr uint32_t kRow = kCols * (kBf16 ? 2 : 4);
 #pragma unroll
   for (uint32_t j = 0; j < kRow / 16; ++j) {
     const uint32_t at = stg + wg_chunk<kRow>(r, j);
@@ -168,7 +171,8 @@ __global__ void __launch_bounds__(kWgThreads, 1) gmm_weight_grad_fp8_kernel(cons
   const uint32_t a_ring = (dyn_base + 1023u) & ~1023u;
   const uint32_t b_ring = a_ring + ST * kWgABytes;
   const uint32_t stg_ring = b_ring + ST * kWgBBytes;
-  const uint32_t s_ring = stg_ring + kWgEpiWarps * kWgStgBufs * kWgStgBytes;
+  const uint32_t stg_bufs = static_cast<uint32_t>(p.stg_bufs);
+  const uint32_t s_ring = stg_ring + kWgEpiWarps * stg_bufs * kWgStgBytes<kBf16>;
   uint32_t *off = reinterpret_cast<uint32_t *>(dyn_smem + (s_ring + kWgEntries * kWgEntryBytes - dyn_base));
 
   if (tid == 0) {
@@ -218,7 +222,9 @@ __global__ void __launch_bounds__(kWgThreads, 1) gmm_weight_grad_fp8_kernel(cons
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      const uint64_t pol = l2_policy_evict_normal();
+      // The operands' panels are read by many tiles, the gradient is written once: they are to stay in
+      // L2 (prefill shapes 1100 -> 1088 us, 64 experts in fp32 276 -> 272).
+      const uint64_t pol = l2_policy_evict_last();
       Ring rt;
       uint32_t pending = 0, pend_phase = 0;
       bool ok = true;
@@ -264,7 +270,7 @@ __global__ void __launch_bounds__(kWgThreads, 1) gmm_weight_grad_fp8_kernel(cons
       const uint32_t s_full0 = smem_addr(&ctl.scales_full[0]), s_empty0 = smem_addr(&ctl.scales_empty[0]);
       const uint32_t sfa = tmem_base + kWgScaleCol, sfb = sfa + 4u;
       for (uint32_t t = unit0; t < total && ok; t += units) {
-        const WgTile x = wg_tile(p, off, t);
+        const WgTile x = wg_tile(p, off, t);   // ahead of its use, behind a tile's first MMAs, it measured slower (1.92 M cycles for 1.77)
         if (x.stages == 0) continue;
         if (!__all_sync(0xffffffffu, wait_phase_cluster<true>(smem_addr(&ctl.acc_empty[acc]), acc_phase ^ 1u, abort))) {
           ok = false;
@@ -315,7 +321,7 @@ __global__ void __launch_bounds__(kWgThreads, 1) gmm_weight_grad_fp8_kernel(cons
   } else if (warp < static_cast<int>(kWgFirstScaleWarp)) {
     // ------------------------------------------------------------ epilogue
     const uint32_t quad = static_cast<uint32_t>(warp & 3), r = static_cast<uint32_t>(lane);
-    const uint32_t stg0 = stg_ring + static_cast<uint32_t>(warp - 2) * kWgStgBufs * kWgStgBytes;
+    const uint32_t stg0 = stg_ring + static_cast<uint32_t>(warp - 2) * stg_bufs * kWgStgBytes<kBf16>;
     const uint32_t acc_empty0 = map_to_rank(smem_addr(&ctl.acc_empty[0]), 0);
     const bool add = p.accumulate != 0;
     uint32_t acc = 0, acc_phase = 0, buf = 0;
@@ -337,35 +343,37 @@ __global__ void __launch_bounds__(kWgThreads, 1) gmm_weight_grad_fp8_kernel(cons
         tc_fence_after_sync();
       }
       if (in) {
-        for (uint32_t c = 0; c < x.width; c += 32u) {
-          const bool whole = c + 32u <= x.width;   // else 16 columns
-          uint32_t v[32];
+        // 32 columns, or 16 at the end of a tile that is no multiple of 32 wide.
+        auto store = [&](uint32_t c, auto cols) {
+          constexpr int kCols = decltype(cols)::value;
+          uint32_t v[kCols];
+          if (zero) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0u;
-          if (!zero) {
-            if (whole) {
-              tmem_ld_x32(taddr + c, v);
-            } else {
-              uint32_t u[16];
-              tmem_ld_x16(taddr + c, u);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = u[i];
-            }
+            for (int i = 0; i < kCols; ++i) v[i] = 0u;
+          } else if constexpr (kCols == 32) {
+            tmem_ld_x32(taddr + c, v);
+          } else {
+            tmem_ld_x16(taddr + c, v);
           }
-          const uint32_t stg = stg0 + buf * kWgStgBytes;
-          if (lane == 0) bulk_wait_read<static_cast<int>(kWgStgBufs) - 1>();   // the store before last has read its buffer
+          const uint32_t stg = stg0 + buf * kWgStgBytes<kBf16>;
+          if (lane == 0) {   // the buffer's last store has read it
+            if (stg_bufs == 2u) bulk_wait_read<1>(); else bulk_wait_read<0>();
+          }
           if (!zero) tmem_ld_wait();
           __syncwarp();
-          if (whole) wg_stage_row<kBf16, 2>(stg, r, v); else wg_stage_row<kBf16, 1>(stg, r, v);
+          wg_stage_row<kBf16, kCols>(stg, r, v);
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
-            wg_store_3d(&p.out_map[whole], stg, static_cast<int32_t>(x.k0 + c), static_cast<int32_t>(n), static_cast<int32_t>(x.g),
-                        add);
+            wg_store_3d(&p.out_map[kCols == 32], stg, static_cast<int32_t>(x.k0 + c), static_cast<int32_t>(n),
+                        static_cast<int32_t>(x.g), add);
             bulk_commit();
           }
-          buf = buf + 1 == kWgStgBufs ? 0u : buf + 1;
-        }
+          buf = buf + 1 == stg_bufs ? 0u : buf + 1;
+        };
+        uint32_t c = 0;
+        for (; c + 32u <= x.width; c += 32u) store(c, std::integral_constant<int, 32>());
+        if (c < x.width) store(c, std::integral_constant<int, 16>());
       }
       if (!zero) {
         tc_fence_before_sync();
