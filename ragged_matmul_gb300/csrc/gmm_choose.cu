@@ -55,7 +55,7 @@ int run_choose(gmm_ctx *h, const gmm::ChooseParams &p, bool score, bool grad, cu
                                 reinterpret_cast<uintptr_t>(p.d_logits) | static_cast<unsigned long long>(p.d_pitch);
   auto vec = [&](int v) { return run % v == 0 && at % std::min<size_t>(16, v * sizeof(T)) == 0; };
   if (many && p.num_experts <= 64 && p.top_k <= 8) return launch_choose<T, 8, 8>(p, vec(8), score, grad, stream);
-  if (many && p.num_experts <= 128 && p.top_k <= 16) return launch_choose<T, 16, 8>(p, vec(8), score, grad, stream);
+  if (many && p.num_experts <= 128 && p.top_k <= 8) return launch_choose<T, 8, 16>(p, vec(16), score, grad, stream);
   if (need <= 2) return launch_choose<T, 32, 2>(p, vec(2), score, grad, stream);
   if (need <= 4) return launch_choose<T, 32, 4>(p, vec(4), score, grad, stream);
   if (need <= 8) return launch_choose<T, 32, 8>(p, vec(8), score, grad, stream);
@@ -121,6 +121,7 @@ int gmm_route(gmm_handle_t h, int32_t *slot_experts, float *weights, const void 
   if (num_tokens > 0 && (!slot_experts || !weights || !aligned_to(slot_experts, 4) || !aligned_to(weights, 4)))
     return GMM_ERR_INVALID_ARG;
   p.bias = bias;
+  p.bias_vec = aligned16(bias);
   p.ids = slot_experts;
   p.weights = weights;
   if (options->top_groups < groups) {   // else every group is kept

@@ -66,6 +66,7 @@ struct ChooseParams {
   int top_groups;
   int group_top;
   int renormalise;
+  int bias_vec;                 // bias is 16-byte aligned
   float scale;
   uint32_t *status;
 };
@@ -154,6 +155,59 @@ __device__ __forceinline__ void merge_top2(float &a1, float &a2, float b1, float
   a1 = fmaxf(a1, b1);
 }
 
+// Sorted lists of the eight largest keys, in registers.
+__device__ __forceinline__ void order2(uint32_t &hi, uint32_t &lo) {
+  const uint32_t a = max(hi, lo), b = min(hi, lo);
+  hi = a;
+  lo = b;
+}
+__device__ __forceinline__ void sort8(uint32_t (&a)[8]) {   // descending, the 19-comparator network
+  order2(a[0], a[2]), order2(a[1], a[3]), order2(a[4], a[6]), order2(a[5], a[7]);
+  order2(a[0], a[4]), order2(a[1], a[5]), order2(a[2], a[6]), order2(a[3], a[7]);
+  order2(a[0], a[1]), order2(a[2], a[3]), order2(a[4], a[5]), order2(a[6], a[7]);
+  order2(a[2], a[4]), order2(a[3], a[5]);
+  order2(a[1], a[4]), order2(a[3], a[6]);
+  order2(a[1], a[2]), order2(a[3], a[4]), order2(a[5], a[6]);
+}
+// a: the eight largest of two sorted lists, sorted.  The larger of a[i] and b[7 - i] are these eight, rising
+// and falling once, which three rounds of comparators at distances 4, 2, 1 sort (Batcher's merge).
+__device__ __forceinline__ void merge8(uint32_t (&a)[8], const uint32_t (&b)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = max(a[i], b[7 - i]);
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((i & d) == 0) order2(a[i], a[i + d]);
+}
+// The eight largest keys of a token's L lanes, in every one of them.
+template <int L, int V>
+__device__ __forceinline__ void largest8(const uint32_t (&key)[V], uint32_t (&a)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = i < V ? key[i] : 0u;
+  sort8(a);
+#pragma unroll
+  for (int c = 8; c < V; c += 8) {
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = key[c + i];
+    sort8(b);
+    merge8(a, b);
+  }
+#pragma unroll
+  for (int o = 1; o < L; o <<= 1) {
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = __shfl_xor_sync(0xffffffffu, a[i], o);
+    merge8(a, b);
+  }
+}
+__device__ __forceinline__ uint32_t pick8(const uint32_t (&a)[8], int j) {   // a[j & 7]
+  const uint32_t w = (j & 1) ? a[1] : a[0], x = (j & 1) ? a[3] : a[2], y = (j & 1) ? a[5] : a[4], z = (j & 1) ? a[7] : a[6];
+  const uint32_t u = (j & 2) ? x : w, v = (j & 2) ? z : y;
+  return (j & 4) ? v : u;
+}
+
 // The choice of one token by 64-bit keys, by a whole warp: ids[j] for lane j < top_k.  Only the
 // experts whose fp32 key reaches `least` are looked at (all of them and the groups again where
 // `all` is set); `kept`: bit g, group g is kept.
@@ -163,11 +217,13 @@ __device__ __noinline__ int choose_exact(const ChooseParams &p, const T *row, fl
   const int lane = static_cast<int>(threadIdx.x & 31u), E = p.num_experts;
   double zd = 0.0;
   if (p.scoring == kScoreSoftmax) {
+#pragma unroll 4
     for (int e = lane; e < E; e += 32) zd += exp(static_cast<double>(choose_float<T>(row[e])) - static_cast<double>(top));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) zd += __shfl_xor_sync(0xffffffffu, zd, o);
   }
-  for (int e = lane; e < E; e += 32) {
+#pragma unroll 4
+  for (int e = lane; e < E; e += 32) {   // several at a time: a 64-bit exponential is one long chain
     const float x = choose_float<T>(row[e]);
     unsigned long long k = 0ull;
     const float s = p.scoring == kScoreSoftmax ? expf(x - top) / z : sigmoid32(x);
@@ -247,6 +303,7 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
   static_assert(!kScore || L == 32, "a score's token has a whole warp");
   constexpr bool kPacked = !kScore && sizeof(T) == 2;
   extern __shared__ unsigned long long choose_smem[];
+  __shared__ float2 choose_slots[kChooseWarps * (32 / L)][8];   // expert and logit of a token's chosen ones
   const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
   const int sub = lane & (L - 1), seg = lane & ~(L - 1);
   const uint32_t seg_mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << seg;
@@ -269,6 +326,19 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
   }
   float x[V];
   choose_load<T, V, kVec>(row, first, n, x);
+  float bias[kScore ? V : 1];   // beside the logits' loads, not behind them
+  if constexpr (kScore) {
+    if (p.bias != nullptr && kVec && V % 4 == 0 && p.bias_vec) {
+#pragma unroll
+      for (int v = 0; v < V; v += 4) {
+        const float4 b = n > 0 ? __ldg(reinterpret_cast<const float4 *>(p.bias + first + v)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        bias[v] = b.x, bias[v + 1] = b.y, bias[v + 2] = b.z, bias[v + 3] = b.w;
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) bias[v] = p.bias != nullptr && v < n ? __ldg(p.bias + first + v) : 0.0f;
+    }
+  }
 
   // NaN (and, for softmax, +infinity) anywhere: no expert at all.
   bool bad = false;
@@ -310,7 +380,7 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
 
   float score_tol = 0.0f;   // two fp32 keys (of magnitude up to 1) are this near at least to be unsure of
   bool unsure = false, unsure_groups = false;
-  uint32_t kept = 0xffffffffu;
+  uint32_t kept_lanes = 0xffffffffu;   // lanes whose group is kept
   if constexpr (kScore) {
     // expf, the sum and the quotient are each off by a few units in the last place of values up to
     // 1; z by one a term and lane; the bias adds half of one of the key.  Two keys, so twice that.
@@ -319,7 +389,7 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
     for (int v = 0; v < V; ++v)
       if (key[v] != 0u) {
         const float s = p.scoring == kScoreSoftmax ? expf(x[v] - top) / z : sigmoid32(x[v]);
-        key[v] = order_key(s + (p.bias != nullptr ? __ldg(p.bias + first + v) : 0.0f));
+        key[v] = order_key(s + bias[v]);
       }
   }
   if (p.groups > 1) {
@@ -349,10 +419,7 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
       const uint32_t in = ~redux_max(keep ? ~gk : 0u);
       const float a = key_value(in), b = key_value(out);
       unsure_groups = out != 0u && in != 0u && !(a - b > 2.0f * (score_tol + 2.4e-7f * fmaxf(fabsf(a), fabsf(b))));
-      uint32_t k = 0u;
-      for (int g = 0; g < p.groups; ++g)
-        k |= (__shfl_sync(0xffffffffu, keep ? 1u : 0u, g * p.group_lanes)) << g;
-      kept = k;
+      kept_lanes = __ballot_sync(0xffffffffu, keep);
       if (p.bias == nullptr)
 #pragma unroll
         for (int v = 0; v < V; ++v) key[v] = order_key(x[v]);   // the experts by their logits
@@ -362,73 +429,160 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
       for (int v = 0; v < V; ++v) key[v] = 0u;
   }
 
-  // top_k maxima; lane j keeps the j-th expert's number.
+  // The chosen experts: lane j keeps the j-th one's number and logit.
   int id = -1;
-  float kth = 0.0f;
-  auto take = [&](int &e) -> uint32_t {   // the largest key left, and its expert
-    uint32_t m = key[0];
-#pragma unroll
-    for (int v = 1; v < V; ++v) m = max(m, key[v]);
-    const uint32_t M = lanes_max<L>(m);
+  float xj = -INFINITY;
+  bool done = false;
+  if (p.top_k <= 8) {
+    // Every lane gets the eight largest keys, sorted.
+    uint32_t best[8];
+    largest8<L, V>(key, best);
+    const uint32_t mine_key = sub < p.top_k ? pick8(best, sub) : 0u;
     if constexpr (kPacked) {
-      e = static_cast<int>(0xffffu - (M & 0xffffu));
-#pragma unroll
-      for (int v = 0; v < V; ++v) key[v] = key[v] == M ? 0u : key[v];
-    } else {
-      const uint32_t holders = __ballot_sync(0xffffffffu, m == M) & seg_mask;
-      const int owner = __ffs(static_cast<int>(holders)) - 1;   // the lowest expert's lane
-      int at = 0;
-      if (lane == owner) {
-        bool done = false;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (!done && key[v] == M) {
-            at = first + v;
-            key[v] = 0u;
-            done = true;
-          }
+      done = true;
+      if (mine_key != 0u) {
+        id = static_cast<int>(0xffffu - (mine_key & 0xffffu));
+        const uint32_t k = mine_key >> 16;
+        if constexpr (std::is_same_v<T, __half>)
+          xj = __half2float(__ushort_as_half(static_cast<unsigned short>((k & 0x8000u) ? k & 0x7fffu : ~k)));
+        else
+          xj = __uint_as_float(((k & 0x8000u) ? k & 0x7fffu : ~k) << 16);
       }
-      e = __shfl_sync(0xffffffffu, at, owner);
-    }
-    return M;
-  };
-  float prev_key = 0.0f, prev_x = 0.0f, prev_b = 0.0f;
-  for (int j = 0; j < p.top_k; ++j) {
-    int e;
-    const uint32_t M = take(e);
-    if (sub == j && M != 0u) id = e;
-    if (__all_sync(0xffffffffu, M == 0u)) break;
-    if constexpr (kScore) {
-      if (p.bias != nullptr && M != 0u) {
-        const float k = key_value(M), xe = choose_float<T>(row[e]), be = __ldg(p.bias + e);
-        if (j > 0 && !(prev_key - k > score_tol + 2.4e-7f * fabsf(prev_key)) && !(prev_x == xe && prev_b == be)) unsure = true;
-        prev_key = k;
-        prev_x = xe;
-        prev_b = be;
-        kth = k;
+    } else {
+      // Which experts they are: each lane looks for its own, and their places are how many are larger.
+      // Only where no two of the list, nor the last of it and one behind it, are equal or unsure.
+      const uint32_t last = __shfl_sync(0xffffffffu, mine_key, seg + p.top_k - 1);
+      uint32_t least = last;   // keys from here on count
+      float tol = 0.0f;
+      if (kScore && p.bias != nullptr) {
+        tol = score_tol + 2.4e-7f * fmaxf(fabsf(key_value(best[0])), fabsf(key_value(last)));
+        least = order_key(key_value(last) - tol);
+      }
+      const uint32_t next_key = __shfl_down_sync(0xffffffffu, mine_key, 1);
+      bool clear = last != 0u && tol < INFINITY && !unsure_groups;
+      if (sub + 1 < p.top_k)
+        clear = clear && (tol > 0.0f ? key_value(mine_key) - key_value(next_key) > tol : mine_key != next_key);
+      int count = 0;
+      float2 *slot = choose_slots[warp * (32 / L) + lane / L];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const bool hit = key[v] != 0u && key[v] >= least;
+        if (__any_sync(0xffffffffu, hit)) {
+          if (hit) {
+            int at = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) at += best[j] > key[v] ? 1 : 0;
+            slot[at & 7] = make_float2(__int_as_float(first + v), x[v]);
+            ++count;
+          }
+        }
+      }
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
+      clear = clear && count == p.top_k;
+      done = __all_sync(0xffffffffu, clear);
+      __syncwarp();   // the slots are written
+      if (done && sub < p.top_k) {
+        const float2 f = slot[sub];
+        id = __float_as_int(f.x);
+        xj = f.y;
       }
     }
   }
-  if constexpr (kScore) {
-    if (p.bias != nullptr && __shfl_sync(0xffffffffu, id, p.top_k - 1) >= 0) {   // every slot is filled: who came next?
-      const float tol = score_tol + 2.4e-7f * fabsf(kth);
-      for (int i = 0; i < p.num_experts; ++i) {
-        int e;
-        const uint32_t M = take(e);
-        if (M == 0u || kth - key_value(M) > tol) break;
-        if (!(choose_float<T>(row[e]) == prev_x && __ldg(p.bias + e) == prev_b)) {
-          unsure = true;
-          break;
+  if (!done) {
+    // One maximum after the other.
+    float kth = 0.0f, prev_key = 0.0f, prev_x = 0.0f, prev_b = 0.0f;
+    auto take = [&](int &e) -> uint32_t {   // the largest key left, and its expert
+      uint32_t m = key[0];
+#pragma unroll
+      for (int v = 1; v < V; ++v) m = max(m, key[v]);
+      const uint32_t M = lanes_max<L>(m);
+      if constexpr (kPacked) {
+        e = static_cast<int>(0xffffu - (M & 0xffffu));
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = key[v] == M ? 0u : key[v];
+      } else {
+        const uint32_t holders = __ballot_sync(0xffffffffu, m == M) & seg_mask;
+        const int owner = __ffs(static_cast<int>(holders)) - 1;   // the lowest expert's lane
+        int at = 0;
+        if (lane == owner) {
+          bool found = false;
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            if (!found && key[v] == M) {
+              at = first + v;
+              key[v] = 0u;
+              found = true;
+            }
+        }
+        e = __shfl_sync(0xffffffffu, at, owner);
+      }
+      return M;
+    };
+    int taken = 0;
+    for (; taken < p.top_k; ++taken) {
+      int e;
+      const uint32_t M = take(e);
+      if (sub == taken && M != 0u) id = e;
+      if (__all_sync(0xffffffffu, M == 0u)) break;
+      if constexpr (kScore) {
+        if (p.bias != nullptr) {
+          const float k = key_value(M), xe = choose_float<T>(row[e]), be = __ldg(p.bias + e);
+          if (taken > 0 && !(prev_key - k > score_tol + 2.4e-7f * fabsf(prev_key)) && !(prev_x == xe && prev_b == be)) unsure = true;
+          prev_key = k;
+          prev_x = xe;
+          prev_b = be;
+          kth = k;
         }
       }
     }
-    if ((unsure || unsure_groups) && !bad) {
-      // Every fp32 key that might belong among the chosen ones.
-      const bool full = __shfl_sync(0xffffffffu, id, p.top_k - 1) >= 0;
-      const float least = full && kth < INFINITY ? kth - 2.0f * (score_tol + 2.4e-7f * fabsf(kth)) : -INFINITY;
-      id = choose_exact<T>(p, row, top, z, least, unsure_groups || p.bias == nullptr, kept,
-                           choose_smem + static_cast<size_t>(warp) * p.num_experts);
+    if constexpr (kScore) {
+      const bool full = taken == p.top_k;
+      const float tol = score_tol + 2.4e-7f * fabsf(kth);
+      if (p.bias != nullptr && full) {   // is one of those left as near to the last one?
+        bool near = false;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (key[v] != 0u && !(kth - key_value(key[v]) > tol))
+            near |= !(x[v] == prev_x && bias[v] == prev_b);
+        unsure |= __any_sync(0xffffffffu, near);
+      }
+      if ((unsure || unsure_groups) && !bad) {
+        // Every fp32 key that might belong among the chosen ones: where there are few, a lane each.
+        const float least = full && kth < INFINITY ? kth - 2.0f * tol : -INFINITY;
+        bool few = !unsure_groups && p.scoring == kScoreSigmoid;
+        while (few) {
+          int e;
+          const uint32_t M = take(e);
+          if (M == 0u || !(key_value(M) >= least)) break;
+          if (taken == 32) few = false;
+          else if (lane == taken++) id = e;
+        }
+        if (few) {
+          unsigned long long k = 0ull;
+          if (id >= 0)
+            k = order_key(sigmoid64(static_cast<double>(choose_float<T>(row[id]))) + static_cast<double>(__ldg(p.bias + id)));
+          int rank = 0;
+          for (int i = 0; i < taken; ++i) {
+            const unsigned long long o = __shfl_sync(0xffffffffu, k, i);
+            const int oid = __shfl_sync(0xffffffffu, id, i);
+            rank += o > k || (o == k && oid < id) ? 1 : 0;
+          }
+          int best_id = -1;
+          for (int i = 0; i < taken; ++i) {
+            const int at = __shfl_sync(0xffffffffu, rank, i), oid = __shfl_sync(0xffffffffu, id, i);
+            if (at == lane) best_id = oid;
+          }
+          id = lane < p.top_k ? best_id : -1;
+        } else {
+          uint32_t kept = 0u;
+          for (int g = 0; g < p.groups; ++g) kept |= (kept_lanes >> (g * p.group_lanes) & 1u) << g;
+          id = choose_exact<T>(p, row, top, z, least, unsure_groups || p.bias == nullptr, kept,
+                               choose_smem + static_cast<size_t>(warp) * p.num_experts);
+        }
+      }
     }
+    if (id >= 0) xj = choose_float<T>(row[id]);
   }
   if (bad) {
     id = -1;
@@ -436,7 +590,7 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
   }
 
   // Weights.
-  const float xj = id >= 0 ? choose_float<T>(row[id]) : -INFINITY;
+  if (id < 0) xj = -INFINITY;
   float wj;
   if (p.renormalise) {
     // Scores relative to the largest chosen logit's: the sum is not below 1 (softmax).  Sigmoids of
