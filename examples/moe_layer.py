@@ -8,6 +8,11 @@ sum takes the rows back to their tokens.
 `Experts` is one bf16 expert product with its gradients for the layer's input and for
 the router's weights, for training (the expert weights are frozen).
 
+`Route` chooses the experts (scores, a balancing bias, groups, renormalised weights) with
+the gradient for the logits, and `Fp8Experts` is an expert product in 8 bits, a scale for
+each block of 128, whose expert weights are trained too: forward, gradient of the input and
+gradient of the weights all run on e4m3 operands.
+
     python examples/moe_layer.py        # needs the GPU and the built library
 """
 from __future__ import annotations
@@ -124,6 +129,92 @@ class Experts(torch.autograd.Function):
         return d_x, d_weights, None, None, None, None
 
 
+class Route(torch.autograd.Function):
+    """(weights fp32, expert ids int32), both [tokens, top_k], of logits [tokens, E]; options as gmm_route's."""
+
+    @staticmethod
+    def forward(ctx, logits, top_k, h, options, bias=None):
+        T = logits.shape[0]
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+        gmm.gmm_route(h, ids, weights, logits, bias=bias, **options)
+        ctx.save_for_backward(logits, ids)
+        ctx.h = h
+        ctx.options = {k: options[k] for k in ("scoring", "renormalise", "scale") if k in options}
+        ctx.mark_non_differentiable(ids)
+        return weights, ids
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_weights, _):
+        logits, ids = ctx.saved_tensors
+        d_logits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        gmm.gmm_route_grad(ctx.h, d_logits, d_weights.contiguous(), ids, logits, **ctx.options)
+        return d_logits, None, None, None, None
+
+
+def _fp8_buffers(rows, width, groups, dev):
+    """Buffers of one operand in both forms: (q, scales) by rows, (q_t, t_scales) along each group's rows."""
+    pitch = gmm.fp8_cols_pitch(rows, groups)
+    u8 = dict(dtype=torch.uint8, device=dev)
+    return (torch.empty((rows, width), **u8), torch.empty((rows, -(-width // 128)), device=dev),
+            torch.empty((width, pitch), **u8), torch.empty((pitch // 128, width), **u8))
+
+
+class Fp8Experts(torch.autograd.Function):
+    """out[t] = sum_j weights[t, j] * (x[t] @ w[ids[t, j]].T) in 8 bits, with the gradients for x, weights and w.
+
+    x is bf16 [tokens, K], w bf16 [E, N, K] (quantised in every call, as after every optimizer step); K and N are
+    multiples of 16."""
+
+    @staticmethod
+    def forward(ctx, x, weights, ids, w, h):
+        T, K = x.shape
+        k = ids.shape[1]
+        E, N, _ = w.shape
+        dev = x.device
+        off = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        slot_rows = torch.empty((T, k), dtype=torch.int32, device=dev)
+        row_slots = torch.empty(T * k, dtype=torch.int32, device=dev)
+        experts = torch.arange(E, dtype=torch.int32, device=dev)
+        stats = torch.empty(2, dtype=torch.int32, device=dev)
+        gmm.gmm_dispatch(h, off, slot_rows, row_slots, ids)
+        w8 = torch.empty((E, N, K), dtype=torch.uint8, device=dev)
+        w_scales = torch.empty((E, -(-N // 128), -(-K // 128)), device=dev)
+        gmm.gmm_quantize_fp8_tiles(h, w8, w_scales, w)
+        a8, a_scales, a_t, a_t_scales = _fp8_buffers(T * k, K, E, dev)
+        gmm.gmm_quantize_fp8_cols(h, a_t, a_t_scales, x, off, row_slots=row_slots, top_k=k, q=a8, scales=a_scales)
+        y = torch.empty((T * k, N), dtype=x.dtype, device=dev)
+        gmm.gmm_run_fp8(h, y, a8, off, w8, experts, stats, a_scales, w_scales, (1, 128, 128))
+        out = torch.empty((T, N), dtype=x.dtype, device=dev)
+        gmm.gmm_combine(h, out, y, slot_rows, weights)
+        ctx.save_for_backward(y, weights, off, slot_rows, experts, stats, w8, w_scales, a_t, a_t_scales)
+        ctx.h, ctx.w_type = h, w.dtype
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_out):
+        y, weights, off, slot_rows, experts, stats, w8, w_scales, a_t, a_t_scales = ctx.saved_tensors
+        h = ctx.h
+        E, N, K = w8.shape
+        rows, dev = y.shape[0], y.device
+        if d_out.stride(1) != 1:     # an expanded or transposed gradient (that of out.sum(), for one)
+            d_out = d_out.contiguous()
+        d_y, d_weights = torch.empty_like(y), torch.empty_like(weights)
+        gmm.gmm_combine_grad(h, d_y, d_weights, d_out, y, slot_rows, weights)
+        d8, d_scales, d_t, d_t_scales = _fp8_buffers(rows, N, E, dev)
+        gmm.gmm_quantize_fp8_cols(h, d_t, d_t_scales, d_y, off, q=d8, scales=d_scales)
+        d_w = torch.empty((E, N, K), dtype=torch.float32, device=dev)
+        gmm.gmm_weight_grad_fp8(h, d_w, d_t, d_t_scales, a_t, a_t_scales, off)
+        d_rows = torch.empty((rows, K), dtype=y.dtype, device=dev)
+        gmm.gmm_run_fp8(h, d_rows, d8, off, w8.transpose(1, 2).contiguous(), experts, stats, d_scales,
+                        w_scales.transpose(1, 2).contiguous(), (1, 128, 128))
+        d_x = torch.empty((slot_rows.shape[0], K), dtype=y.dtype, device=dev)
+        gmm.gmm_combine(h, d_x, d_rows, slot_rows)     # the gradient of the gather
+        return d_x, d_weights, None, d_w.to(ctx.w_type), None
+
+
 def main():
     torch.manual_seed(0)
     T, width, hidden, E, top_k = 300, 512, 1024, 16, 4
@@ -148,6 +239,12 @@ def main():
     out = Experts.apply(xt, wt, ids, w, w.transpose(1, 2).contiguous(), h)
     out.float().square().mean().backward()
     print(f"train: |d_x| {float(xt.grad.float().norm()):.4f}, |d_weights| {float(wt.grad.norm()):.4f}")
+    xt, rt, wt = x.clone().requires_grad_(), router.bfloat16().requires_grad_(), w.clone().requires_grad_()
+    options = dict(scoring="sigmoid", expert_groups=4, top_groups=2, group_top=2, scale=2.5)
+    weights8, ids8 = Route.apply(xt @ rt, top_k, h, options, torch.zeros(E, device=dev))
+    Fp8Experts.apply(xt, weights8, ids8, wt, h).float().square().mean().backward()
+    print(f"train in 8 bits: |d_x| {float(xt.grad.float().norm()):.4f}, |d_router| {float(rt.grad.float().norm()):.4f}, "
+          f"|d_w| {float(wt.grad.float().norm()):.4f}")
     status = gmm.gmm_query_status(h)
     print("status:", gmm.gmm_error_string(status))
     gmm.gmm_destroy(h)
