@@ -230,7 +230,8 @@ int gmm_run_fp8(gmm_handle_t h, void *c, const void *a, const uint32_t *a_offset
  *   choice      the top_k largest y_e of the groups that stay, in descending order;
  *   weights     scale * s_j, or with renormalise scale * s_j / (the sum of the chosen s_j).
  * Equal keys, of experts or of groups, go to the lowest index.  Keys are compared to 64-bit
- * accuracy; equal logits of equal bias are equal keys.  Scores and weights are fp32.
+ * accuracy, single scores without a bias (which stand in the order of the logits) as the logits;
+ * equal logits of equal bias are equal keys.  Scores and weights are fp32.
  * An expert whose key is -infinity or NaN (a masked logit or bias) is never chosen; a group's key
  * leaves such experts out.  A slot that finds no expert gets id -1 and weight 0, which
  * gmm_dispatch drops.  A token with a NaN logit (softmax: or one of +infinity) gets no expert and

@@ -13,7 +13,8 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 INCLUDE_DIR = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG_DIR, "csrc")
-SOURCES = [os.path.join(CSRC, f) for f in ("gmm.cu", "gmm_choose.cu", "gmm_fp8_quant.cu", "gmm_weight_grad.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("gmm.cu", "gmm_choose.cu", "gmm_choose_bf16.cu", "gmm_choose_fp16.cu",
+                                                  "gmm_choose_fp32.cu", "gmm_fp8_quant.cu", "gmm_weight_grad.cu")]
 LIB_PATH = os.path.join(PKG_DIR, "libgmm.so")
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",

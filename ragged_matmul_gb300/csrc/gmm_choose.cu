@@ -1,68 +1,11 @@
-// Host side of a router's choice and its gradient (gmm_route, gmm_route_grad): argument
-// checks, the kernel variant and the launch.
+// Host side of a router's choice and its gradient (gmm_route, gmm_route_grad): argument checks.
 #include <cmath>
-#include <type_traits>
 
-#include "gmm_choose.cuh"
-#include "gmm_host.h"
+#include "gmm_choose_launch.h"
 
 namespace {
 
 using namespace gmm::host;
-
-// Warps a CTA: fewer where a warp's `smem` bytes (64-bit keys of every expert, rows of the
-// gradient) would not leave the default 48 KB.
-int choose_warps(size_t smem) {
-  return static_cast<int>(std::max<size_t>(1, std::min<size_t>(gmm::kChooseWarps, 48 * 1024 / std::max<size_t>(1, smem))));
-}
-
-template <class T, int L, int V>
-int launch_choose(const gmm::ChooseParams &p, bool vec, bool score, bool grad, cudaStream_t stream) {
-  const long long warps = (p.num_tokens + 32 / L - 1) / (32 / L);
-  const bool dense = p.scoring == GMM_SCORE_SOFTMAX && !p.renormalise;
-  const size_t per_warp = grad ? static_cast<size_t>(32) * V * 4 : (score ? static_cast<size_t>(p.num_experts) * 8 : 0);
-  const int wc = choose_warps(per_warp);
-  const unsigned grid = static_cast<unsigned>((warps + wc - 1) / wc), threads = 32u * wc;
-  const size_t smem = per_warp * wc;
-  auto go = [&](auto vec_c) {
-    constexpr bool kVec = decltype(vec_c)::value;
-    if (grad) {
-      if (dense) gmm::gmm_route_grad_kernel<T, L, V, kVec, true><<<grid, threads, smem, stream>>>(p);
-      else gmm::gmm_route_grad_kernel<T, L, V, kVec, false><<<grid, threads, smem, stream>>>(p);
-    } else if constexpr (L == 32) {
-      if (score) gmm::gmm_route_kernel<T, L, V, kVec, true><<<grid, threads, smem, stream>>>(p);
-      else gmm::gmm_route_kernel<T, L, V, kVec, false><<<grid, threads, smem, stream>>>(p);
-    } else {
-      gmm::gmm_route_kernel<T, L, V, kVec, false><<<grid, threads, smem, stream>>>(p);
-    }
-  };
-  if constexpr (V * sizeof(T) <= 128) {
-    if (vec) go(std::true_type()); else go(std::false_type());
-  } else {
-    go(std::false_type());
-  }
-  return launch_status(grad ? "launch of the route gradient kernel" : "launch of the route kernel");
-}
-
-template <class T>
-int run_choose(gmm_ctx *h, const gmm::ChooseParams &p, bool score, bool grad, cudaStream_t stream) {
-  // Lanes a token: a whole warp has the shortest way through one token; with many tokens fewer
-  // lanes leave fewer of them idle.
-  const int run = p.groups > 1 ? p.group_size : p.num_experts;           // consecutive experts
-  const int need = (run + p.group_lanes - 1) / p.group_lanes;            // a lane's share in a whole warp
-  const bool many = p.groups == 1 && !score && p.num_tokens > 16 * h->num_sms;
-  const unsigned long long at = reinterpret_cast<uintptr_t>(p.logits) | static_cast<unsigned long long>(p.logits_pitch) |
-                                reinterpret_cast<uintptr_t>(p.d_logits) | static_cast<unsigned long long>(p.d_pitch);
-  auto vec = [&](int v) { return run % v == 0 && at % std::min<size_t>(16, v * sizeof(T)) == 0; };
-  if (many && p.num_experts <= 64 && p.top_k <= 8) return launch_choose<T, 8, 8>(p, vec(8), score, grad, stream);
-  if (many && p.num_experts <= 128 && p.top_k <= 8) return launch_choose<T, 8, 16>(p, vec(16), score, grad, stream);
-  if (need <= 2) return launch_choose<T, 32, 2>(p, vec(2), score, grad, stream);
-  if (need <= 4) return launch_choose<T, 32, 4>(p, vec(4), score, grad, stream);
-  if (need <= 8) return launch_choose<T, 32, 8>(p, vec(8), score, grad, stream);
-  if (need <= 16) return launch_choose<T, 32, 16>(p, vec(16), score, grad, stream);
-  if (need <= 32) return launch_choose<T, 32, 32>(p, vec(32), score, grad, stream);
-  return launch_choose<T, 32, gmm::kChooseMaxPerLane>(p, false, score, grad, stream);
-}
 
 int check_route(gmm_ctx *h, gmm::ChooseParams &p, const void *logits, long long logits_stride, int num_tokens, int top_k,
                 int dtype, const gmm_route_options *o) {
@@ -94,9 +37,9 @@ int check_route(gmm_ctx *h, gmm::ChooseParams &p, const void *logits, long long 
 int run_choose_dtype(gmm_ctx *h, const gmm::ChooseParams &p, int dtype, bool score, bool grad, cudaStream_t stream) {
   DeviceGuard guard(h->device);
   switch (dtype) {
-    case GMM_DTYPE_BF16: return run_choose<__nv_bfloat16>(h, p, score, grad, stream);
-    case GMM_DTYPE_FP16: return run_choose<__half>(h, p, score, grad, stream);
-    default: return run_choose<float>(h, p, score, grad, stream);
+    case GMM_DTYPE_BF16: return run_choose_bf16(h, p, score, grad, stream);
+    case GMM_DTYPE_FP16: return run_choose_fp16(h, p, score, grad, stream);
+    default: return run_choose_fp32(h, p, score, grad, stream);
   }
 }
 

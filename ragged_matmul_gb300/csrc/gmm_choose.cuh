@@ -146,7 +146,70 @@ __device__ __forceinline__ void choose_load(const T *row, int first, int n, floa
   }
 }
 
-__device__ __forceinline__ float sigmoid32(float x) { return 1.0f / (1.0f + expf(-x)); }
+// 16-bit logits compared as they stand.  A key holds the logit's 16 bits in the order of the values above
+// 65535 less the expert's number, so that the largest key is the largest logit's lowest expert.
+template <class T>
+struct Packed16 {
+  static constexpr uint32_t kMinusInf = std::is_same_v<T, __half> ? 0x03ffu : 0x007fu;   // of -infinity
+  static constexpr uint32_t kPlusInf = std::is_same_v<T, __half> ? 0xfc00u : 0xff80u;    // of +infinity; NaN is above
+  static constexpr uint32_t kPad = std::is_same_v<T, __half> ? 0xfc00fc00u : 0xff80ff80u;   // two logits of -infinity
+  static constexpr uint32_t kNone = kMinusInf << 16 | 0xffffu;   // keys up to here are never chosen
+  __device__ __forceinline__ static uint32_t canonical(uint32_t w) {   // -0 becomes +0, a NaN a positive one
+    if constexpr (std::is_same_v<T, __half>) {
+      const __half2 h = __hadd2(*reinterpret_cast<const __half2 *>(&w), __half2half2(__ushort_as_half(0)));
+      return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+      const __nv_bfloat162 h = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&w), __bfloat162bfloat162(__ushort_as_bfloat16(0)));
+      return *reinterpret_cast<const uint32_t *>(&h);
+    }
+  }
+  __device__ __forceinline__ static float value(uint32_t bits) {   // of 16 bits
+    if constexpr (std::is_same_v<T, __half>) return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+    else return __uint_as_float(bits << 16);
+  }
+  __device__ __forceinline__ static float key_value(uint32_t key) {
+    const uint32_t k = key >> 16;
+    return value((k & 0x8000u) ? k & 0x7fffu : ~k & 0xffffu);
+  }
+  // Two keys of a word of two logits, experts e and e + 1.
+  __device__ __forceinline__ static void keys(uint32_t w, uint32_t e, uint32_t &k0, uint32_t &k1) {
+    uint32_t sign;   // each half all ones where it is negative
+    asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(sign) : "r"(w));
+    const uint32_t k = w ^ (sign | 0x80008000u);
+    k0 = (k << 16) | (0xffffu - e);
+    k1 = (k & 0xffff0000u) | (0xfffeu - e);
+  }
+};
+
+// V consecutive 16-bit logits as words, -infinity past the lane's `n`.
+template <class T, int V, bool kVec>
+__device__ __forceinline__ void choose_load16(const T *row, int first, int n, uint32_t (&w)[V / 2]) {
+  constexpr uint32_t kPad = Packed16<T>::kPad;
+  if constexpr (kVec) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) w[i] = kPad;
+    if (n > 0) {
+      if constexpr (V >= 8) {
+#pragma unroll
+        for (int i = 0; i < V / 8; ++i)
+          *reinterpret_cast<uint4 *>(&w[4 * i]) = __ldg(reinterpret_cast<const uint4 *>(row + first) + i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(row + first) + i);
+      }
+    }
+  } else {
+    const unsigned short *p = reinterpret_cast<const unsigned short *>(row + first);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const uint32_t a = 2 * i < n ? __ldg(p + 2 * i) : kPad & 0xffffu, b = 2 * i + 1 < n ? __ldg(p + 2 * i + 1) : kPad & 0xffffu;
+      w[i] = a | (b << 16);
+    }
+  }
+}
+
+// Off by about 4 units in the last place (the quotient by 2); 0 below about -87.
+__device__ __forceinline__ float sigmoid32(float x) { return __fdividef(1.0f, 1.0f + expf(-x)); }
 __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
 
 // The largest two of a run of lanes, each lane with its own two.
@@ -324,8 +387,10 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
     first = sub * V;
     n = max(0, min(V, p.num_experts - first));
   }
-  float x[V];
-  choose_load<T, V, kVec>(row, first, n, x);
+  float x[kPacked ? 1 : V];
+  uint32_t raw[kPacked ? V / 2 : 1], key[V];
+  if constexpr (kPacked) choose_load16<T, V, kVec>(row, first, n, raw);
+  else choose_load<T, V, kVec>(row, first, n, x);
   float bias[kScore ? V : 1];   // beside the logits' loads, not behind them
   if constexpr (kScore) {
     if (p.bias != nullptr && kVec && V % 4 == 0 && p.bias_vec) {
@@ -340,41 +405,39 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
     }
   }
 
-  // NaN (and, for softmax, +infinity) anywhere: no expert at all.
+  // NaN (and, for softmax, +infinity) anywhere: no expert at all.  Of packed keys the largest one tells.
   bool bad = false;
+  if constexpr (kPacked) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) bad |= !(x[v] < INFINITY) && (p.scoring == kScoreSoftmax || x[v] != x[v]);
-  bad = (__ballot_sync(0xffffffffu, bad) & seg_mask) != 0u;
-
-  uint32_t key[V];
+    for (int i = 0; i < V / 2; ++i) {
+      raw[i] = Packed16<T>::canonical(raw[i]);
+      Packed16<T>::keys(raw[i], static_cast<uint32_t>(first + 2 * i), key[2 * i], key[2 * i + 1]);
+    }
+  } else {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    if constexpr (kPacked) {   // fp32's order on the type's own 16 bits, then the lowest expert first
-      const uint32_t k = order_key(x[v]);
-      const uint32_t k16 = std::is_same_v<T, __half> ? 0u : k >> 16;
-      if constexpr (std::is_same_v<T, __half>) {
-        const uint32_t h = __half_as_ushort(__float2half_rn(x[v] + 0.0f));
-        key[v] = k == 0u ? 0u : ((((h & 0x8000u) ? ~h : h | 0x8000u) & 0xffffu) << 16) | (0xffffu - static_cast<uint32_t>(first + v));
-      } else {
-        key[v] = k == 0u ? 0u : (k16 << 16) | (0xffffu - static_cast<uint32_t>(first + v));
-      }
-    } else {
+    for (int v = 0; v < V; ++v) {
+      bad |= !(x[v] < INFINITY) && (p.scoring == kScoreSoftmax || x[v] != x[v]);
       key[v] = order_key(x[v]);
     }
+    bad = (__ballot_sync(0xffffffffu, bad) & seg_mask) != 0u;
   }
 
   // Softmax's maximum and sum, where a score itself is needed.
   float top = 0.0f, z = 1.0f;
   if (p.scoring == kScoreSoftmax && (kScore || !p.renormalise)) {
+    auto logit = [&](int v) {
+      if constexpr (kPacked) return Packed16<T>::value((raw[v / 2] >> (16 * (v & 1))) & 0xffffu);
+      else return x[v];
+    };
     float m = -INFINITY;
 #pragma unroll
-    for (int v = 0; v < V; ++v) m = fmaxf(m, x[v]);
+    for (int v = 0; v < V; ++v) m = fmaxf(m, logit(v));
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     top = m > -INFINITY ? m : 0.0f;
     float sum = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) sum += expf(x[v] - top);
+    for (int v = 0; v < V; ++v) sum += expf(logit(v) - top);
     z = lanes_sum<L>(sum);
   }
 
@@ -397,8 +460,8 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
     if constexpr (kPacked) {
       uint32_t m = 0u;
 #pragma unroll
-      for (int v = 0; v < V; ++v) m = max(m, key[v] >> 16);
-      g1 = m == 0u ? -INFINITY : static_cast<float>(m);   // any value in the keys' order
+      for (int v = 0; v < V; ++v) m = max(m, key[v]);
+      g1 = m <= Packed16<T>::kNone ? -INFINITY : static_cast<float>(m >> 16);   // any value in the keys' order
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) merge_top2(g1, g2, key_value(key[v]), -INFINITY);
@@ -440,13 +503,10 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
     const uint32_t mine_key = sub < p.top_k ? pick8(best, sub) : 0u;
     if constexpr (kPacked) {
       done = true;
-      if (mine_key != 0u) {
+      bad = (best[0] >> 16) > Packed16<T>::kPlusInf - (p.scoring == kScoreSoftmax ? 1u : 0u);
+      if (mine_key > Packed16<T>::kNone) {
         id = static_cast<int>(0xffffu - (mine_key & 0xffffu));
-        const uint32_t k = mine_key >> 16;
-        if constexpr (std::is_same_v<T, __half>)
-          xj = __half2float(__ushort_as_half(static_cast<unsigned short>((k & 0x8000u) ? k & 0x7fffu : ~k)));
-        else
-          xj = __uint_as_float(((k & 0x8000u) ? k & 0x7fffu : ~k) << 16);
+        xj = Packed16<T>::key_value(mine_key);
       }
     } else {
       // Which experts they are: each lane looks for its own, and their places are how many are larger.
@@ -519,10 +579,14 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
       }
       return M;
     };
+    if constexpr (kPacked)
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = key[v] > Packed16<T>::kNone ? key[v] : 0u;
     int taken = 0;
     for (; taken < p.top_k; ++taken) {
       int e;
       const uint32_t M = take(e);
+      if (kPacked && taken == 0) bad = (M >> 16) > Packed16<T>::kPlusInf - (p.scoring == kScoreSoftmax ? 1u : 0u);
       if (sub == taken && M != 0u) id = e;
       if (__all_sync(0xffffffffu, M == 0u)) break;
       if constexpr (kScore) {

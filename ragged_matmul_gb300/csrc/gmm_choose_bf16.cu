@@ -1,0 +1,11 @@
+#include "gmm_choose_launch.cuh"
+
+namespace gmm {
+namespace host {
+
+int run_choose_bf16(gmm_ctx *h, const gmm::ChooseParams &p, bool score, bool grad, cudaStream_t stream) {
+  return run_choose<__nv_bfloat16>(h, p, score, grad, stream);
+}
+
+}  // namespace host
+}  // namespace gmm

@@ -1,0 +1,68 @@
+// The variants of the router's kernels and the rule that picks one, for one type of the logits.
+#pragma once
+
+#include <algorithm>
+#include <type_traits>
+
+#include "gmm_choose_launch.h"
+
+namespace gmm {
+namespace host {
+
+// Warps a CTA: fewer where a warp's `smem` bytes (64-bit keys of every expert, rows of the
+// gradient) would not leave the default 48 KB.
+inline int choose_warps(size_t smem) {
+  return static_cast<int>(std::max<size_t>(1, std::min<size_t>(gmm::kChooseWarps, 48 * 1024 / std::max<size_t>(1, smem))));
+}
+
+template <class T, int L, int V>
+int launch_choose(const gmm::ChooseParams &p, bool vec, bool score, bool grad, cudaStream_t stream) {
+  const long long warps = (p.num_tokens + 32 / L - 1) / (32 / L);
+  const bool dense = p.scoring == GMM_SCORE_SOFTMAX && !p.renormalise;
+  const size_t per_warp = grad ? static_cast<size_t>(32) * V * 4 : (score ? static_cast<size_t>(p.num_experts) * 8 : 0);
+  const int wc = choose_warps(per_warp);
+  const unsigned grid = static_cast<unsigned>((warps + wc - 1) / wc), threads = 32u * wc;
+  const size_t smem = per_warp * wc;
+  auto go = [&](auto vec_c) {
+    constexpr bool kVec = decltype(vec_c)::value;
+    if (grad) {
+      if (dense) gmm::gmm_route_grad_kernel<T, L, V, kVec, true><<<grid, threads, smem, stream>>>(p);
+      else gmm::gmm_route_grad_kernel<T, L, V, kVec, false><<<grid, threads, smem, stream>>>(p);
+    } else if constexpr (L == 32) {
+      if (score) gmm::gmm_route_kernel<T, L, V, kVec, true><<<grid, threads, smem, stream>>>(p);
+      else gmm::gmm_route_kernel<T, L, V, kVec, false><<<grid, threads, smem, stream>>>(p);
+    } else {
+      gmm::gmm_route_kernel<T, L, V, kVec, false><<<grid, threads, smem, stream>>>(p);
+    }
+  };
+  if constexpr (V * sizeof(T) <= 128) {
+    if (vec) go(std::true_type()); else go(std::false_type());
+  } else {
+    go(std::false_type());
+  }
+  return launch_status(grad ? "launch of the route gradient kernel" : "launch of the route kernel");
+}
+
+template <class T>
+int run_choose(gmm_ctx *h, const gmm::ChooseParams &p, bool score, bool grad, cudaStream_t stream) {
+  // Lanes a token: a whole warp has the shortest way through one token; with many tokens fewer
+  // lanes leave fewer of them idle.
+  const int run = p.groups > 1 ? p.group_size : p.num_experts;           // consecutive experts
+  const int need = (run + p.group_lanes - 1) / p.group_lanes;            // a lane's share in a whole warp
+  const bool many = p.groups == 1 && !score && p.num_tokens > 16 * h->num_sms;
+  const unsigned long long at = reinterpret_cast<uintptr_t>(p.logits) | static_cast<unsigned long long>(p.logits_pitch) |
+                                reinterpret_cast<uintptr_t>(p.d_logits) | static_cast<unsigned long long>(p.d_pitch);
+  auto vec = [&](int v) { return run % v == 0 && at % std::min<size_t>(16, v * sizeof(T)) == 0; };
+  if (many && p.num_experts <= 64 && p.top_k <= 8) return launch_choose<T, 8, 8>(p, vec(8), score, grad, stream);
+  if (many && p.num_experts <= 128 && p.top_k <= 8) return launch_choose<T, 8, 16>(p, vec(16), score, grad, stream);
+  if (many && p.num_experts <= 256 && p.top_k <= 8) return launch_choose<T, 8, 32>(p, vec(32), score, grad, stream);
+  if (need <= 2) return launch_choose<T, 32, 2>(p, vec(2), score, grad, stream);
+  if (need <= 4) return launch_choose<T, 32, 4>(p, vec(4), score, grad, stream);
+  if (need <= 8) return launch_choose<T, 32, 8>(p, vec(8), score, grad, stream);
+  if (need <= 16) return launch_choose<T, 32, 16>(p, vec(16), score, grad, stream);
+  if (need <= 32) return launch_choose<T, 32, 32>(p, vec(32), score, grad, stream);
+  return launch_choose<T, 32, gmm::kChooseMaxPerLane>(p, false, score, grad, stream);
+}
+
+}  // namespace host
+}  // namespace gmm

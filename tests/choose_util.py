@@ -36,8 +36,9 @@ def choose(x, top_k, scoring="softmax", bias=None, groups=1, top_groups=None, gr
         allowed = key[t] > -np.inf
         if top_groups < groups:
             total = np.full(groups, -np.inf)
+            of = x[t] if bias is None and group_top == 1 else key[t]     # as below: a single score stands in its logit's order
             for g in range(groups):
-                best = np.sort(key[t, g * per:(g + 1) * per])[::-1][:group_top]
+                best = np.sort(of[g * per:(g + 1) * per])[::-1][:group_top]
                 best = best[best > -np.inf]
                 if best.size:
                     total[g] = best.sum()

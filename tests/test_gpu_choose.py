@@ -224,6 +224,53 @@ def test_nan_logits_give_no_expert_and_are_reported(handles, dtype, many):
     assert (ids[3] == -1).all() and ids[6, 0] == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("top_k", [3, 12])
+def test_the_smallest_logits_keep_their_order(handles, dtype, top_k):
+    """Subnormal values of both signs, zeros of both signs and the smallest normal ones."""
+    torch = _t()
+    rng = np.random.default_rng(13)
+    E, T = 32, 12
+    if dtype == "fp32":
+        bits = rng.integers(0, 20, (T, E)).astype(np.int32)
+        x = torch.from_numpy((bits | (rng.integers(0, 2, (T, E)) << 31).astype(np.int64)).astype(np.int64).astype(np.uint32).view(np.float32)).cuda()
+    else:
+        bits = rng.integers(0, 20, (T, E)) | (rng.integers(0, 2, (T, E)) << 15)
+        x = torch.from_numpy(bits.astype(np.uint16).view(np.int16)).cuda().view(_dtype(dtype))
+    _check(handles(E), x, top_k, scoring="sigmoid")
+    _check(handles(E), x, top_k, scoring="softmax", groups=4, top_groups=2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("top_k", [4, 12])
+def test_nan_of_either_sign(handles, dtype, top_k):
+    torch = _t()
+    from ragged_matmul_gb300 import binding
+    rng = np.random.default_rng(14)
+    x = _logits(rng, 6, 64, dtype)
+    nan = torch.tensor([float("nan")], device="cuda").to(x.dtype)
+    x[1, 60], x[4, 0] = nan[0], -nan[0].abs()
+    view = x.view(torch.int32 if dtype == "fp32" else torch.int16)
+    view[4, 0] = -1                        # a NaN with every bit set
+    for groups, kept in ((1, 1), (8, 6)):
+        ids, w = _route(handles(64), x, top_k, scoring="sigmoid", expert_groups=groups, top_groups=kept)
+        assert binding.gmm_query_status(handles(64)) == binding.GMM_ERR_BAD_INPUT
+        assert (ids[[1, 4]] == -1).all() and (w[[1, 4]] == 0).all() and (ids[[0, 2, 3, 5]] >= 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("E", [64, 100, 128, 200, 256])
+def test_many_tokens_with_ties_and_masks(handles, E, dtype):
+    """Tokens of few different logits, next to masked ones, where several share a warp."""
+    torch = _t()
+    rng = np.random.default_rng([E, 5])
+    x = torch.from_numpy(rng.integers(-3, 4, (2600, E)).astype(np.float32)).to(_dtype(dtype)).cuda()
+    x[::7, 5:] = -float("inf")
+    x[3::11] = -float("inf")
+    _check(handles(E), x, 8, scoring="softmax")
+    _check(handles(E), x, 3, scoring="sigmoid", renormalise=False)
+
+
 def test_strides_and_one_row_for_all(handles):
     torch = _t()
     rng = np.random.default_rng(11)
