@@ -102,6 +102,16 @@ def test_with_a_bias(handles, E, top_k, scoring, dtype):
         _check(handles(E), _logits(rng, 9, E, dtype), top_k, bias=bias, scoring=scoring, renormalise=renormalise)
 
 
+@pytest.mark.parametrize("E", [1500, 1536, 2000, 2048, 4000])
+def test_shared_memory_at_every_number_of_experts(handles, E):
+    """The 64-bit keys of a token and the gradient's rows, where fewer warps share a block."""
+    torch = _t()
+    rng = np.random.default_rng(E)
+    x = _logits(rng, 9, E, "fp32")
+    ids, _ = _check(handles(E), x, 8, bias=np.full(E, 2.0), scoring="softmax", renormalise=False)
+    _check_grad(handles(E), x, ids, torch.ones((9, 8), device="cuda"), scoring="softmax", renormalise=False)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("with_bias", [False, True])
 @pytest.mark.parametrize("group_top", [1, 2])
