@@ -111,7 +111,6 @@ extern "C" int gmm_weight_grad_fp8(gmm_handle_t h, void *d_b, const void *d_t, c
   p.n_tiles = (static_cast<uint32_t>(N) + gmm::kWgTileN - 1) / gmm::kWgTileN;
   const unsigned long long total = static_cast<unsigned long long>(p.k_tiles) * p.n_tiles * num_groups;
   if (total > 0x7fffffffull) return GMM_ERR_UNSUPPORTED;
-  p.per_group = p.k_tiles * p.n_tiles;
   p.total = static_cast<uint32_t>(total);
   // Two staging buffers where a CTA has a tile or three, whose last stores are then waited for side by
   // side (fp32, 16 groups, N = 1024, K = 512: 12.8 us, with one 15.5); with more tiles one, for a deeper
@@ -121,7 +120,11 @@ extern "C" int gmm_weight_grad_fp8(gmm_handle_t h, void *d_b, const void *d_t, c
   p.num_stages = stages_of(v, num_groups, bf16, p.stg_bufs);
   if (p.num_stages < v.min_stages) return GMM_ERR_UNSUPPORTED;   // the offsets leave no room for the ring
   // As many n tiles a band as make the tiles that run side by side about as deep as they are wide.
-  p.band = 8;
+  const uint32_t band = std::min(8u, p.n_tiles);
+  p.band = gmm::WgDivisor::of(band);
+  p.rest = gmm::WgDivisor::of(std::max(1u, p.n_tiles % band));
+  p.whole = gmm::WgDivisor::of(band * p.k_tiles);
+  p.per_group = gmm::WgDivisor::of(p.k_tiles * p.n_tiles);
   p.d_scales = static_cast<const uint8_t *>(d_t_scales);
   p.a_scales = static_cast<const uint8_t *>(a_t_scales);
   p.a_offsets = rows > 0 ? a_offsets : nullptr;
