@@ -31,8 +31,8 @@ cudaLaunchConfig_t pair_config(unsigned grid, size_t smem, cudaStream_t stream, 
   return cfg;
 }
 
-size_t staging_bytes(bool bf16, int bufs) {
-  return static_cast<size_t>(bufs) * gmm::kWgEpiWarps * (bf16 ? gmm::kWgStgBytes<true> : gmm::kWgStgBytes<false>);
+size_t staging_bytes(bool bf16, int bufs) {   // buffers of all epilogue warps
+  return static_cast<size_t>(bufs) * (bf16 ? gmm::kWgStgBytes<true> : gmm::kWgStgBytes<false>);
 }
 
 int stages_of(const gmm_variant &v, int groups, bool bf16, int bufs) {
@@ -65,7 +65,7 @@ void configure_weight_grad(gmm_variant (&vars)[2], int optin, int sm_smem, int d
     const long avail = static_cast<long>(optin) - static_cast<long>(attr.sharedSizeBytes);
     if (avail <= 0 || num_sms < 2) return;
     v.budget = static_cast<size_t>(avail);
-    v.stages = stages_of(v, 1, bf16, 2);
+    v.stages = stages_of(v, 1, bf16, 8);
     if (v.stages < v.min_stages) return;
     const long reserve = static_cast<long>(sm_smem) / 2 + 1024;   // more than half an SM: one CTA per SM
     const long cap = static_cast<long>(device_optin) - static_cast<long>(attr.sharedSizeBytes);
@@ -112,12 +112,18 @@ extern "C" int gmm_weight_grad_fp8(gmm_handle_t h, void *d_b, const void *d_t, c
   const unsigned long long total = static_cast<unsigned long long>(p.k_tiles) * p.n_tiles * num_groups;
   if (total > 0x7fffffffull) return GMM_ERR_UNSUPPORTED;
   p.total = static_cast<uint32_t>(total);
-  // Two staging buffers where a CTA has a tile or three, whose last stores are then waited for side by
-  // side (fp32, 16 groups, N = 1024, K = 512: 12.8 us, with one 15.5); with more tiles one, for a deeper
-  // ring of operands (64 groups, N = 2816, K = 2048: 273 us, with two 297).  In bf16 the ring is as deep
-  // with two.
-  p.stg_bufs = bf16 || p.total <= 3u * static_cast<uint32_t>(v.grid / 2) ? 2 : 1;
-  p.num_stages = stages_of(v, num_groups, bf16, p.stg_bufs);
+  // The epilogue: warps and staging buffers of each, against stages of the operands' ring (a buffer is
+  // 4 KB in fp32 and 2 in bf16).  A warp's way through 32 columns is latency, so where a tile has few
+  // stages or a CTA few tiles, eight warps: bf16, 15 groups of 308 rows, N = 3120, K = 1152, 29.6 us
+  // with eight and 39.1 with four; fp32, 16 groups, N = 1024, K = 512, 10.4 us with two buffers
+  // each and 11.7 with four warps.  Long groups hide four (32768 rows over 8 groups, N = 14336,
+  // K = 4096, bf16: 1094 us, 1116 with eight).  Many tiles in fp32 are bound by the gradient's bytes, and
+  // the ring counts: 64 groups, N = 2816, K = 2048, 278 us with four warps of one buffer, 293 with
+  // eight, 297 with four of two.
+  const bool few = total <= 3u * static_cast<uint32_t>(v.grid / 2);
+  p.epi_warps = (bf16 ? rows / num_groups < 1024 : few) ? 8 : 4;
+  p.stg_bufs = (bf16 ? p.epi_warps == 4 : few) ? 2 : 1;
+  p.num_stages = stages_of(v, num_groups, bf16, p.epi_warps * p.stg_bufs);
   if (p.num_stages < v.min_stages) return GMM_ERR_UNSUPPORTED;   // the offsets leave no room for the ring
   // As many n tiles a band as make the tiles that run side by side about as deep as they are wide.
   const uint32_t band = std::min(8u, p.n_tiles);

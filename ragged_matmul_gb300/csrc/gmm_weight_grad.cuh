@@ -19,13 +19,13 @@
 // stages: the way of a scale (a freed entry, the peer's warps, its forwarder, the leader) takes
 // longer than the values' ring is deep.
 //
-// Roles (288 threads per CTA):
+// Roles (416 threads per CTA):
 //   warp 0       TMA producer of both operands' codes;
 //   warp 1       TMEM allocation; in the pair's leader the scale copies and MMAs, in the peer the news
 //                that its scales of a stage are written;
-//   warps 2..5   epilogue, one per TMEM lane quadrant: 32 columns at a time through shared memory to
-//                a TMA store (or reduction, when the call accumulates);
-//   warps 6..8   scales: the n rows' block, and the k rows' two.
+//   warps 2..9   epilogue, one or two per TMEM lane quadrant (the host's choice): 32 columns at a time
+//                through shared memory to a TMA store (or reduction, when the call accumulates);
+//   warps 10..12 scales: the n rows' block, and the k rows' two.
 // Every group has the same tiles, so a tile's group is a division, and the offsets are in shared
 // memory: each role finds its tiles itself.  Every wait is bounded as in the grouped kernel.
 #pragma once
@@ -36,7 +36,7 @@
 
 namespace gmm {
 
-constexpr uint32_t kWgEpiWarps = 4;
+constexpr uint32_t kWgEpiWarps = 8;
 constexpr uint32_t kWgScaleWarps = 3;
 constexpr uint32_t kWgFirstScaleWarp = 2 + kWgEpiWarps;
 constexpr int kWgThreads = 32 * static_cast<int>(2 + kWgEpiWarps + kWgScaleWarps);
@@ -86,7 +86,8 @@ struct alignas(128) WeightGradParams {
   int N;
   int K;
   int num_stages;
-  int stg_bufs;             // staging buffers per epilogue warp: 1 or 2
+  int epi_warps;            // epilogue warps at work: 4 or 8
+  int stg_bufs;             // staging buffers of each: 1 or 2
   int accumulate;
   uint32_t k_tiles;         // tiles along K, of which the first `wide` are 16 wider than `width`
   uint32_t wide;
@@ -187,7 +188,8 @@ __global__ void __launch_bounds__(kWgThreads, 1) gmm_weight_grad_fp8_kernel(cons
   const uint32_t b_ring = a_ring + ST * kWgABytes;
   const uint32_t stg_ring = b_ring + ST * kWgBBytes;
   const uint32_t stg_bufs = static_cast<uint32_t>(p.stg_bufs);
-  const uint32_t s_ring = stg_ring + kWgEpiWarps * stg_bufs * kWgStgBytes<kBf16>;
+  const uint32_t epi_warps = static_cast<uint32_t>(p.epi_warps);
+  const uint32_t s_ring = stg_ring + epi_warps * stg_bufs * kWgStgBytes<kBf16>;
   uint32_t *off = reinterpret_cast<uint32_t *>(dyn_smem + (s_ring + kWgEntries * kWgEntryBytes - dyn_base));
 
   if (tid == 0) {
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(kWgThreads, 1) gmm_weight_grad_fp8_kernel(cons
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_addr(&ctl.acc_full[a]), 1);
-      mbar_init(smem_addr(&ctl.acc_empty[a]), 2 * kWgEpiWarps);
+      mbar_init(smem_addr(&ctl.acc_empty[a]), 2 * epi_warps);
     }
     ctl.abort = 0;
     fence_barrier_init();
@@ -336,11 +338,11 @@ __global__ void __launch_bounds__(kWgThreads, 1) gmm_weight_grad_fp8_kernel(cons
   } else if (warp < static_cast<int>(kWgFirstScaleWarp)) {
     // ------------------------------------------------------------ epilogue
     const uint32_t quad = static_cast<uint32_t>(warp & 3), r = static_cast<uint32_t>(lane);
-    const uint32_t stg0 = stg_ring + static_cast<uint32_t>(warp - 2) * stg_bufs * kWgStgBytes<kBf16>;
+    const uint32_t ew = static_cast<uint32_t>(warp - 2), stg0 = stg_ring + ew * stg_bufs * kWgStgBytes<kBf16>;
     const uint32_t acc_empty0 = map_to_rank(smem_addr(&ctl.acc_empty[0]), 0);
     const bool add = p.accumulate != 0;
     uint32_t acc = 0, acc_phase = 0, buf = 0;
-    for (uint32_t t = unit0; t < total; t += units) {
+    for (uint32_t t = ew < epi_warps ? unit0 : total; t < total; t += units) {
       const WgTile x = wg_tile(p, off, t);
       const bool zero = x.stages == 0;
       if (zero && add) continue;
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(kWgThreads, 1) gmm_weight_grad_fp8_kernel(cons
         tc_fence_after_sync();
       }
       if (in) {
-        // 32 columns, or 16 at the end of a tile that is no multiple of 32 wide.
+        // 32 columns at a time, or 16 at the end of a tile that is no multiple of 32 wide.
         auto store = [&](uint32_t c, auto cols) {
           constexpr int kCols = decltype(cols)::value;
           uint32_t v[kCols];
@@ -386,9 +388,10 @@ __global__ void __launch_bounds__(kWgThreads, 1) gmm_weight_grad_fp8_kernel(cons
           }
           buf = buf + 1 == stg_bufs ? 0u : buf + 1;
         };
-        uint32_t c = 0;
-        for (; c + 32u <= x.width; c += 32u) store(c, std::integral_constant<int, 32>());
-        if (c < x.width) store(c, std::integral_constant<int, 16>());
+        for (uint32_t c = 32u * (ew >> 2); c < x.width; c += 8u * epi_warps) {
+          if (c + 32u <= x.width) store(c, std::integral_constant<int, 32>());
+          else store(c, std::integral_constant<int, 16>());
+        }
       }
       if (!zero) {
         tc_fence_before_sync();
