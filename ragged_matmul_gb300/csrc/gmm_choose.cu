@@ -77,8 +77,7 @@ int gmm_route(gmm_handle_t h, int32_t *slot_experts, float *weights, const void 
     if ((p.group_size + p.group_lanes - 1) / p.group_lanes > gmm::kChooseMaxPerLane) return GMM_ERR_UNSUPPORTED;
   }
   if (num_tokens == 0) return GMM_OK;
-  const bool score = p.bias != nullptr || (p.groups > 1 && p.group_top == 2);
-  return run_choose_dtype(h, p, dtype, score, false, stream);
+  return run_choose_dtype(h, p, dtype, p.bias != nullptr, false, stream);
 }
 
 int gmm_route_grad(gmm_handle_t h, void *d_logits, long long d_logits_stride, const float *d_weights,

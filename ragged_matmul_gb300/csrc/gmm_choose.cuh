@@ -22,15 +22,19 @@
 //     sigmoid   d x_j = g_j s_j (1 - s_j)
 // and zero elsewhere; slots that name an expert twice add up.
 //
-// The choice is that of the keys to 64-bit accuracy.  Without a bias the scores stand in the
-// order of the logits, which are compared themselves.  With one, the keys are computed in fp32;
-// two keys (or group keys) nearer than their error bounds, of different logit or bias, send the
-// token to a path that computes the candidates in 64 bits (about one token in a hundred at 256
-// experts), because fp32 sums of near keys would otherwise choose by their rounding.
+// The choice is that of the keys to 64-bit accuracy.  Without a bias the scores stand in the order of
+// the logits, which are compared themselves; a group's sum of two is a score pair.  Where fp32 keys
+// (with a bias) or sums are nearer than their error bounds and of different logit or bias, those
+// near enough to matter are computed again in 64 bits (about one token in a hundred at 256 experts),
+// because fp32 sums of near keys would otherwise choose by their rounding.
 //
-// Bound by latency and, with many tokens, by instruction issue: L lanes hold a token's logits in
-// registers, V consecutive experts each, and take the maximum top_k times.  Keys are unsigned
-// words in the order of the values, so that a maximum over 32 lanes is one redux instruction.
+// Bound by latency and, with many tokens, by instruction issue (integer minimum and maximum run at
+// half rate).  L lanes hold a token's logits in registers, V each, as unsigned keys in the order of the
+// values; sorted lists of eight are merged across the lanes.  16-bit logits carry the expert's number
+// in their key's low half.  Of 32-bit keys the lists give only the last one's value; the keys that reach
+// it are gathered, a lane each, and ranked against one another, which also settles ties.
+// Measured: 32768 tokens of 128 bf16 logits, top-8, 6.1 us; 256 tokens of 256 fp32 logits with a bias
+// and groups 4.4 us.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -118,31 +122,41 @@ __device__ __forceinline__ float choose_float(T x) {
   else return __bfloat162float(x);
 }
 
-// V consecutive logits of one token as fp32; -infinity past the lane's `n`.  kVec: the lane's run
-// is whole and aligned to its size, 16 bytes at most.
+// Where a lane's V logits lie.  kRun (every lane's run is whole, its rows aligned to 16 bytes or the run's
+// size): consecutive, one vector load.  Else a lane's logits are `step` apart, so that the lanes of a
+// token (of a group) read consecutive ones.
+template <bool kRun>
+struct ChoosePlace {
+  int first, step, end;   // experts first + v (* step), below `end`
+  __device__ __forceinline__ ChoosePlace(int base, int size, int lane, int lanes, int V)
+      : first(base + (kRun ? lane * V : lane)), step(lanes), end(base + size) {}
+  __device__ __forceinline__ int expert(int v) const { return kRun ? first + v : first + v * step; }
+  __device__ __forceinline__ bool there(int v) const { return kRun ? first < end : first + v * step < end; }
+};
+
+// A lane's logits as fp32, -infinity where there is none.
 template <class T, int V, bool kVec>
-__device__ __forceinline__ void choose_load(const T *row, int first, int n, float (&x)[V]) {
+__device__ __forceinline__ void choose_load(const T *row, const ChoosePlace<kVec> &at, float (&x)[V]) {
   constexpr int kBytes = V * static_cast<int>(sizeof(T));
   if constexpr (kVec) {
     alignas(16) T raw[V];
-    if (n > 0) {
+    const bool there = at.there(0);
+    if (there) {
       if constexpr (kBytes >= 16) {
 #pragma unroll
         for (int i = 0; i < kBytes / 16; ++i)
-          reinterpret_cast<uint4 *>(raw)[i] = __ldg(reinterpret_cast<const uint4 *>(row + first) + i);
+          reinterpret_cast<uint4 *>(raw)[i] = __ldg(reinterpret_cast<const uint4 *>(row + at.first) + i);
       } else if constexpr (kBytes == 8) {
-        *reinterpret_cast<uint2 *>(raw) = __ldg(reinterpret_cast<const uint2 *>(row + first));
-      } else if constexpr (kBytes == 4) {
-        *reinterpret_cast<uint32_t *>(raw) = __ldg(reinterpret_cast<const uint32_t *>(row + first));
+        *reinterpret_cast<uint2 *>(raw) = __ldg(reinterpret_cast<const uint2 *>(row + at.first));
       } else {
-        raw[0] = row[first];
+        *reinterpret_cast<uint32_t *>(raw) = __ldg(reinterpret_cast<const uint32_t *>(row + at.first));
       }
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) x[v] = n > 0 ? choose_float<T>(raw[v]) : -INFINITY;
+    for (int v = 0; v < V; ++v) x[v] = there ? choose_float<T>(raw[v]) : -INFINITY;
   } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) x[v] = v < n ? choose_float<T>(row[first + v]) : -INFINITY;
+    for (int v = 0; v < V; ++v) x[v] = at.there(v) ? choose_float<T>(row[at.expert(v)]) : -INFINITY;
   }
 }
 
@@ -171,38 +185,39 @@ struct Packed16 {
     const uint32_t k = key >> 16;
     return value((k & 0x8000u) ? k & 0x7fffu : ~k & 0xffffu);
   }
-  // Two keys of a word of two logits, experts e and e + 1.
-  __device__ __forceinline__ static void keys(uint32_t w, uint32_t e, uint32_t &k0, uint32_t &k1) {
+  // Two keys of a word of two logits, experts e0 and e1.
+  __device__ __forceinline__ static void keys(uint32_t w, uint32_t e0, uint32_t e1, uint32_t &k0, uint32_t &k1) {
     uint32_t sign;   // each half all ones where it is negative
     asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(sign) : "r"(w));
     const uint32_t k = w ^ (sign | 0x80008000u);
-    k0 = (k << 16) | (0xffffu - e);
-    k1 = (k & 0xffff0000u) | (0xfffeu - e);
+    k0 = (k << 16) | (0xffffu - e0);
+    k1 = (k & 0xffff0000u) | (0xffffu - e1);
   }
 };
 
-// V consecutive 16-bit logits as words, -infinity past the lane's `n`.
+// A lane's 16-bit logits as words of two, -infinity where there is none.
 template <class T, int V, bool kVec>
-__device__ __forceinline__ void choose_load16(const T *row, int first, int n, uint32_t (&w)[V / 2]) {
+__device__ __forceinline__ void choose_load16(const T *row, const ChoosePlace<kVec> &at, uint32_t (&w)[V / 2]) {
   constexpr uint32_t kPad = Packed16<T>::kPad;
   if constexpr (kVec) {
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) w[i] = kPad;
-    if (n > 0) {
+    if (at.there(0)) {
       if constexpr (V >= 8) {
 #pragma unroll
         for (int i = 0; i < V / 8; ++i)
-          *reinterpret_cast<uint4 *>(&w[4 * i]) = __ldg(reinterpret_cast<const uint4 *>(row + first) + i);
+          *reinterpret_cast<uint4 *>(&w[4 * i]) = __ldg(reinterpret_cast<const uint4 *>(row + at.first) + i);
       } else {
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(row + first) + i);
+        for (int i = 0; i < V / 2; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(row + at.first) + i);
       }
     }
   } else {
-    const unsigned short *p = reinterpret_cast<const unsigned short *>(row + first);
+    const unsigned short *p = reinterpret_cast<const unsigned short *>(row);
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) {
-      const uint32_t a = 2 * i < n ? __ldg(p + 2 * i) : kPad & 0xffffu, b = 2 * i + 1 < n ? __ldg(p + 2 * i + 1) : kPad & 0xffffu;
+      const uint32_t a = at.there(2 * i) ? __ldg(p + at.expert(2 * i)) : kPad & 0xffffu;
+      const uint32_t b = at.there(2 * i + 1) ? __ldg(p + at.expert(2 * i + 1)) : kPad & 0xffffu;
       w[i] = a | (b << 16);
     }
   }
@@ -271,72 +286,69 @@ __device__ __forceinline__ uint32_t pick8(const uint32_t (&a)[8], int j) {   // 
   return (j & 4) ? v : u;
 }
 
-// The choice of one token by 64-bit keys, by a whole warp: ids[j] for lane j < top_k.  Only the
-// experts whose fp32 key reaches `least` are looked at (all of them and the groups again where
-// `all` is set); `kept`: bit g, group g is kept.
+// Score of logit x in 64 bits; zd: softmax's sum relative to `top`.
+__device__ __forceinline__ double score64(int scoring, float x, float top, double zd) {
+  return scoring == kScoreSoftmax ? exp(static_cast<double>(x) - static_cast<double>(top)) / zd : sigmoid64(static_cast<double>(x));
+}
+
+// Softmax's sum in 64 bits, by a whole warp.
 template <class T>
-__device__ __noinline__ int choose_exact(const ChooseParams &p, const T *row, float top, float z, float least, bool all,
-                                         uint32_t kept, unsigned long long *keys) {
-  const int lane = static_cast<int>(threadIdx.x & 31u), E = p.num_experts;
+__device__ __noinline__ double choose_sum64(const T *row, int E, float top) {
   double zd = 0.0;
-  if (p.scoring == kScoreSoftmax) {
 #pragma unroll 4
-    for (int e = lane; e < E; e += 32) zd += exp(static_cast<double>(choose_float<T>(row[e])) - static_cast<double>(top));
+  for (int e = static_cast<int>(threadIdx.x & 31u); e < E; e += 32)   // several at a time: an exponential is one long chain
+    zd += exp(static_cast<double>(choose_float<T>(row[e])) - static_cast<double>(top));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) zd += __shfl_xor_sync(0xffffffffu, zd, o);
-  }
-#pragma unroll 4
-  for (int e = lane; e < E; e += 32) {   // several at a time: a 64-bit exponential is one long chain
-    const float x = choose_float<T>(row[e]);
-    unsigned long long k = 0ull;
+  for (int o = 16; o > 0; o >>= 1) zd += __shfl_xor_sync(0xffffffffu, zd, o);
+  return zd;
+}
+
+// The key of this lane's group in 64 bits, by a whole warp: the sum of its two largest keys (or the one).
+// Only experts whose fp32 key reaches `least` of their group are computed.
+template <class T>
+__device__ __noinline__ double choose_group64(const ChooseParams &p, const T *row, int base, int size, int lane, float top, float z,
+                                              float least) {
+  const double zd = p.scoring == kScoreSoftmax ? choose_sum64<T>(row, p.num_experts, top) : 0.0;
+  double m1 = -INFINITY, m2 = -INFINITY;
+  for (int i = lane; i < size; i += p.group_lanes) {
+    const float x = choose_float<T>(row[base + i]), b = __ldg(p.bias + base + i);
     const float s = p.scoring == kScoreSoftmax ? expf(x - top) / z : sigmoid32(x);
-    const float b = p.bias != nullptr ? __ldg(p.bias + e) : 0.0f;
-    if (x > -INFINITY && (all || s + b >= least))
-      k = order_key((p.scoring == kScoreSoftmax ? exp(static_cast<double>(x) - static_cast<double>(top)) / zd
-                                                : sigmoid64(static_cast<double>(x))) +
-                    static_cast<double>(b));
-    keys[e] = k;
+    if (x > -INFINITY && s + b >= least) {
+      const double k = score64(p.scoring, x, top, zd) + static_cast<double>(b);
+      m2 = fmax(fmin(k, m1), m2);
+      m1 = fmax(k, m1);
+    }
+  }
+  for (int o = p.group_lanes / 2; o > 0; o >>= 1) {
+    const double k1 = __shfl_xor_sync(0xffffffffu, m1, o), k2 = __shfl_xor_sync(0xffffffffu, m2, o);
+    m2 = fmax(fmin(m1, k1), fmax(m2, k2));
+    m1 = fmax(m1, k1);
+  }
+  return p.group_top == 2 && m2 > -static_cast<double>(INFINITY) ? m1 + m2 : m1;
+}
+
+// The choice of one token by 64-bit keys in shared memory, by a whole warp: ids[j] for lane j < top_k.  Only the
+// experts whose fp32 key reaches `least` are looked at; `kept`: bit g, group g is kept.
+template <class T>
+__device__ __noinline__ int choose_exact(const ChooseParams &p, const T *row, float top, float z, float least, uint32_t kept,
+                                         unsigned long long *keys) {
+  const int lane = static_cast<int>(threadIdx.x & 31u), E = p.num_experts;
+  const double zd = p.scoring == kScoreSoftmax ? choose_sum64<T>(row, E, top) : 0.0;
+#pragma unroll 4
+  for (int e = lane; e < E; e += 32) {
+    const float x = choose_float<T>(row[e]), b = __ldg(p.bias + e);
+    const float s = p.scoring == kScoreSoftmax ? expf(x - top) / z : sigmoid32(x);
+    keys[e] = x > -INFINITY && s + b >= least && ((kept >> (e / p.group_size)) & 1u)
+                  ? order_key(score64(p.scoring, x, top, zd) + static_cast<double>(b))
+                  : 0ull;
   }
   __syncwarp();
-  if (all && p.groups > 1) {   // lane g: group g's key
-    unsigned long long gk = 0ull;
-    if (lane < p.groups) {
-      unsigned long long m1 = 0ull, m2 = 0ull;
-      for (int i = 0; i < p.group_size; ++i) {
-        const unsigned long long k = keys[lane * p.group_size + i];
-        if (k > m1) {
-          m2 = m1;
-          m1 = k;
-        } else if (k > m2) {
-          m2 = k;
-        }
-      }
-      gk = m1;
-      if (p.group_top == 2 && m2 != 0ull) {
-        auto value = [](unsigned long long k) {
-          return __longlong_as_double(static_cast<long long>((k >> 63) ? k & ~(1ull << 63) : ~k));
-        };
-        gk = order_key(value(m1) + value(m2));
-      }
-    }
-    int rank = 0;
-    for (int g = 0; g < p.groups; ++g) {
-      const unsigned long long o = __shfl_sync(0xffffffffu, gk, g);
-      rank += o > gk || (o == gk && g < lane) ? 1 : 0;
-    }
-    kept = __ballot_sync(0xffffffffu, lane < p.groups && rank < p.top_groups);
-  }
-  if (p.bias == nullptr) {   // the experts themselves by their logits, which are exact
-    __syncwarp();
-    for (int e = lane; e < E; e += 32) keys[e] = order_key(static_cast<double>(choose_float<T>(row[e])));
-    __syncwarp();
-  }
   int id = -1;
   for (int j = 0; j < p.top_k; ++j) {
     unsigned long long m = 0ull;
     int at = E;
     for (int e = lane; e < E; e += 32)
-      if (((kept >> (e / p.group_size)) & 1u) && keys[e] > m) {
+      if (keys[e] > m) {
         m = keys[e];
         at = e;
       }
@@ -358,15 +370,14 @@ __device__ __noinline__ int choose_exact(const ChooseParams &p, const T *row, fl
   return id;
 }
 
-// One token per L lanes, 32 / L tokens a warp.  kScore: a key that is not the logit itself is
-// compared (a bias, or groups by two scores); then L = 32.  16-bit logits that are compared
-// themselves carry the expert's number in the key's low half, so that a maximum is also its place.
+// One token per L lanes, 32 / L tokens a warp (groups: L = 32).  kScore: a bias, the keys are not the logits
+// themselves; then L = 32 too.
 template <class T, int L, int V, bool kVec, bool kScore>
 __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __grid_constant__ ChooseParams p) {
   static_assert(!kScore || L == 32, "a score's token has a whole warp");
   constexpr bool kPacked = !kScore && sizeof(T) == 2;
   extern __shared__ unsigned long long choose_smem[];
-  __shared__ float2 choose_slots[kChooseWarps * (32 / L)][8];   // expert and logit of a token's chosen ones
+  __shared__ uint4 choose_slots[kPacked ? 1 : 32 * kChooseWarps];   // gathered keys: key, expert, logit, bias
   const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
   const int sub = lane & (L - 1), seg = lane & ~(L - 1);
   const uint32_t seg_mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << seg;
@@ -375,33 +386,28 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
   if (w * (32 / L) >= p.num_tokens) return;   // the whole warp
   const bool live = t < p.num_tokens;
   const T *row = reinterpret_cast<const T *>(p.logits + (live ? t : 0) * p.logits_pitch);
+  const bool softmax = p.scoring == kScoreSoftmax;
 
-  // This lane's run of experts: of group `mine`, from `first`, n of them.
-  int mine = 0, first, n;   // V at most
-  if (p.groups > 1) {
-    mine = sub / p.group_lanes;
-    const int at = (sub - mine * p.group_lanes) * V;
-    first = mine * p.group_size + at;
-    n = mine < p.groups ? max(0, min(V, p.group_size - at)) : 0;
-  } else {
-    first = sub * V;
-    n = max(0, min(V, p.num_experts - first));
-  }
+  // This lane's experts: of group `mine`.
+  const bool grouped = L == 32 && p.groups > 1;
+  const int mine = grouped ? sub / p.group_lanes : 0, part = grouped ? sub - mine * p.group_lanes : sub;
+  const int base = mine * p.group_size, size = mine < p.groups ? p.group_size : 0;
+  const ChoosePlace<kVec> at(base, size, part, grouped ? p.group_lanes : L, V);
   float x[kPacked ? 1 : V];
   uint32_t raw[kPacked ? V / 2 : 1], key[V];
-  if constexpr (kPacked) choose_load16<T, V, kVec>(row, first, n, raw);
-  else choose_load<T, V, kVec>(row, first, n, x);
+  if constexpr (kPacked) choose_load16<T, V, kVec>(row, at, raw);
+  else choose_load<T, V, kVec>(row, at, x);
   float bias[kScore ? V : 1];   // beside the logits' loads, not behind them
   if constexpr (kScore) {
-    if (p.bias != nullptr && kVec && V % 4 == 0 && p.bias_vec) {
+    if (kVec && V % 4 == 0 && p.bias_vec) {
 #pragma unroll
       for (int v = 0; v < V; v += 4) {
-        const float4 b = n > 0 ? __ldg(reinterpret_cast<const float4 *>(p.bias + first + v)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const float4 b = at.there(0) ? __ldg(reinterpret_cast<const float4 *>(p.bias + at.first + v)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         bias[v] = b.x, bias[v + 1] = b.y, bias[v + 2] = b.z, bias[v + 3] = b.w;
       }
     } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) bias[v] = p.bias != nullptr && v < n ? __ldg(p.bias + first + v) : 0.0f;
+      for (int v = 0; v < V; ++v) bias[v] = at.there(v) ? __ldg(p.bias + at.expert(v)) : 0.0f;
     }
   }
 
@@ -411,12 +417,13 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) {
       raw[i] = Packed16<T>::canonical(raw[i]);
-      Packed16<T>::keys(raw[i], static_cast<uint32_t>(first + 2 * i), key[2 * i], key[2 * i + 1]);
+      Packed16<T>::keys(raw[i], static_cast<uint32_t>(at.expert(2 * i)), static_cast<uint32_t>(at.expert(2 * i + 1)), key[2 * i],
+                        key[2 * i + 1]);
     }
   } else {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      bad |= !(x[v] < INFINITY) && (p.scoring == kScoreSoftmax || x[v] != x[v]);
+      bad |= !(x[v] < INFINITY) && (softmax || x[v] != x[v]);
       key[v] = order_key(x[v]);
     }
     bad = (__ballot_sync(0xffffffffu, bad) & seg_mask) != 0u;
@@ -424,7 +431,7 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
 
   // Softmax's maximum and sum, where a score itself is needed.
   float top = 0.0f, z = 1.0f;
-  if (p.scoring == kScoreSoftmax && (kScore || !p.renormalise)) {
+  if (softmax && (kScore || !p.renormalise)) {
     auto logit = [&](int v) {
       if constexpr (kPacked) return Packed16<T>::value((raw[v / 2] >> (16 * (v & 1))) & 0xffffu);
       else return x[v];
@@ -441,52 +448,89 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
     z = lanes_sum<L>(sum);
   }
 
-  float score_tol = 0.0f;   // two fp32 keys (of magnitude up to 1) are this near at least to be unsure of
-  bool unsure = false, unsure_groups = false;
-  uint32_t kept_lanes = 0xffffffffu;   // lanes whose group is kept
+  // How far apart two fp32 keys have to be, beside 2.4e-7 of the larger one (the bias added, twice half a
+  // step): sigmoid, each off by 3.3e-7 at most (expf and the quotient 2 units in the last place, the sum
+  // half of one); softmax, values up to 1 / z each off by V + 16 half steps (the sum's terms).
+  float score_tol = 0.0f;
   if constexpr (kScore) {
-    // expf, the sum and the quotient are each off by a few units in the last place of values up to
-    // 1; z by one a term and lane; the bias adds half of one of the key.  Two keys, so twice that.
-    score_tol = p.scoring == kScoreSoftmax ? 1.2e-7f * (V + 16) : 6e-7f;
+    score_tol = softmax ? 1.2e-7f * (V + 16) / z : 8e-7f;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (key[v] != 0u) {
-        const float s = p.scoring == kScoreSoftmax ? expf(x[v] - top) / z : sigmoid32(x[v]);
-        key[v] = order_key(s + bias[v]);
-      }
+      if (key[v] != 0u) key[v] = order_key((softmax ? expf(x[v] - top) / z : sigmoid32(x[v])) + bias[v]);
   }
-  if (p.groups > 1) {
-    float g1 = -INFINITY, g2 = -INFINITY;
+
+  uint32_t kept_lanes = 0xffffffffu;   // lanes whose group is kept
+  if (grouped) {
+    float g1 = -INFINITY, g2 = -INFINITY;   // the group's two largest keys (without a bias: logits)
     if constexpr (kPacked) {
-      uint32_t m = 0u;
+      uint32_t m1 = 0u, m2 = 0u;
 #pragma unroll
-      for (int v = 0; v < V; ++v) m = max(m, key[v]);
-      g1 = m <= Packed16<T>::kNone ? -INFINITY : static_cast<float>(m >> 16);   // any value in the keys' order
+      for (int v = 0; v < V; ++v) {
+        m2 = max(min(m1, key[v]), m2);
+        m1 = max(m1, key[v]);
+      }
+      bad = (lanes_max<L>(m1) >> 16) > Packed16<T>::kPlusInf - (softmax ? 1u : 0u);   // before its group is left out
+      if (m1 > Packed16<T>::kNone) g1 = Packed16<T>::key_value(m1);
+      if (m2 > Packed16<T>::kNone) g2 = Packed16<T>::key_value(m2);
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) merge_top2(g1, g2, key_value(key[v]), -INFINITY);
     }
     for (int o = p.group_lanes / 2; o > 0; o >>= 1)
       merge_top2(g1, g2, __shfl_xor_sync(0xffffffffu, g1, o), __shfl_xor_sync(0xffffffffu, g2, o));
-    const float gv = p.group_top == 2 && kScore && g2 > -INFINITY ? g1 + g2 : g1;
+    const bool pair = p.group_top == 2;
+    float far = 0.0f, gv = g1;   // far: how far below the largest logit the group's is
+    if (pair) {
+      if constexpr (kScore) {
+        gv = g2 > -INFINITY ? g1 + g2 : g1;
+      } else if (softmax) {   // scores relative to the largest logit's
+        float m = g1;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        top = p.renormalise ? m : top;
+        far = m - g1;
+        gv = g1 > -INFINITY ? expf(g1 - m) + expf(g2 - m) : -INFINITY;
+      } else {
+        gv = g1 > -INFINITY ? sigmoid32(g1) + sigmoid32(g2) : -INFINITY;
+      }
+    }
     const uint32_t gk = mine < p.groups ? order_key(gv) : 0u;
     int rank = 0;
     for (int g = 0; g < p.groups; ++g) {
-      const uint32_t o = __shfl_sync(0xffffffffu, gk, seg + g * p.group_lanes);
+      const uint32_t o = __shfl_sync(0xffffffffu, gk, g * p.group_lanes);
       rank += o > gk || (o == gk && g < mine) ? 1 : 0;
     }
-    const bool keep = mine < p.groups && rank < p.top_groups;
-    if constexpr (kScore) {
-      // The last group kept and the first one left out.
-      const uint32_t out = redux_max(keep || mine >= p.groups ? 0u : gk);
-      const uint32_t in = ~redux_max(keep ? ~gk : 0u);
+    bool keep = mine < p.groups && rank < p.top_groups;
+    if (kScore || pair) {
+      // The last group kept and the first one left out: near enough to be the other way round?
+      const uint32_t out = redux_max(keep || mine >= p.groups ? 0u : gk), in = ~redux_max(keep ? ~gk : 0u);
       const float a = key_value(in), b = key_value(out);
-      unsure_groups = out != 0u && in != 0u && !(a - b > 2.0f * (score_tol + 2.4e-7f * fmaxf(fabsf(a), fabsf(b))));
-      kept_lanes = __ballot_sync(0xffffffffu, keep);
-      if (p.bias == nullptr)
-#pragma unroll
-        for (int v = 0; v < V; ++v) key[v] = order_key(x[v]);   // the experts by their logits
+      float tol;
+      if constexpr (kScore) {
+        tol = 2.0f * (score_tol + 2.4e-7f * fmaxf(fabsf(a), fabsf(b)));
+      } else {   // relative: 1e-6, and of softmax's exponentials half a step of their argument
+        const float f = __uint_as_float(redux_max((keep || gk == out) && far < INFINITY ? __float_as_uint(far) : 0u));
+        tol = a * (1e-6f + 1.3e-7f * f);
+      }
+      if (out != 0u && !(a - b > tol) && !bad) {
+        double gd;
+        if constexpr (kScore) {
+          const float g = pair ? g2 : g1;
+          gd = choose_group64<T>(p, row, base, size, part, top, z,
+                                 fabsf(g) < INFINITY ? g - 2.0f * (score_tol + 2.4e-7f * fabsf(g)) : -INFINITY);
+        } else {
+          gd = score64(p.scoring, g1, top, 1.0) + score64(p.scoring, g2, top, 1.0);
+        }
+        const unsigned long long k = mine < p.groups && g1 > -INFINITY ? order_key(gd) : 0ull;
+        rank = 0;
+        for (int g = 0; g < p.groups; ++g) {
+          const unsigned long long o = __shfl_sync(0xffffffffu, k, g * p.group_lanes);
+          rank += o > k || (o == k && g < mine) ? 1 : 0;
+        }
+        keep = mine < p.groups && rank < p.top_groups;
+      }
     }
+    kept_lanes = __ballot_sync(0xffffffffu, keep);
     if (!keep)
 #pragma unroll
       for (int v = 0; v < V; ++v) key[v] = 0u;
@@ -500,59 +544,82 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
     // Every lane gets the eight largest keys, sorted.
     uint32_t best[8];
     largest8<L, V>(key, best);
-    const uint32_t mine_key = sub < p.top_k ? pick8(best, sub) : 0u;
     if constexpr (kPacked) {
+      const uint32_t mine_key = sub < p.top_k ? pick8(best, sub) : 0u;
       done = true;
-      bad = (best[0] >> 16) > Packed16<T>::kPlusInf - (p.scoring == kScoreSoftmax ? 1u : 0u);
+      bad |= (best[0] >> 16) > Packed16<T>::kPlusInf - (softmax ? 1u : 0u);
       if (mine_key > Packed16<T>::kNone) {
         id = static_cast<int>(0xffffu - (mine_key & 0xffffu));
         xj = Packed16<T>::key_value(mine_key);
       }
     } else {
-      // Which experts they are: each lane looks for its own, and their places are how many are larger.
-      // Only where no two of the list, nor the last of it and one behind it, are equal or unsure.
-      const uint32_t last = __shfl_sync(0xffffffffu, mine_key, seg + p.top_k - 1);
-      uint32_t least = last;   // keys from here on count
-      float tol = 0.0f;
-      if (kScore && p.bias != nullptr) {
-        tol = score_tol + 2.4e-7f * fmaxf(fabsf(key_value(best[0])), fabsf(key_value(last)));
-        least = order_key(key_value(last) - tol);
+      // The keys that reach the last of them (or come so near that they might belong to them), a lane each.
+      const uint32_t last = pick8(best, p.top_k - 1);
+      uint32_t least = max(last, 1u);
+      if constexpr (kScore) {
+        const float l = key_value(last);
+        if (last != 0u && l < INFINITY) least = max(order_key(l - 2.0f * (score_tol + 2.4e-7f * fabsf(l))), 1u);
       }
-      const uint32_t next_key = __shfl_down_sync(0xffffffffu, mine_key, 1);
-      bool clear = last != 0u && tol < INFINITY && !unsure_groups;
-      if (sub + 1 < p.top_k)
-        clear = clear && (tol > 0.0f ? key_value(mine_key) - key_value(next_key) > tol : mine_key != next_key);
+      uint4 *slots = choose_slots + warp * 32 + seg;
       int count = 0;
-      float2 *slot = choose_slots[warp * (32 / L) + lane / L];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const bool hit = key[v] != 0u && key[v] >= least;
-        if (__any_sync(0xffffffffu, hit)) {
-          if (hit) {
-            int at = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) at += best[j] > key[v] ? 1 : 0;
-            slot[at & 7] = make_float2(__int_as_float(first + v), x[v]);
-            ++count;
+        const bool hit = key[v] >= least;
+        const uint32_t hits = __ballot_sync(0xffffffffu, hit) & seg_mask;
+        if (hit) {
+          const int to = count + __popc(hits & ((1u << lane) - 1u));
+          if (to < L)
+            slots[to] = make_uint4(key[v], static_cast<uint32_t>(at.expert(v)), __float_as_uint(x[v]),
+                                   kScore ? __float_as_uint(bias[v]) : 0u);
+        }
+        count += __popc(hits);
+      }
+      __syncwarp();
+      done = __all_sync(0xffffffffu, count <= L);
+      if (done) {
+        const bool have = sub < count;
+        const uint4 f = have ? slots[sub] : make_uint4(0u, 0xffffffffu, 0u, 0u);
+        const float fx = __uint_as_float(f.z), fb = __uint_as_float(f.w), fv = key_value(f.x);
+        const int most = L == 32 ? count : static_cast<int>(redux_max(static_cast<uint32_t>(count)));
+        int rank = 0;
+        bool near = false;   // a key as near that its place is not sure, of another logit or bias
+        for (int i = 0; i < most; ++i) {
+          const uint32_t ko = __shfl_sync(0xffffffffu, f.x, seg + i), eo = __shfl_sync(0xffffffffu, f.y, seg + i);
+          rank += ko > f.x || (ko == f.x && eo < f.y) ? 1 : 0;
+          if constexpr (kScore) {
+            const float xo = __uint_as_float(__shfl_sync(0xffffffffu, f.z, i)), bo = __uint_as_float(__shfl_sync(0xffffffffu, f.w, i));
+            const float vo = key_value(ko);
+            near |= have && !(fabsf(vo - fv) > score_tol + 2.4e-7f * fmaxf(fabsf(vo), fabsf(fv))) && !(xo == fx && bo == fb);
           }
         }
-      }
-#pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
-      clear = clear && count == p.top_k;
-      done = __all_sync(0xffffffffu, clear);
-      __syncwarp();   // the slots are written
-      if (done && sub < p.top_k) {
-        const float2 f = slot[sub];
-        id = __float_as_int(f.x);
-        xj = f.y;
+        if constexpr (kScore) {
+          if (__any_sync(0xffffffffu, near) && !bad) {
+            const double zd = softmax ? choose_sum64<T>(row, p.num_experts, top) : 0.0;
+            const unsigned long long k = have ? order_key(score64(p.scoring, fx, top, zd) + static_cast<double>(fb)) : 0ull;
+            rank = 0;
+            for (int i = 0; i < most; ++i) {
+              const unsigned long long o = __shfl_sync(0xffffffffu, k, i);
+              const uint32_t eo = __shfl_sync(0xffffffffu, f.y, i);
+              rank += o > k || (o == k && eo < f.y) ? 1 : 0;
+            }
+          }
+        }
+        __syncwarp();   // the slots are read
+        if (have && rank < p.top_k) slots[rank] = f;
+        __syncwarp();
+        if (sub < p.top_k && sub < count) {
+          const uint4 g = slots[sub];
+          id = static_cast<int>(g.y);
+          xj = __uint_as_float(g.z);
+        }
       }
     }
   }
   if (!done) {
     // One maximum after the other.
+    bool unsure = false;
     float kth = 0.0f, prev_key = 0.0f, prev_x = 0.0f, prev_b = 0.0f;
-    auto take = [&](int &e) -> uint32_t {   // the largest key left, and its expert
+    auto take = [&](int &e) -> uint32_t {   // the largest key left, and its lowest expert
       uint32_t m = key[0];
 #pragma unroll
       for (int v = 1; v < V; ++v) m = max(m, key[v]);
@@ -562,20 +629,12 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
 #pragma unroll
         for (int v = 0; v < V; ++v) key[v] = key[v] == M ? 0u : key[v];
       } else {
-        const uint32_t holders = __ballot_sync(0xffffffffu, m == M) & seg_mask;
-        const int owner = __ffs(static_cast<int>(holders)) - 1;   // the lowest expert's lane
-        int at = 0;
-        if (lane == owner) {
-          bool found = false;
+        uint32_t lowest = 0u;   // its complement
 #pragma unroll
-          for (int v = 0; v < V; ++v)
-            if (!found && key[v] == M) {
-              at = first + v;
-              key[v] = 0u;
-              found = true;
-            }
-        }
-        e = __shfl_sync(0xffffffffu, at, owner);
+        for (int v = 0; v < V; ++v) lowest = max(lowest, key[v] == M ? ~static_cast<uint32_t>(at.expert(v)) : 0u);
+        e = static_cast<int>(~lanes_max<L>(lowest));
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = key[v] == M && at.expert(v) == e ? 0u : key[v];
       }
       return M;
     };
@@ -586,64 +645,33 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
     for (; taken < p.top_k; ++taken) {
       int e;
       const uint32_t M = take(e);
-      if (kPacked && taken == 0) bad = (M >> 16) > Packed16<T>::kPlusInf - (p.scoring == kScoreSoftmax ? 1u : 0u);
+      if (kPacked && taken == 0) bad |= (M >> 16) > Packed16<T>::kPlusInf - (softmax ? 1u : 0u);
       if (sub == taken && M != 0u) id = e;
       if (__all_sync(0xffffffffu, M == 0u)) break;
       if constexpr (kScore) {
-        if (p.bias != nullptr) {
-          const float k = key_value(M), xe = choose_float<T>(row[e]), be = __ldg(p.bias + e);
-          if (taken > 0 && !(prev_key - k > score_tol + 2.4e-7f * fabsf(prev_key)) && !(prev_x == xe && prev_b == be)) unsure = true;
-          prev_key = k;
-          prev_x = xe;
-          prev_b = be;
-          kth = k;
-        }
+        const float k = key_value(M), xe = choose_float<T>(row[e]), be = __ldg(p.bias + e);
+        if (taken > 0 && !(prev_key - k > score_tol + 2.4e-7f * fabsf(prev_key)) && !(prev_x == xe && prev_b == be)) unsure = true;
+        prev_key = k;
+        prev_x = xe;
+        prev_b = be;
+        kth = k;
       }
     }
     if constexpr (kScore) {
       const bool full = taken == p.top_k;
       const float tol = score_tol + 2.4e-7f * fabsf(kth);
-      if (p.bias != nullptr && full) {   // is one of those left as near to the last one?
+      if (full) {   // is one of those left as near to the last one?
         bool near = false;
 #pragma unroll
         for (int v = 0; v < V; ++v)
-          if (key[v] != 0u && !(kth - key_value(key[v]) > tol))
-            near |= !(x[v] == prev_x && bias[v] == prev_b);
+          if (key[v] != 0u && !(kth - key_value(key[v]) > tol)) near |= !(x[v] == prev_x && bias[v] == prev_b);
         unsure |= __any_sync(0xffffffffu, near);
       }
-      if ((unsure || unsure_groups) && !bad) {
-        // Every fp32 key that might belong among the chosen ones: where there are few, a lane each.
-        const float least = full && kth < INFINITY ? kth - 2.0f * tol : -INFINITY;
-        bool few = !unsure_groups && p.scoring == kScoreSigmoid;
-        while (few) {
-          int e;
-          const uint32_t M = take(e);
-          if (M == 0u || !(key_value(M) >= least)) break;
-          if (taken == 32) few = false;
-          else if (lane == taken++) id = e;
-        }
-        if (few) {
-          unsigned long long k = 0ull;
-          if (id >= 0)
-            k = order_key(sigmoid64(static_cast<double>(choose_float<T>(row[id]))) + static_cast<double>(__ldg(p.bias + id)));
-          int rank = 0;
-          for (int i = 0; i < taken; ++i) {
-            const unsigned long long o = __shfl_sync(0xffffffffu, k, i);
-            const int oid = __shfl_sync(0xffffffffu, id, i);
-            rank += o > k || (o == k && oid < id) ? 1 : 0;
-          }
-          int best_id = -1;
-          for (int i = 0; i < taken; ++i) {
-            const int at = __shfl_sync(0xffffffffu, rank, i), oid = __shfl_sync(0xffffffffu, id, i);
-            if (at == lane) best_id = oid;
-          }
-          id = lane < p.top_k ? best_id : -1;
-        } else {
-          uint32_t kept = 0u;
-          for (int g = 0; g < p.groups; ++g) kept |= (kept_lanes >> (g * p.group_lanes) & 1u) << g;
-          id = choose_exact<T>(p, row, top, z, least, unsure_groups || p.bias == nullptr, kept,
-                               choose_smem + static_cast<size_t>(warp) * p.num_experts);
-        }
+      if (unsure && !bad) {
+        uint32_t kept = 0u;
+        for (int g = 0; g < p.groups; ++g) kept |= (kept_lanes >> (g * p.group_lanes) & 1u) << g;
+        id = choose_exact<T>(p, row, top, z, full && kth < INFINITY ? kth - 2.0f * tol : -INFINITY, kept,
+                             choose_smem + static_cast<size_t>(warp) * p.num_experts);
       }
     }
     if (id >= 0) xj = choose_float<T>(row[id]);
@@ -663,11 +691,11 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (id < 0) wj = 0.0f;
-    else wj = p.scoring == kScoreSoftmax || m < -80.0f ? expf(xj - m) : sigmoid32(xj);
+    else wj = softmax || m < -80.0f ? expf(xj - m) : sigmoid32(xj);
     const float sum = lanes_sum<L>(wj);
     if (id >= 0) wj = wj / sum;
   } else {
-    wj = id < 0 ? 0.0f : (p.scoring == kScoreSoftmax ? expf(xj - top) / z : sigmoid32(xj));
+    wj = id < 0 ? 0.0f : (softmax ? expf(xj - top) / z : sigmoid32(xj));
   }
   if (live && sub < p.top_k) {
     const long long s = t * p.top_k + sub;
@@ -690,7 +718,7 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_grad_kernel(const
   const bool live = t < p.num_tokens;
   const T *row = reinterpret_cast<const T *>(p.logits + (live ? t : 0) * p.logits_pitch);
   float *buf = choose_row + (static_cast<size_t>(warp) * (32 / L) + lane / L) * (L * V);
-  const int first = sub * V, n = max(0, min(V, p.num_experts - first));
+  const ChoosePlace<kVec> at(0, p.num_experts, sub, L, V);
 
   int id = -1;
   float g = 0.0f, xj = -INFINITY;
@@ -710,7 +738,7 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_grad_kernel(const
   float top = 0.0f, z = 1.0f;
   bool bad = id >= 0 && (!(xj < INFINITY) && (p.scoring == kScoreSoftmax || xj != xj));
   if constexpr (kDense) {
-    choose_load<T, V, kVec>(row, first, n, x);
+    choose_load<T, V, kVec>(row, at, x);
     float m = -INFINITY;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -754,13 +782,8 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_grad_kernel(const
   }
   if (id < 0) dj = 0.0f;
 
-  if constexpr (V % 4 == 0) {
 #pragma unroll
-    for (int v = 0; v < V; v += 4) *reinterpret_cast<float4 *>(buf + first + v) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) buf[first + v] = 0.0f;
-  }
+  for (int v = 0; v < V; ++v) buf[sub + v * L] = 0.0f;
   __syncwarp();
   // A lane whose expert an earlier slot names too adds after it, in the slots' order.
   for (int j = 0; j < p.top_k; ++j) {
@@ -768,30 +791,30 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_grad_kernel(const
     __syncwarp();
   }
   if (!live) return;
-  T *out = reinterpret_cast<T *>(p.d_logits + t * p.d_pitch) + first;
+  T *out = reinterpret_cast<T *>(p.d_logits + t * p.d_pitch);
   alignas(16) T y[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    float d = buf[first + v];
+    float d = buf[kVec ? at.first + v : sub + v * L];
     if constexpr (kDense) d = bad || z == 0.0f ? 0.0f : x[v] / z * (d - common);   // z = 0: every logit is masked
     y[v] = route_from_float<T>(d);
   }
   constexpr int kBytes = V * static_cast<int>(sizeof(T));
-  if (kVec && n > 0) {
+  if constexpr (kVec) {
+    if (!at.there(0)) return;
     if constexpr (kBytes >= 16) {
 #pragma unroll
-      for (int i = 0; i < kBytes / 16; ++i) reinterpret_cast<uint4 *>(out)[i] = reinterpret_cast<const uint4 *>(y)[i];
+      for (int i = 0; i < kBytes / 16; ++i)
+        reinterpret_cast<uint4 *>(out + at.first)[i] = reinterpret_cast<const uint4 *>(y)[i];
     } else if constexpr (kBytes == 8) {
-      *reinterpret_cast<uint2 *>(out) = *reinterpret_cast<const uint2 *>(y);
-    } else if constexpr (kBytes == 4) {
-      *reinterpret_cast<uint32_t *>(out) = *reinterpret_cast<const uint32_t *>(y);
+      *reinterpret_cast<uint2 *>(out + at.first) = *reinterpret_cast<const uint2 *>(y);
     } else {
-      out[0] = y[0];
+      *reinterpret_cast<uint32_t *>(out + at.first) = *reinterpret_cast<const uint32_t *>(y);
     }
   } else {
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (v < n) out[v] = y[v];
+      if (at.there(v)) out[at.expert(v)] = y[v];
   }
 }
 

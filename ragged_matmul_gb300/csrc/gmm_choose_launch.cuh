@@ -10,9 +10,9 @@ namespace gmm {
 namespace host {
 
 // Warps a CTA: fewer where a warp's `smem` bytes (64-bit keys of every expert, rows of the
-// gradient) and the kernel's own shared memory (1 KB at most) would not fit the default 48 KB.
+// gradient) and the kernel's own shared memory (2 KB) would not fit the default 48 KB.
 inline int choose_warps(size_t smem) {
-  return static_cast<int>(std::max<size_t>(1, std::min<size_t>(gmm::kChooseWarps, 47 * 1024 / std::max<size_t>(1, smem))));
+  return static_cast<int>(std::max<size_t>(1, std::min<size_t>(gmm::kChooseWarps, 46 * 1024 / std::max<size_t>(1, smem))));
 }
 
 template <class T, int L, int V>

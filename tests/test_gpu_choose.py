@@ -157,6 +157,43 @@ def test_keys_that_32_bits_do_not_tell_apart(handles, scoring):
     _check(handles(E), x, 8, bias=np.full(E, 3.0), scoring=scoring, groups=16, top_groups=4, group_top=2)
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("top_k", [6, 12])
+def test_more_near_keys_than_lanes(handles, scoring, top_k):
+    """Every expert's key within the fp32 error of every other's, and all of them equal."""
+    torch = _t()
+    rng = np.random.default_rng(15)
+    E, T = 200, 12
+    x = (np.full((T, E), -1.5, np.float32).view(np.int32) + rng.integers(-3, 4, (T, E)).astype(np.int32)).view(np.float32)
+    x = torch.from_numpy(x).cuda()
+    bias = np.full(E, 1.0) + rng.integers(0, 2, E) * 2.0 ** -23
+    for b in (None, bias, np.zeros(E)):
+        _check(handles(E), x, top_k, bias=b, scoring=scoring)
+        _check(handles(E), x, top_k, bias=b, scoring=scoring, groups=10, top_groups=4, group_top=2)
+        _check(handles(E), torch.zeros_like(x), top_k, bias=b, scoring=scoring, groups=10, top_groups=4, group_top=1)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_groups_far_below(handles, scoring, dtype):
+    """Groups of logits so low that their scores are tiny or underflow, some with one expert left."""
+    torch = _t()
+    rng = np.random.default_rng(16)
+    E, T = 64, 30
+    x = _logits(rng, T, E, "fp32")
+    x[:10] -= 20.0
+    x[10:20, ::2] -= 60.0
+    x[20:] *= 20.0
+    x[:, 8:15] = -float("inf")
+    x = x.to(_dtype(dtype))
+    bias = 0.01 * rng.standard_normal(E)
+    bias[40:47] = -np.inf
+    bias[50] = np.inf
+    for b in (None, bias):
+        for group_top in (1, 2):
+            _check(handles(E), x, 8, bias=b, scoring=scoring, groups=8, top_groups=3, group_top=group_top)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("with_bias", [False, True])
