@@ -30,9 +30,9 @@
 //
 // Bound by latency and, with many tokens, by instruction issue (integer minimum and maximum run at
 // half rate).  L lanes hold a token's logits in registers, V each, as unsigned keys in the order of the
-// values; sorted lists of eight are merged across the lanes.  16-bit logits carry the expert's number
-// in their key's low half.  Of 32-bit keys the lists give only the last one's value; the keys that reach
-// it are gathered, a lane each, and ranked against one another, which also settles ties.
+// values.  16-bit logits carry the expert's number in their key's low half, and sorted lists of eight are
+// merged across the lanes.  Of 32-bit keys those that reach a bound are gathered, a lane each, and
+// ranked against one another, which also settles ties.
 // Measured: 32768 tokens of 128 bf16 logits, top-8, 6.1 us; 256 tokens of 256 fp32 logits with a bias
 // and groups 4.4 us.
 #pragma once
@@ -225,6 +225,13 @@ __device__ __forceinline__ void choose_load16(const T *row, const ChoosePlace<kV
 
 // Off by about 4 units in the last place (the quotient by 2); 0 below about -87.
 __device__ __forceinline__ float sigmoid32(float x) { return __fdividef(1.0f, 1.0f + expf(-x)); }
+// For keys, which allow for its error: 2.7e-7 at most (the exponential of 2^-22 relative and 2^-24 a unit of x,
+// times s (1 - s); the sum half a step, the quotient one unit in the last place).
+__device__ __forceinline__ float sigmoid_key(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-x)));
+  return r;
+}
 __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
 
 // The largest two of a run of lanes, each lane with its own two.
@@ -424,7 +431,7 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       bad |= !(x[v] < INFINITY) && (softmax || x[v] != x[v]);
-      key[v] = order_key(x[v]);
+      if constexpr (!kScore) key[v] = order_key(x[v]);
     }
     bad = (__ballot_sync(0xffffffffu, bad) & seg_mask) != 0u;
   }
@@ -444,19 +451,23 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
     top = m > -INFINITY ? m : 0.0f;
     float sum = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) sum += expf(logit(v) - top);
+    for (int v = 0; v < V; ++v) sum += kScore ? __expf(logit(v) - top) : expf(logit(v) - top);
     z = lanes_sum<L>(sum);
   }
 
   // How far apart two fp32 keys have to be, beside 2.4e-7 of the larger one (the bias added, twice half a
-  // step): sigmoid, each off by 3.3e-7 at most (expf and the quotient 2 units in the last place, the sum
-  // half of one); softmax, values up to 1 / z each off by V + 16 half steps (the sum's terms).
+  // step), for their order to be sure.  sigmoid: each is off by sigmoid_key's error.  softmax: an
+  // exponential at distance d below the largest is exp(-d) off by 2.4e-7 + 1.5e-7 d relative, 3e-7 at
+  // most, the sum by as much and V + 5 half steps, the quotient by one step: 2 (9 + V + 5) half steps of 1 / z.
   float score_tol = 0.0f;
   if constexpr (kScore) {
-    score_tol = softmax ? 1.2e-7f * (V + 16) / z : 8e-7f;
+    score_tol = softmax ? 1.2e-7f * (V + 20) / z : 6e-7f;
+    const float rz = 1.0f / z;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (key[v] != 0u) key[v] = order_key((softmax ? expf(x[v] - top) / z : sigmoid32(x[v])) + bias[v]);
+    for (int v = 0; v < V; ++v) {
+      const float k = (softmax ? __expf(x[v] - top) * rz : sigmoid_key(x[v])) + bias[v];
+      key[v] = x[v] > -INFINITY ? order_key(k) : 0u;
+    }
   }
 
   uint32_t kept_lanes = 0xffffffffu;   // lanes whose group is kept
@@ -541,10 +552,10 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
   float xj = -INFINITY;
   bool done = false;
   if (p.top_k <= 8) {
-    // Every lane gets the eight largest keys, sorted.
-    uint32_t best[8];
-    largest8<L, V>(key, best);
     if constexpr (kPacked) {
+      // Every lane gets the eight largest keys, sorted.
+      uint32_t best[8];
+      largest8<L, V>(key, best);
       const uint32_t mine_key = sub < p.top_k ? pick8(best, sub) : 0u;
       done = true;
       bad |= (best[0] >> 16) > Packed16<T>::kPlusInf - (softmax ? 1u : 0u);
@@ -553,13 +564,32 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
         xj = Packed16<T>::key_value(mine_key);
       }
     } else {
-      // The keys that reach the last of them (or come so near that they might belong to them), a lane each.
-      const uint32_t last = pick8(best, p.top_k - 1);
-      uint32_t least = max(last, 1u);
-      if constexpr (kScore) {
-        const float l = key_value(last);
-        if (last != 0u && l < INFINITY) least = max(order_key(l - 2.0f * (score_tol + 2.4e-7f * fabsf(l))), 1u);
+      // A key that top_k others reach: with a whole warp the top_k-th largest of the lanes' largest (about
+      // nine keys reach the eighth), else the top_k-th largest itself, from sorted lists.
+      uint32_t least;
+      if constexpr (L == 32) {
+        uint32_t m = key[0];
+#pragma unroll
+        for (int v = 1; v < V; ++v) m = max(m, key[v]);
+#pragma unroll
+        for (int k = 2; k <= 32; k <<= 1)   // a bitonic sort across the lanes, descending
+#pragma unroll
+          for (int j = k >> 1; j > 0; j >>= 1) {
+            const uint32_t o = __shfl_xor_sync(0xffffffffu, m, j);
+            m = ((lane & j) == 0) == ((lane & k) == 0) ? max(m, o) : min(m, o);
+          }
+        least = __shfl_sync(0xffffffffu, m, p.top_k - 1);
+      } else {
+        uint32_t best[8];
+        largest8<L, V>(key, best);
+        least = pick8(best, p.top_k - 1);
       }
+      if constexpr (kScore) {   // and those that are so near that they might belong to them
+        const float l = key_value(least);
+        if (least != 0u && l < INFINITY) least = order_key(l - 2.0f * (score_tol + 2.4e-7f * fabsf(l)));
+      }
+      least = max(least, 1u);
+      // They are gathered, a lane each, and ranked against one another.
       uint4 *slots = choose_slots + warp * 32 + seg;
       int count = 0;
 #pragma unroll
@@ -577,40 +607,44 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
       __syncwarp();
       done = __all_sync(0xffffffffu, count <= L);
       if (done) {
-        const bool have = sub < count;
-        const uint4 f = have ? slots[sub] : make_uint4(0u, 0xffffffffu, 0u, 0u);
-        const float fx = __uint_as_float(f.z), fb = __uint_as_float(f.w), fv = key_value(f.x);
         const int most = L == 32 ? count : static_cast<int>(redux_max(static_cast<uint32_t>(count)));
+        const bool have = sub < count;
+        uint4 f = have ? slots[sub] : make_uint4(0u, 0xffffffffu, 0u, 0u);
         int rank = 0;
-        bool near = false;   // a key as near that its place is not sure, of another logit or bias
         for (int i = 0; i < most; ++i) {
           const uint32_t ko = __shfl_sync(0xffffffffu, f.x, seg + i), eo = __shfl_sync(0xffffffffu, f.y, seg + i);
           rank += ko > f.x || (ko == f.x && eo < f.y) ? 1 : 0;
-          if constexpr (kScore) {
-            const float xo = __uint_as_float(__shfl_sync(0xffffffffu, f.z, i)), bo = __uint_as_float(__shfl_sync(0xffffffffu, f.w, i));
-            const float vo = key_value(ko);
-            near |= have && !(fabsf(vo - fv) > score_tol + 2.4e-7f * fmaxf(fabsf(vo), fabsf(fv))) && !(xo == fx && bo == fb);
-          }
         }
+        __syncwarp();   // the slots are read
+        if (have) slots[rank] = f;
+        __syncwarp();
+        if (have) f = slots[sub];   // in descending order now
         if constexpr (kScore) {
+          // A key as near to its neighbour that their order is not sure, of another logit or bias?  (Behind
+          // the last one too: equal ones may stand between it and one that belongs before them.)
+          const float v = key_value(f.x), vo = key_value(__shfl_down_sync(0xffffffffu, f.x, 1));
+          const uint32_t xo = __shfl_down_sync(0xffffffffu, f.z, 1), bo = __shfl_down_sync(0xffffffffu, f.w, 1);
+          const bool near = sub + 1 < count && !(v - vo > score_tol + 2.4e-7f * fmaxf(fabsf(v), fabsf(vo))) &&
+                            !(__uint_as_float(xo) == __uint_as_float(f.z) && __uint_as_float(bo) == __uint_as_float(f.w));
           if (__any_sync(0xffffffffu, near) && !bad) {
             const double zd = softmax ? choose_sum64<T>(row, p.num_experts, top) : 0.0;
-            const unsigned long long k = have ? order_key(score64(p.scoring, fx, top, zd) + static_cast<double>(fb)) : 0ull;
+            const unsigned long long k =
+                have ? order_key(score64(p.scoring, __uint_as_float(f.z), top, zd) + static_cast<double>(__uint_as_float(f.w))) : 0ull;
             rank = 0;
             for (int i = 0; i < most; ++i) {
               const unsigned long long o = __shfl_sync(0xffffffffu, k, i);
               const uint32_t eo = __shfl_sync(0xffffffffu, f.y, i);
               rank += o > k || (o == k && eo < f.y) ? 1 : 0;
             }
+            __syncwarp();
+            if (have) slots[rank] = f;
+            __syncwarp();
+            if (have) f = slots[sub];
           }
         }
-        __syncwarp();   // the slots are read
-        if (have && rank < p.top_k) slots[rank] = f;
-        __syncwarp();
-        if (sub < p.top_k && sub < count) {
-          const uint4 g = slots[sub];
-          id = static_cast<int>(g.y);
-          xj = __uint_as_float(g.z);
+        if (have && sub < p.top_k) {
+          id = static_cast<int>(f.y);
+          xj = __uint_as_float(f.z);
         }
       }
     }

@@ -220,6 +220,22 @@ def test_masked_experts(handles, scoring, dtype, with_bias):
     assert (ids[12:14] == -1).all() and (w[12:14] == 0).all()
 
 
+def test_equal_keys_between_near_ones(handles):
+    """An expert whose exact key belongs among the chosen ones, behind equal keys that its fp32 key follows."""
+    torch = _t()
+    E = 40
+    x = np.full((64, E), -3.0, np.float32)
+    bias = np.zeros(E, np.float32)
+    rng = np.random.default_rng(17)
+    for t in range(64):
+        at = rng.permutation(E)[:6]
+        x[t, at[:4]] = 1.0                                  # equal
+        x[t, at[4:]] = np.nextafter(np.float32(1.0), np.float32(2.0)) if t % 2 else np.nextafter(np.float32(1.0), np.float32(0.0))
+    for top_k in (1, 2, 3, 4, 5):
+        _check(handles(E), torch.from_numpy(x).cuda(), top_k, bias=bias, scoring="sigmoid")
+        _check(handles(E), torch.from_numpy(x).cuda(), top_k, bias=bias + 1, scoring="softmax")
+
+
 def test_every_key_infinite(handles):
     """Biases of +infinity force experts; among them the lowest come first."""
     rng = np.random.default_rng(8)
