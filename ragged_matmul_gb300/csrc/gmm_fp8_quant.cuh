@@ -284,47 +284,59 @@ __global__ void __launch_bounds__(kQ8Threads, sizeof(T) == 2 ? 4 : 2) gmm_quanti
   __shared__ uint32_t part[kWarps][kWords * 16];
   __shared__ __align__(16) float inv[kQ8Block];
   __shared__ float2 row_scale[kQ8Block];
-  __shared__ int source[kQ8Block];
   __shared__ uint32_t s_first, s_rows;
   const int tid = threadIdx.x, cv = tid & 15, rg = tid >> 4, lane = tid & 31, warp = tid >> 5;
   const uint32_t block = blockIdx.x / static_cast<uint32_t>(p.blocks), cb = blockIdx.x - block * p.blocks;
 
-  // The group whose blocks hold this one; offsets that decrease or lead past the buffers: nothing.
-  if (tid == 0) s_rows = 0;
-  __syncthreads();
+  // The group whose blocks hold this one; offsets that decrease or lead past the buffers: nothing.  Up to 32
+  // groups every warp looks for itself, which saves two barriers.
   bool bad = false;
-  for (int g = tid; g < p.groups; g += kQ8Threads) {
+  uint32_t first = 0, n = 0;
+  auto look = [&](int g) {
     const uint32_t r0 = __ldg(p.a_offsets + g), r1 = __ldg(p.a_offsets + g + 1);
     bad |= r1 < r0 || r1 > static_cast<uint32_t>(p.rows);
-    const uint32_t base = r0 / kQ8Block + static_cast<uint32_t>(g);
-    if (!bad && block >= base && (block - base) * kQ8Block < r1 - r0) {
-      s_first = r0 + (block - base) * kQ8Block;
-      s_rows = min(static_cast<uint32_t>(kQ8Block), r1 - r0 - (block - base) * kQ8Block);
+    const uint32_t at = block - (r0 / kQ8Block + static_cast<uint32_t>(g));   // of the group's blocks
+    if (!bad && at < 0x80000000u && at * kQ8Block < r1 - r0) {
+      first = r0 + at * kQ8Block;
+      n = min(static_cast<uint32_t>(kQ8Block), r1 - r0 - at * kQ8Block);
     }
+  };
+  if (p.groups <= 32) {
+    if (lane < p.groups) look(lane);
+    bad = __any_sync(0xffffffffu, bad);
+    n = __reduce_max_sync(0xffffffffu, n);
+    first = __reduce_max_sync(0xffffffffu, first);
+  } else {
+    if (tid == 0) s_rows = 0;
+    __syncthreads();
+    for (int g = tid; g < p.groups; g += kQ8Threads) look(g);
+    if (n != 0) {
+      s_first = first;
+      s_rows = n;
+    }
+    bad = __syncthreads_or(bad);
+    n = s_rows;
+    first = s_first;
   }
-  if (__syncthreads_or(bad)) {
+  if (bad) {
     if (tid == 0 && blockIdx.x == 0) atomicOr(p.status, kStatusBadOffsets);
     return;
   }
-  const uint32_t n = s_rows;
   if (n == 0) return;   // no group's block
-  const uint32_t first = s_first;
-  if (p.row_slots != nullptr) {
-    if (tid < kQ8Block) source[tid] = static_cast<uint32_t>(tid) < n ? quant8_source(p, static_cast<int>(first) + tid) : -1;
-    __syncthreads();
-  }
+
+  // Source rows: the lane of column piece i < 8 finds the one of row rg 8 + i.
+  int src = -1;
+  if (cv < 8 && static_cast<uint32_t>(rg * 8 + cv) < n) src = quant8_source(p, static_cast<int>(first) + rg * 8 + cv);
+  const uint32_t live = (__ballot_sync(0xffffffffu, src >= 0) >> (lane & 16)) & 0xffu;   // bit i: row rg 8 + i has one
 
   const int c0 = static_cast<int>(cb) * kQ8Block, col = c0 + cv * 8;
   const bool in = col < p.width;
   QuantRaw8<T> raw[8];
-  bool live[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int r = rg * 8 + i;
     raw[i] = QuantRaw8<T>{};
-    const int src = static_cast<uint32_t>(r) >= n ? -1 : (p.row_slots != nullptr ? source[r] : static_cast<int>(first) + r);
-    live[i] = src >= 0;
-    if (live[i] && in) raw[i] = quant_load8<T, kVec>(p.x + src * p.x_pitch + static_cast<long long>(col) * sizeof(T));
+    const int from = __shfl_sync(0xffffffffu, src, (lane & 16) + i);
+    if (from >= 0 && in) raw[i] = quant_load8<T, kVec>(p.x + from * p.x_pitch + static_cast<long long>(col) * sizeof(T));
   }
 
   // Largest magnitudes of the columns: over the thread's rows, the warp's, the CTA's.
@@ -367,14 +379,14 @@ __global__ void __launch_bounds__(kQ8Threads, sizeof(T) == 2 ? 4 : 2) gmm_quanti
     const int r = rg * 8 + mine;
     if ((lane & 1) == 0) {
       row_scale[r] = make_float2(c.s, c.how == 3 ? -1.0f : c.r);   // -1: divide; 0: all codes are zero
-      if (static_cast<uint32_t>(r) < n && (p.row_slots == nullptr || source[r] >= 0))
+      if ((live >> mine) & 1u)
         p.scales[static_cast<size_t>(first + static_cast<uint32_t>(r)) * p.blocks + cb] = c.s;
     }
     __syncwarp();
     uint8_t *out = p.q + static_cast<size_t>(first + static_cast<uint32_t>(rg * 8)) * p.width + col;
 #pragma unroll
     for (int i = 0; i < 8; ++i, out += p.width) {
-      if (!live[i] || !in) continue;
+      if (!((live >> i) & 1u) || !in) continue;
       const float2 f = row_scale[rg * 8 + i];
       float v[8], y[8];   // -x, and x / s
 #pragma unroll
