@@ -38,7 +38,9 @@
  * gmm_matmul_int4's single group, per-CTA tensor-map slots, and the chunk counts of
  * gmm_dispatch) that every launch made through it rewrites.  Launches made through the
  * same handle must therefore not overlap on the GPU: issue them on one stream, or
- * use one handle per stream.
+ * use one handle per stream.  (gmm_route, gmm_route_grad, the gmm_quantize_fp8 calls and
+ * gmm_weight_grad_fp8 use nothing of it but the status word, and may overlap with one
+ * another and with other calls.)
  */
 #ifndef GMM_H_
 #define GMM_H_

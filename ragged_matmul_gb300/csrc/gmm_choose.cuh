@@ -33,8 +33,9 @@
 // values.  16-bit logits carry the expert's number in their key's low half, and sorted lists of eight are
 // merged across the lanes.  Of 32-bit keys those that reach a bound are gathered, a lane each, and
 // ranked against one another, which also settles ties.
-// Measured: 32768 tokens of 128 bf16 logits, top-8, 6.1 us; 256 tokens of 256 fp32 logits with a bias
-// and groups 4.4 us.
+// Measured: 32768 tokens of 128 bf16 logits, top-8, 5.7 us (their bytes
+// take 1.5); 256 tokens of 256 fp32 logits with a bias and groups 4.1 us, 5.6 with a token in 64 bits; one token
+// 1.8 us, about an empty launch.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -738,7 +739,8 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
   }
 }
 
-// The gradient.  L lanes a token; a token's row of d_logits is put together in shared memory (zeros,
+// The gradient (16384 tokens of 64 bf16 logits, all of them in it, 4.2 us; 5003 of 161 fp32 4.2 us: latency of
+// one pass).  L lanes a token; a token's row of d_logits is put together in shared memory (zeros,
 // then the chosen experts') and written V consecutive experts a lane; kDense (softmax, not
 // renormalised): every logit is read, and every expert's value is its score times a difference.
 template <class T, int L, int V, bool kVec, bool kDense>

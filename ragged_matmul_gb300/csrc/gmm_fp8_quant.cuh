@@ -15,7 +15,9 @@
 //           blocks from group to group, so no prefix sum is needed, and each group's rows are a
 //           K-major operand of its own for the weight gradient's MMA.
 //
-// All three read and write every byte once and are bound by that.  Quotients are the correctly
+// All three read and write every byte once and are bound by that: tiles of 64 matrices of 2816 x 2048 bf16
+// 155 us (7.1 TB/s); rows in both forms, 32768 x 4096 bf16, 93 us (5.8 TB/s; 17 instructions an element, of
+// which the exact quotients of the rows take a tenth).  Quotients are the correctly
 // rounded ones, as for the 4-bit formats (see gmm_fp4_quant.cuh), and powers of two divide exactly.
 #pragma once
 
@@ -274,7 +276,8 @@ __device__ __forceinline__ uint32_t quant_bits(uint32_t m) {
   else return m << 16;
 }
 
-// Cols: a CTA takes 128 rows of a group and 128 columns; thread (cv, rg) holds 8 columns from 8 cv
+// Cols: a CTA takes 128 rows of a group and 128 columns (four CTAs an SM for 16-bit rows: 99 us, 114 with
+// three); thread (cv, rg) holds 8 columns from 8 cv
 // of 8 rows from 8 rg, so that a warp's load is two whole row pieces, a column's codes of 8 rows are
 // 8 bytes of the transposed tile in shared memory, and a row's codes of 8 columns 8 bytes of q.
 template <class T, bool kVec, bool kBoth>

@@ -26,6 +26,11 @@
 //   warps 2..9   epilogue, one or two per TMEM lane quadrant (the host's choice): 32 columns at a time
 //                through shared memory to a TMA store (or reduction, when the call accumulates);
 //   warps 10..12 scales: the n rows' block, and the k rows' two.
+// Measured: 32768 rows over 8 groups, N = 14336, K = 4096, bf16: 1083 us, 3.55 PFLOP/s; 1245 back to back,
+// at the power cap.  Power bounds it: the tensor pipe is 83% active at 1.64 GHz (ncu, half the groups of half
+// the rows), and the launch without operand loads and epilogue takes 12% fewer cycles.  Many short groups in
+// fp32 (64 groups, 16384 rows, N = 2816, K = 2048): 278 us, the gradient's 1.5 GB at 5.3 TB/s.
+//
 // Every group has the same tiles, so a tile's group is a division, and the offsets are in shared
 // memory: each role finds its tiles itself.  Every wait is bounded as in the grouped kernel.
 #pragma once
