@@ -517,13 +517,11 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
       // The last group kept and the first one left out: near enough to be the other way round?
       const uint32_t out = redux_max(keep || mine >= p.groups ? 0u : gk), in = ~redux_max(keep ? ~gk : 0u);
       const float a = key_value(in), b = key_value(out);
-      float tol;
-      if constexpr (kScore) {
-        tol = 2.0f * (score_tol + 2.4e-7f * fmaxf(fabsf(a), fabsf(b)));
-      } else {   // relative: 1e-6, and of softmax's exponentials half a step of their argument
-        const float f = __uint_as_float(redux_max((keep || gk == out) && far < INFINITY ? __float_as_uint(far) : 0u));
-        tol = a * (1e-6f + 1.3e-7f * f);
-      }
+      float of = far;   // what a group's error grows with: of a sum the terms' magnitudes, which may cancel
+      if constexpr (kScore) of = fabsf(g1) + (pair && g2 > -INFINITY ? fabsf(g2) : 0.0f);
+      of = __uint_as_float(redux_max((keep || gk == out) && of < INFINITY ? __float_as_uint(of) : 0u));
+      // Without a bias relative: 1e-6, and of softmax's exponentials half a step of their argument.
+      const float tol = kScore ? 2.0f * (score_tol + 2.4e-7f * of) : a * (1e-6f + 1.3e-7f * of);
       if (out != 0u && !(a - b > tol) && !bad) {
         double gd;
         if constexpr (kScore) {

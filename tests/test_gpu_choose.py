@@ -174,6 +174,15 @@ def test_more_near_keys_than_lanes(handles, scoring, top_k):
 
 
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_groups_whose_terms_cancel(handles, scoring):
+    """Biases of opposite signs, far larger than the scores: a group's sum is small and its fp32 error is not."""
+    rng = np.random.default_rng(18)
+    E = 16
+    bias = np.where(np.arange(E) % 2 == 0, 1000.0, -1000.0)
+    _check(handles(E), _logits(rng, 1500, E, "fp32", spread=0.5), 4, bias=bias, scoring=scoring, groups=8, top_groups=3, group_top=2)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_groups_far_below(handles, scoring, dtype):
     """Groups of logits so low that their scores are tiny or underflow, some with one expert left."""
