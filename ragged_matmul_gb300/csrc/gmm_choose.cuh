@@ -381,7 +381,7 @@ __device__ __noinline__ int choose_exact(const ChooseParams &p, const T *row, fl
 // One token per L lanes, 32 / L tokens a warp (groups: L = 32).  kScore: a bias, the keys are not the logits
 // themselves; then L = 32 too.
 template <class T, int L, int V, bool kVec, bool kScore>
-__global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __grid_constant__ ChooseParams p) {
+__global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (V <= 32 ? 4 : 1)) gmm_route_kernel(const __grid_constant__ ChooseParams p) {
   static_assert(!kScore || L == 32, "a score's token has a whole warp");
   constexpr bool kPacked = !kScore && sizeof(T) == 2;
   extern __shared__ unsigned long long choose_smem[];
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
   } else {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      bad |= !(x[v] < INFINITY) && (softmax || x[v] != x[v]);
+      bad |= softmax ? !(x[v] < INFINITY) : x[v] != x[v];
       if constexpr (!kScore) key[v] = order_key(x[v]);
     }
     bad = (__ballot_sync(0xffffffffu, bad) & seg_mask) != 0u;
@@ -463,11 +463,13 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
   float score_tol = 0.0f;
   if constexpr (kScore) {
     score_tol = softmax ? 1.2e-7f * (V + 20) / z : 6e-7f;
-    const float rz = 1.0f / z;
+    if (softmax) {
+      const float rz = 1.0f / z;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float k = (softmax ? __expf(x[v] - top) * rz : sigmoid_key(x[v])) + bias[v];
-      key[v] = x[v] > -INFINITY ? order_key(k) : 0u;
+      for (int v = 0; v < V; ++v) key[v] = x[v] > -INFINITY ? order_key(__expf(x[v] - top) * rz + bias[v]) : 0u;
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = x[v] > -INFINITY ? order_key(sigmoid_key(x[v]) + bias[v]) : 0u;
     }
   }
 
@@ -598,7 +600,7 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_kernel(const __gr
         if (hit) {
           const int to = count + __popc(hits & ((1u << lane) - 1u));
           if (to < L)
-            slots[to] = make_uint4(key[v], static_cast<uint32_t>(at.expert(v)), __float_as_uint(x[v]),
+            slots[to] = make_uint4(key[v], static_cast<uint32_t>(at.expert(v)), __float_as_uint(kScore ? x[v] : key_value(key[v])),
                                    kScore ? __float_as_uint(bias[v]) : 0u);
         }
         count += __popc(hits);
