@@ -25,7 +25,6 @@ int check_route(gmm_ctx *h, gmm::ChooseParams &p, const void *logits, long long 
   p.scoring = o->scoring;
   p.groups = 1;
   p.group_size = E;
-  p.group_lanes = 32;
   p.top_groups = 1;
   p.group_top = 1;
   p.renormalise = o->renormalise != 0;
@@ -70,11 +69,11 @@ int gmm_route(gmm_handle_t h, int32_t *slot_experts, float *weights, const void 
   if (options->top_groups < groups) {   // else every group is kept
     p.groups = groups;
     p.group_size = E / groups;
-    p.group_lanes = 1;
-    while (2 * p.group_lanes * groups <= 32) p.group_lanes *= 2;
+    int lanes = 1;   // of a group, in a whole warp
+    while (2 * lanes * groups <= 32) lanes *= 2;
     p.top_groups = options->top_groups;
     p.group_top = options->group_top;
-    if ((p.group_size + p.group_lanes - 1) / p.group_lanes > gmm::kChooseMaxPerLane) return GMM_ERR_UNSUPPORTED;
+    if ((p.group_size + lanes - 1) / lanes > gmm::kChooseMaxPerLane) return GMM_ERR_UNSUPPORTED;
   }
   if (num_tokens == 0) return GMM_OK;
   return run_choose_dtype(h, p, dtype, p.bias != nullptr, false, stream);

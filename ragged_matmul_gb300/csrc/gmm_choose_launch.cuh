@@ -16,7 +16,8 @@ inline int choose_warps(size_t smem) {
 }
 
 template <class T, int L, int V>
-int launch_choose(const gmm::ChooseParams &p, bool vec, bool score, bool grad, cudaStream_t stream) {
+int launch_choose(gmm::ChooseParams p, bool vec, bool score, bool grad, cudaStream_t stream) {
+  for (p.group_lanes = L; p.group_lanes > 1 && p.group_lanes * p.groups > L;) p.group_lanes /= 2;
   const long long warps = (p.num_tokens + 32 / L - 1) / (32 / L);
   const bool dense = p.scoring == GMM_SCORE_SOFTMAX && !p.renormalise;
   const size_t per_warp = grad ? static_cast<size_t>(32) * V * 4 : (score ? static_cast<size_t>(p.num_experts) * 8 : 0);
@@ -43,19 +44,25 @@ int launch_choose(const gmm::ChooseParams &p, bool vec, bool score, bool grad, c
   return launch_status(grad ? "launch of the route gradient kernel" : "launch of the route kernel");
 }
 
+// The most logits that one of a token's `lanes` holds.
+inline int choose_share(const gmm::ChooseParams &p, int lanes) {
+  int per_group = lanes;
+  while (per_group > 1 && per_group * p.groups > lanes) per_group /= 2;
+  return per_group * p.groups > lanes ? 1 << 30 : (p.group_size + per_group - 1) / per_group;
+}
+
 template <class T>
 int run_choose(gmm_ctx *h, const gmm::ChooseParams &p, bool score, bool grad, cudaStream_t stream) {
-  // Lanes a token: a whole warp has the shortest way through one token; with many tokens fewer
-  // lanes leave fewer of them idle.
-  const int run = p.groups > 1 ? p.group_size : p.num_experts;           // consecutive experts
-  const int need = (run + p.group_lanes - 1) / p.group_lanes;            // a lane's share in a whole warp
-  const bool many = p.groups == 1 && !score && p.num_tokens > 16 * h->num_sms;
+  // Lanes a token: a whole warp has the shortest way through one token; with many tokens eight
+  // lanes leave fewer of them idle.  With a bias always a whole warp.
+  const bool many = !score && p.num_tokens > 16 * h->num_sms && p.top_k <= 8;
+  const int need8 = choose_share(p, 8), need = choose_share(p, 32);
   const unsigned long long at = reinterpret_cast<uintptr_t>(p.logits) | static_cast<unsigned long long>(p.logits_pitch) |
                                 reinterpret_cast<uintptr_t>(p.d_logits) | static_cast<unsigned long long>(p.d_pitch);
-  auto vec = [&](int v) { return run % v == 0 && at % std::min<size_t>(16, v * sizeof(T)) == 0; };
-  if (many && p.num_experts <= 64 && p.top_k <= 8) return launch_choose<T, 8, 8>(p, vec(8), score, grad, stream);
-  if (many && p.num_experts <= 128 && p.top_k <= 8) return launch_choose<T, 8, 16>(p, vec(16), score, grad, stream);
-  if (many && p.num_experts <= 256 && p.top_k <= 8) return launch_choose<T, 8, 32>(p, vec(32), score, grad, stream);
+  auto vec = [&](int v) { return p.group_size % v == 0 && at % std::min<size_t>(16, v * sizeof(T)) == 0; };
+  if (many && need8 <= 8) return launch_choose<T, 8, 8>(p, vec(8), score, grad, stream);
+  if (many && need8 <= 16) return launch_choose<T, 8, 16>(p, vec(16), score, grad, stream);
+  if (many && need8 <= 32) return launch_choose<T, 8, 32>(p, vec(32), score, grad, stream);
   if (need <= 2) return launch_choose<T, 32, 2>(p, vec(2), score, grad, stream);
   if (need <= 4) return launch_choose<T, 32, 4>(p, vec(4), score, grad, stream);
   if (need <= 8) return launch_choose<T, 32, 8>(p, vec(8), score, grad, stream);

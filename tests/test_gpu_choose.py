@@ -102,6 +102,36 @@ def test_with_a_bias(handles, E, top_k, scoring, dtype):
         _check(handles(E), _logits(rng, 9, E, dtype), top_k, bias=bias, scoring=scoring, renormalise=renormalise)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top_groups,top_k", [(64, 1, 1, 8), (30, 1, 1, 3), (100, 1, 1, 8), (256, 8, 4, 8), (120, 3, 2, 6),
+                                                       (160, 8, 3, 8), (256, 1, 1, 8), (48, 6, 2, 4), (9, 3, 1, 3)])
+def test_many_tokens_with_a_bias_or_groups(handles, E, groups, top_groups, top_k, scoring, dtype):
+    """Several tokens a warp: near keys, ties, masks and NaN of one leave its neighbours alone."""
+    torch = _t()
+    from ragged_matmul_gb300 import binding
+    rng = np.random.default_rng([E, groups])
+    T = 2561
+    x = _logits(rng, T, E, "fp32")
+    x[5::9] = torch.from_numpy(rng.integers(-2, 3, (len(range(5, T, 9)), E)).astype(np.float32)).cuda()      # ties
+    x[6::9] = 1.0 + 2.0 ** -22 * torch.from_numpy(rng.integers(-3, 4, (len(range(6, T, 9)), E)).astype(np.float32)).cuda()
+    x[7::9, 3:] = -float("inf")
+    x[8::18] = -float("inf")
+    x = x.to(_dtype(dtype))
+    bias = (0.05 * rng.standard_normal(E)).astype(np.float32)
+    for b in (None, bias, np.zeros(E)):
+        for group_top in (1, 2):
+            _check(handles(E), x, top_k, bias=b, scoring=scoring, groups=groups, top_groups=top_groups, group_top=group_top)
+    x[40, E - 1] = float("nan")
+    xs = x.double().cpu().numpy()
+    ids, w = _route(handles(E), x, top_k, bias=bias, scoring=scoring, expert_groups=groups, top_groups=top_groups, group_top=2)
+    assert binding.gmm_query_status(handles(E)) == binding.GMM_ERR_BAD_INPUT
+    clean = [t for t in range(30, 50) if t != 40]
+    want_ids, _ = cu.choose(xs[clean], top_k, bias=bias, scoring=scoring, groups=groups, top_groups=top_groups, group_top=2)
+    np.testing.assert_array_equal(ids.cpu().numpy()[clean], want_ids)
+    assert (ids[40] == -1).all() and (w[40] == 0).all()
+
+
 @pytest.mark.parametrize("E", [1500, 1536, 2000, 2048, 4000])
 def test_shared_memory_at_every_number_of_experts(handles, E):
     """The 64-bit keys of a token and the gradient's rows, where fewer warps share a block."""
