@@ -698,14 +698,13 @@ _ROUTE_OPTIONS = {}
 
 def _route_options(scoring, renormalise, scale, groups=1, top_groups=1, group_top=1):
     """gmm_route_options by reference; one structure for each combination of settings."""
-    key = (scoring, groups, top_groups, group_top, renormalise, scale)
-    o = _ROUTE_OPTIONS.get(key)
+    key = (scoring, int(groups), int(top_groups), int(group_top), int(bool(renormalise)), float(scale))   # values, no objects
+    o = _ROUTE_OPTIONS.get(key) if isinstance(scoring, (str, int)) else None
     if o is None:
-        s = SCORINGS.get(scoring, scoring)
+        s = SCORINGS.get(scoring, scoring) if isinstance(scoring, (str, int)) else None
         if s not in (GMM_SCORE_SOFTMAX, GMM_SCORE_SIGMOID):
             raise ValueError(f"unknown scoring {scoring!r}: one of {tuple(SCORINGS)}")
-        o = ctypes.byref(GmmRouteOptions(s, int(groups), int(top_groups), int(group_top), int(bool(renormalise)),
-                                         float(scale)))
+        o = ctypes.byref(GmmRouteOptions(s, *key[1:]))
         if len(_ROUTE_OPTIONS) >= 64:
             _ROUTE_OPTIONS.clear()
         _ROUTE_OPTIONS[key] = o

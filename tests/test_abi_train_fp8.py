@@ -76,6 +76,20 @@ def test_options_are_the_headers():
         binding._route_options("relu", True, 1.0)
 
 
+def test_options_are_kept_by_value():
+    """A setting given as a tensor counts with the value that it has at the call."""
+    import torch
+    scale, groups = torch.tensor(1.5), torch.tensor(4)
+    first = binding._route_options("softmax", True, scale, groups, 2)._obj
+    scale.fill_(2.5)
+    groups.fill_(8)
+    o = binding._route_options("softmax", True, scale, groups, 2)._obj
+    assert (first.scale, first.expert_groups) == (1.5, 4) and (o.scale, o.expert_groups) == (2.5, 8)
+    for scoring in (None, [], 2, 1.0):
+        with pytest.raises(ValueError):
+            binding._route_options(scoring, True, 1.0)
+
+
 def test_reference_of_the_choice():
     """The tests' own reference on an example by hand."""
     import numpy as np
