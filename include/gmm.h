@@ -415,7 +415,8 @@ int gmm_quantize_fp8_cols(gmm_handle_t h, void *q_t, void *t_scales, void *q, fl
  *   a_t, a_t_scales: A, e4m3 [K, pitch] and uint8 [pitch / 128, K], both of
  *   pitch = GMM_FP8_COLS_PITCH(rows, num_groups) and 16-byte aligned (the scales of any);
  *   a_offsets: as gmm_quantize_fp8_cols took them, with the same meaning of bad ones.
- * Requirements: N and K multiples of 16, up to 2^24; num_groups up to 4096.
+ * Requirements: N and K multiples of 16, up to 2^24; num_groups up to 4096; rows below 2^30 + 128
+ * (a pitch holds up to 127 rows more than the last whole block).
  * Without rows (rows == 0) the operands and a_offsets may be NULL and are not read.
  * num_groups == 0 launches nothing.
  * Errors (nothing is launched): GMM_ERR_INVALID_ARG, GMM_ERR_UNSUPPORTED (a size above its limit,

@@ -91,7 +91,7 @@ extern "C" int gmm_weight_grad_fp8(gmm_handle_t h, void *d_b, const void *d_t, c
   if (!h || num_groups < 0 || rows < 0 || N < 16 || N % 16 || K < 16 || K % 16 || !dtype_bytes(dtype) ||
       (accumulate != 0 && accumulate != 1) || (accumulate && dtype != GMM_DTYPE_FP32))
     return GMM_ERR_INVALID_ARG;
-  if (dtype == GMM_DTYPE_FP16 || N > (1 << 24) || K > (1 << 24) || num_groups > gmm::kMaxGroups || rows > (1 << 30))
+  if (dtype == GMM_DTYPE_FP16 || N > (1 << 24) || K > (1 << 24) || num_groups > gmm::kMaxGroups || rows / 128 > (1 << 23))
     return GMM_ERR_UNSUPPORTED;
   if (num_groups == 0) return GMM_OK;
   if (!d_b || !aligned16(d_b)) return GMM_ERR_INVALID_ARG;

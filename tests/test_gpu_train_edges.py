@@ -102,6 +102,28 @@ def test_weight_gradient_past_32_bits():
     binding.gmm_destroy(h)
 
 
+@pytest.mark.slow
+def test_weight_gradient_of_the_longest_pitch():
+    """2^30 rows, the most that gmm_quantize_fp8_cols takes: the last block's columns lie behind 2^33 bytes."""
+    torch = _t()
+    from ragged_matmul_gb300 import binding
+    G, N, K, R, n = 1, 16, 16, 1 << 30, 200
+    h = binding.gmm_create(G, 0)
+    P = fu.pitch(R, G)
+    d, a = (torch.zeros((w, P), dtype=torch.uint8, device="cuda") for w in (N, K))
+    rng = np.random.default_rng(4)
+    codes = [rng.choice([0x38, 0xB8, 0x40], (w, n)).astype(np.uint8) for w in (N, K)]
+    c = (R - n) // 128 * 128
+    for x, q in zip((d, a), codes):
+        x[:, c:c + n] = torch.from_numpy(q).cuda()
+    ones = lambda w: torch.full((P // 128, w), 127, dtype=torch.uint8, device="cuda")  # noqa: E731
+    out = torch.full((G, N, K), float("nan"), device="cuda")
+    binding.gmm_weight_grad_fp8(h, out, d, ones(N), a, ones(K), torch.tensor([R - n, R], dtype=torch.int32, device="cuda"))
+    assert binding.gmm_query_status(h) == binding.GMM_OK
+    np.testing.assert_array_equal(out[0].double().cpu().numpy(), fu.E4M3[codes[0]] @ fu.E4M3[codes[1]].T)
+    binding.gmm_destroy(h)
+
+
 def _calls(h, E):
     """Each call on inputs of its own: (name, call, result)."""
     torch = _t()
