@@ -299,24 +299,24 @@ __device__ __forceinline__ double score64(int scoring, float x, float top, doubl
   return scoring == kScoreSoftmax ? exp(static_cast<double>(x) - static_cast<double>(top)) / zd : sigmoid64(static_cast<double>(x));
 }
 
-// Softmax's sum in 64 bits, by a whole warp.
-template <class T>
+// Softmax's sum in 64 bits, by the L lanes of a token (every lane of the warp takes part).
+template <class T, int L>
 __device__ __noinline__ double choose_sum64(const T *row, int E, float top) {
   double zd = 0.0;
 #pragma unroll 4
-  for (int e = static_cast<int>(threadIdx.x & 31u); e < E; e += 32)   // several at a time: an exponential is one long chain
+  for (int e = static_cast<int>(threadIdx.x & (L - 1)); e < E; e += L)   // several at a time: an exponential is one long chain
     zd += exp(static_cast<double>(choose_float<T>(row[e])) - static_cast<double>(top));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) zd += __shfl_xor_sync(0xffffffffu, zd, o);
+  for (int o = L / 2; o > 0; o >>= 1) zd += __shfl_xor_sync(0xffffffffu, zd, o);
   return zd;
 }
 
-// The key of this lane's group in 64 bits, by a whole warp: the sum of its two largest keys (or the one).
-// Only experts whose fp32 key reaches `least` of their group are computed.
-template <class T>
+// The key of this lane's group in 64 bits (every lane of the warp takes part): the sum of its two largest
+// keys (or the one).  Only experts whose fp32 key reaches `least` of their group are computed.
+template <class T, int L>
 __device__ __noinline__ double choose_group64(const ChooseParams &p, const T *row, int base, int size, int lane, float top, float z,
                                               float least) {
-  const double zd = p.scoring == kScoreSoftmax ? choose_sum64<T>(row, p.num_experts, top) : 0.0;
+  const double zd = p.scoring == kScoreSoftmax ? choose_sum64<T, L>(row, p.num_experts, top) : 0.0;
   double m1 = -INFINITY, m2 = -INFINITY;
   for (int i = lane; i < size; i += p.group_lanes) {
     const float x = choose_float<T>(row[base + i]), b = __ldg(p.bias + base + i);
@@ -335,15 +335,16 @@ __device__ __noinline__ double choose_group64(const ChooseParams &p, const T *ro
   return p.group_top == 2 && m2 > -static_cast<double>(INFINITY) ? m1 + m2 : m1;
 }
 
-// The choice of one token by 64-bit keys in shared memory, by a whole warp: ids[j] for lane j < top_k.  Only the
-// experts whose fp32 key reaches `least` are looked at; `kept`: bit g, group g is kept.
-template <class T>
+// The choice of a token by 64-bit keys in shared memory, by its L lanes (every lane of the warp takes part):
+// ids[j] for lane j < top_k.  Only the experts whose fp32 key reaches `least` are looked at; `kept`: bit g,
+// group g is kept.
+template <class T, int L>
 __device__ __noinline__ int choose_exact(const ChooseParams &p, const T *row, float top, float z, float least, uint32_t kept,
                                          unsigned long long *keys) {
-  const int lane = static_cast<int>(threadIdx.x & 31u), E = p.num_experts;
-  const double zd = p.scoring == kScoreSoftmax ? choose_sum64<T>(row, E, top) : 0.0;
+  const int sub = static_cast<int>(threadIdx.x & (L - 1)), E = p.num_experts;
+  const double zd = p.scoring == kScoreSoftmax ? choose_sum64<T, L>(row, E, top) : 0.0;
 #pragma unroll 4
-  for (int e = lane; e < E; e += 32) {
+  for (int e = sub; e < E; e += L) {
     const float x = choose_float<T>(row[e]), b = __ldg(p.bias + e);
     const float s = p.scoring == kScoreSoftmax ? expf(x - top) / z : sigmoid32(x);
     keys[e] = x > -INFINITY && s + b >= least && ((kept >> (e / p.group_size)) & 1u)
@@ -355,13 +356,13 @@ __device__ __noinline__ int choose_exact(const ChooseParams &p, const T *row, fl
   for (int j = 0; j < p.top_k; ++j) {
     unsigned long long m = 0ull;
     int at = E;
-    for (int e = lane; e < E; e += 32)
+    for (int e = sub; e < E; e += L)
       if (keys[e] > m) {
         m = keys[e];
         at = e;
       }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = L / 2; o > 0; o >>= 1) {
       const unsigned long long mo = __shfl_xor_sync(0xffffffffu, m, o);
       const int ao = __shfl_xor_sync(0xffffffffu, at, o);
       if (mo > m || (mo == m && ao < at)) {
@@ -369,24 +370,27 @@ __device__ __noinline__ int choose_exact(const ChooseParams &p, const T *row, fl
         at = ao;
       }
     }
-    if (m == 0ull) break;
-    if (lane == j) id = at;
-    if (lane == (at & 31)) keys[at] = 0ull;
+    if (m != 0ull) {
+      if (sub == j) id = at;
+      if (sub == (at & (L - 1))) keys[at] = 0ull;
+    }
     __syncwarp();
   }
-  __syncwarp();
   return id;
 }
 
-// One token per L lanes, 32 / L tokens a warp.  kScore: a bias, the keys are not the logits themselves; then L = 32,
-// as one token of a warp whose keys are too near keeps the others waiting (32768 tokens of 256 experts, fp32, with
-// a bias: 36 us with 32 lanes, 70 with 8; bf16 in 8 groups without one: 27.4 with 32, 14.1 with 8).
+// One token per L lanes, 32 / L tokens a warp.  kScore: a bias, the keys are not the logits themselves.  A whole
+// warp has the shortest way through a token, eight lanes leave fewer of them idle; with a bias up to 16 experts
+// a lane, as a lane works through them one after the other (32768 tokens with a bias, 32 lanes and 8: of 64
+// experts fp32 20.6 and 12.4 us, of 64 in 8 groups 26.6 and 15.2, of 128 bf16 24.3 and 18.6, of 256 fp32 in 8
+// groups 43.6 and 59.6; of 256 bf16 in 8 groups without one 27.4 and 14.1).
 template <class T, int L, int V, bool kVec, bool kScore>
-__global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (V <= 32 ? 4 : 1)) gmm_route_kernel(const __grid_constant__ ChooseParams p) {
-  static_assert(!kScore || L == 32, "a score's token has a whole warp");
+__global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (L == 8 && V <= 16 ? 6 : (V <= 32 ? 4 : 1))) gmm_route_kernel(const __grid_constant__ ChooseParams p) {
   constexpr bool kPacked = !kScore && sizeof(T) == 2;
+  constexpr bool kKeep = kScore && L == 32;   // logits and biases stay in registers, else they are read again
   extern __shared__ unsigned long long choose_smem[];
-  __shared__ uint4 choose_slots[kPacked ? 1 : 32 * kChooseWarps];   // gathered keys: key, expert, logit, bias
+  constexpr int kSlots = kScore && L < 32 ? 2 * L : L;   // of a token's gathered keys: key, expert, logit, bias
+  __shared__ uint4 choose_slots[kPacked ? 1 : 32 / L * kSlots * kChooseWarps];
   const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
   const int sub = lane & (L - 1), seg = lane & ~(L - 1);
   const uint32_t seg_mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << seg;
@@ -419,7 +423,6 @@ __global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (V <= 32 ? 4 :
       for (int v = 0; v < V; ++v) bias[v] = at.there(v) ? __ldg(p.bias + at.expert(v)) : 0.0f;
     }
   }
-
   // NaN (and, for softmax, +infinity) anywhere: no expert at all.  Of packed keys the largest one tells.
   bool bad = false;
   if constexpr (kPacked) {
@@ -526,11 +529,11 @@ __global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (V <= 32 ? 4 :
       // Without a bias relative: 1e-6, and of softmax's exponentials half a step of their argument.
       const float tol = kScore ? 2.0f * (score_tol + 2.4e-7f * of) : a * (1e-6f + 1.3e-7f * of);
       const bool near = out != 0u && !(a - b > tol) && !bad;
-      if (__any_sync(0xffffffffu, near)) {   // every lane takes part: the tokens beside this one too
+      if (__any_sync(0xffffffffu, near)) {
         double gd;
         if constexpr (kScore) {
           const float g = pair ? g2 : g1;
-          gd = choose_group64<T>(p, row, base, size, part, top, z,
+          gd = choose_group64<T, L>(p, row, base, size, part, top, z,
                                  fabsf(g) < INFINITY ? g - 2.0f * (score_tol + 2.4e-7f * fabsf(g)) : -INFINITY);
         } else {
           gd = score64(p.scoring, g1, top, 1.0) + score64(p.scoring, g2, top, 1.0);
@@ -549,6 +552,18 @@ __global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (V <= 32 ? 4 :
 #pragma unroll
       for (int v = 0; v < V; ++v) key[v] = 0u;
   }
+
+  // An expert's logit and bias, once its key is made.
+  auto logit_of = [&](int v) {
+    if constexpr (kKeep) return x[v];
+    else if constexpr (kScore) return choose_float<T>(row[at.expert(v)]);
+    else return key_value(key[v]);
+  };
+  auto bias_of = [&](int v) {
+    if constexpr (kKeep) return bias[v];
+    else if constexpr (kScore) return __ldg(p.bias + at.expert(v));
+    else return 0.0f;
+  };
 
   // The chosen experts: lane j keeps the j-th one's number and logit.
   int id = -1;
@@ -592,8 +607,8 @@ __global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (V <= 32 ? 4 :
         if (least != 0u && l < INFINITY) least = order_key(l - 2.0f * (score_tol + 2.4e-7f * fabsf(l)));
       }
       least = max(least, 1u);
-      // They are gathered, a lane each, and ranked against one another.
-      uint4 *slots = choose_slots + warp * 32 + seg;
+      // They are gathered, a lane each (or two), and ranked against one another.
+      uint4 *slots = choose_slots + (warp * 32 + seg) * (kSlots / L);
       int count = 0;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -601,18 +616,22 @@ __global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (V <= 32 ? 4 :
         const uint32_t hits = __ballot_sync(0xffffffffu, hit) & seg_mask;
         if (hit) {
           const int to = count + __popc(hits & ((1u << lane) - 1u));
-          if (to < L)
-            slots[to] = make_uint4(key[v], static_cast<uint32_t>(at.expert(v)), __float_as_uint(kScore ? x[v] : key_value(key[v])),
-                                   kScore ? __float_as_uint(bias[v]) : 0u);
+          if (to < kSlots)
+            slots[to] = make_uint4(key[v], static_cast<uint32_t>(at.expert(v)),
+                                   kScore && !kKeep ? 0u : __float_as_uint(logit_of(v)), kKeep ? __float_as_uint(bias_of(v)) : 0u);
         }
         count += __popc(hits);
       }
       __syncwarp();
-      done = __all_sync(0xffffffffu, count <= L);
-      if (done) {
-        const int most = L == 32 ? count : static_cast<int>(redux_max(static_cast<uint32_t>(count)));
+      const int most = L == 32 ? count : static_cast<int>(redux_max(static_cast<uint32_t>(count)));
+      done = most <= kSlots;
+      if (most <= L) {
         const bool have = sub < count;
         uint4 f = have ? slots[sub] : make_uint4(0u, 0xffffffffu, 0u, 0u);
+        if (kScore && !kKeep && have) {
+          f.z = __float_as_uint(choose_float<T>(row[f.y]));
+          f.w = __float_as_uint(__ldg(p.bias + f.y));
+        }
         int rank = 0;
         for (int i = 0; i < most; ++i) {
           const uint32_t ko = __shfl_sync(0xffffffffu, f.x, seg + i), eo = __shfl_sync(0xffffffffu, f.y, seg + i);
@@ -629,14 +648,14 @@ __global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (V <= 32 ? 4 :
           const uint32_t xo = __shfl_down_sync(0xffffffffu, f.z, 1), bo = __shfl_down_sync(0xffffffffu, f.w, 1);
           const bool near = sub + 1 < count && !(v - vo > score_tol + 2.4e-7f * fmaxf(fabsf(v), fabsf(vo))) &&
                             !(__uint_as_float(xo) == __uint_as_float(f.z) && __uint_as_float(bo) == __uint_as_float(f.w));
-          if (__any_sync(0xffffffffu, near) && !bad) {
-            const double zd = softmax ? choose_sum64<T>(row, p.num_experts, top) : 0.0;
+          if (__any_sync(0xffffffffu, near && !bad)) {
+            const double zd = softmax ? choose_sum64<T, L>(row, p.num_experts, top) : 0.0;
             const unsigned long long k =
                 have ? order_key(score64(p.scoring, __uint_as_float(f.z), top, zd) + static_cast<double>(__uint_as_float(f.w))) : 0ull;
             rank = 0;
             for (int i = 0; i < most; ++i) {
-              const unsigned long long o = __shfl_sync(0xffffffffu, k, i);
-              const uint32_t eo = __shfl_sync(0xffffffffu, f.y, i);
+              const unsigned long long o = __shfl_sync(0xffffffffu, k, seg + i);
+              const uint32_t eo = __shfl_sync(0xffffffffu, f.y, seg + i);
               rank += o > k || (o == k && eo < f.y) ? 1 : 0;
             }
             __syncwarp();
@@ -648,6 +667,63 @@ __global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (V <= 32 ? 4 :
         if (have && sub < p.top_k) {
           id = static_cast<int>(f.y);
           xj = __uint_as_float(f.z);
+        }
+      } else if constexpr (kSlots > L) {
+        if (done) {   // two keys a lane, as above
+          uint4 f[2];
+          unsigned long long k[2];
+          int rank[2];
+          auto have = [&](int h) { return sub + h * L < count; };
+          auto sort = [&]() {   // by (k, expert)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              rank[h] = 0;
+              for (int i = 0; i < most; ++i) {
+                const unsigned long long ko = __shfl_sync(0xffffffffu, i < L ? k[0] : k[1], seg + (i & (L - 1)));
+                const uint32_t eo = __shfl_sync(0xffffffffu, i < L ? f[0].y : f[1].y, seg + (i & (L - 1)));
+                rank[h] += ko > k[h] || (ko == k[h] && eo < f[h].y) ? 1 : 0;
+              }
+            }
+            __syncwarp();   // the slots are read
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (have(h)) slots[rank[h]] = f[h];
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (have(h)) f[h] = slots[sub + h * L];
+          };
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            f[h] = have(h) ? slots[sub + h * L] : make_uint4(0u, 0xffffffffu, 0u, 0u);
+            if (have(h)) {
+              f[h].z = __float_as_uint(choose_float<T>(row[f[h].y]));
+              f[h].w = __float_as_uint(__ldg(p.bias + f[h].y));
+            }
+            k[h] = f[h].x;
+          }
+          sort();
+          bool near = false;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (sub + h * L + 1 < count) {
+              const uint4 o = slots[sub + h * L + 1];
+              const float v = key_value(f[h].x), vo = key_value(o.x);
+              near |= !(v - vo > score_tol + 2.4e-7f * fmaxf(fabsf(v), fabsf(vo))) &&
+                      !(__uint_as_float(o.z) == __uint_as_float(f[h].z) && __uint_as_float(o.w) == __uint_as_float(f[h].w));
+            }
+          if (__any_sync(0xffffffffu, near && !bad)) {
+            const double zd = softmax ? choose_sum64<T, L>(row, p.num_experts, top) : 0.0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              k[h] = have(h) ? order_key(score64(p.scoring, __uint_as_float(f[h].z), top, zd) + static_cast<double>(__uint_as_float(f[h].w)))
+                             : 0ull;
+            sort();
+          }
+          if (have(0) && sub < p.top_k) {
+            id = static_cast<int>(f[0].y);
+            xj = __uint_as_float(f[0].z);
+          }
         }
       }
     }
@@ -685,7 +761,7 @@ __global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (V <= 32 ? 4 :
       if (kPacked && taken == 0) bad |= (M >> 16) > Packed16<T>::kPlusInf - (softmax ? 1u : 0u);
       if (sub == taken && M != 0u) id = e;
       if (__all_sync(0xffffffffu, M == 0u)) break;
-      if constexpr (kScore) {
+      if (kScore && M != 0u) {
         const float k = key_value(M), xe = choose_float<T>(row[e]), be = __ldg(p.bias + e);
         if (taken > 0 && !(prev_key - k > score_tol + 2.4e-7f * fabsf(prev_key)) && !(prev_x == xe && prev_b == be)) unsure = true;
         prev_key = k;
@@ -695,20 +771,20 @@ __global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (V <= 32 ? 4 :
       }
     }
     if constexpr (kScore) {
-      const bool full = taken == p.top_k;
+      const bool full = (__ballot_sync(0xffffffffu, sub == p.top_k - 1 && id >= 0) & seg_mask) != 0u;   // every slot is filled
       const float tol = score_tol + 2.4e-7f * fabsf(kth);
-      if (full) {   // is one of those left as near to the last one?
-        bool near = false;
+      bool near = false;   // is one of those left as near to the last one?
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (key[v] != 0u && !(kth - key_value(key[v]) > tol)) near |= !(x[v] == prev_x && bias[v] == prev_b);
-        unsure |= __any_sync(0xffffffffu, near);
-      }
-      if (unsure && !bad) {
+      for (int v = 0; v < V; ++v)
+        if (full && key[v] != 0u && !(kth - key_value(key[v]) > tol)) near |= !(logit_of(v) == prev_x && bias_of(v) == prev_b);
+      const uint32_t nears = __ballot_sync(0xffffffffu, near) & seg_mask;   // by every lane, sure or not
+      unsure = (unsure || nears != 0u) && !bad;
+      if (__any_sync(0xffffffffu, unsure)) {
         uint32_t kept = 0u;
-        for (int g = 0; g < p.groups; ++g) kept |= (kept_lanes >> (g * p.group_lanes) & 1u) << g;
-        id = choose_exact<T>(p, row, top, z, full && kth < INFINITY ? kth - 2.0f * tol : -INFINITY, kept,
-                             choose_smem + static_cast<size_t>(warp) * p.num_experts);
+        for (int g = 0; g < p.groups; ++g) kept |= (kept_lanes >> (seg + g * p.group_lanes) & 1u) << g;
+        const int exact = choose_exact<T, L>(p, row, top, z, full && kth < INFINITY ? kth - 2.0f * tol : -INFINITY, kept,
+                                             choose_smem + static_cast<size_t>(warp * (32 / L) + lane / L) * p.num_experts);
+        if (unsure) id = exact;
       }
     }
     if (id >= 0) xj = choose_float<T>(row[id]);

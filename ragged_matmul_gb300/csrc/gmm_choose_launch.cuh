@@ -15,12 +15,15 @@ inline int choose_warps(size_t smem) {
   return static_cast<int>(std::max<size_t>(1, std::min<size_t>(gmm::kChooseWarps, 46 * 1024 / std::max<size_t>(1, smem))));
 }
 
+// The largest share of a token's experts that one of eight lanes takes where there is a bias.
+constexpr int kScoreShare8 = 16;
+
 template <class T, int L, int V>
 int launch_choose(gmm::ChooseParams p, bool vec, bool score, bool grad, cudaStream_t stream) {
   for (p.group_lanes = L; p.group_lanes > 1 && p.group_lanes * p.groups > L;) p.group_lanes /= 2;
   const long long warps = (p.num_tokens + 32 / L - 1) / (32 / L);
   const bool dense = p.scoring == GMM_SCORE_SOFTMAX && !p.renormalise;
-  const size_t per_warp = grad ? static_cast<size_t>(32) * V * 4 : (score ? static_cast<size_t>(p.num_experts) * 8 : 0);
+  const size_t per_warp = grad ? static_cast<size_t>(32) * V * 4 : (score ? static_cast<size_t>(32 / L) * p.num_experts * 8 : 0);
   const int wc = choose_warps(per_warp);
   const unsigned grid = static_cast<unsigned>((warps + wc - 1) / wc), threads = 32u * wc;
   const size_t smem = per_warp * wc;
@@ -29,7 +32,7 @@ int launch_choose(gmm::ChooseParams p, bool vec, bool score, bool grad, cudaStre
     if (grad) {
       if (dense) gmm::gmm_route_grad_kernel<T, L, V, kVec, true><<<grid, threads, smem, stream>>>(p);
       else gmm::gmm_route_grad_kernel<T, L, V, kVec, false><<<grid, threads, smem, stream>>>(p);
-    } else if constexpr (L == 32) {
+    } else if constexpr (L == 32 || V <= kScoreShare8) {
       if (score) gmm::gmm_route_kernel<T, L, V, kVec, true><<<grid, threads, smem, stream>>>(p);
       else gmm::gmm_route_kernel<T, L, V, kVec, false><<<grid, threads, smem, stream>>>(p);
     } else {
@@ -54,15 +57,15 @@ inline int choose_share(const gmm::ChooseParams &p, int lanes) {
 template <class T>
 int run_choose(gmm_ctx *h, const gmm::ChooseParams &p, bool score, bool grad, cudaStream_t stream) {
   // Lanes a token: a whole warp has the shortest way through one token; with many tokens eight
-  // lanes leave fewer of them idle.  With a bias always a whole warp.
-  const bool many = !score && p.num_tokens > 16 * h->num_sms && p.top_k <= 8;
+  // lanes leave fewer of them idle.
+  const bool many = p.num_tokens > 16 * h->num_sms && p.top_k <= 8;
   const int need8 = choose_share(p, 8), need = choose_share(p, 32);
   const unsigned long long at = reinterpret_cast<uintptr_t>(p.logits) | static_cast<unsigned long long>(p.logits_pitch) |
                                 reinterpret_cast<uintptr_t>(p.d_logits) | static_cast<unsigned long long>(p.d_pitch);
   auto vec = [&](int v) { return p.group_size % v == 0 && at % std::min<size_t>(16, v * sizeof(T)) == 0; };
   if (many && need8 <= 8) return launch_choose<T, 8, 8>(p, vec(8), score, grad, stream);
   if (many && need8 <= 16) return launch_choose<T, 8, 16>(p, vec(16), score, grad, stream);
-  if (many && need8 <= 32) return launch_choose<T, 8, 32>(p, vec(32), score, grad, stream);
+  if (many && need8 <= 32 && !score) return launch_choose<T, 8, 32>(p, vec(32), score, grad, stream);
   if (need <= 2) return launch_choose<T, 32, 2>(p, vec(2), score, grad, stream);
   if (need <= 4) return launch_choose<T, 32, 4>(p, vec(4), score, grad, stream);
   if (need <= 8) return launch_choose<T, 32, 8>(p, vec(8), score, grad, stream);

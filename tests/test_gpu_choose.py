@@ -132,6 +132,21 @@ def test_many_tokens_with_a_bias_or_groups(handles, E, groups, top_groups, top_k
     assert (ids[40] == -1).all() and (w[40] == 0).all()
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top_groups,top_k", [(64, 1, 1, 8), (100, 1, 1, 5), (128, 1, 1, 8), (40, 8, 5, 8)])
+def test_many_tokens_with_a_few_near_keys(handles, E, groups, top_groups, top_k, scoring):
+    """Some keys more than a token's lanes, of which 32 bits do not tell all apart."""
+    rng = np.random.default_rng([E, 5])
+    T = 2561
+    x = -3.0 + 0.1 * rng.standard_normal((T, E))
+    for t in range(T):
+        near = rng.permutation(E)[:rng.integers(top_k, 24)]
+        x[t, near] = 1.0 + 2.0 ** -22 * rng.integers(-3, 4, len(near))
+    x = _t().from_numpy(x.astype(np.float32)).cuda()
+    for bias in (np.zeros(E), 2.0 ** -26 * rng.integers(-3, 4, E)):
+        _check(handles(E), x, top_k, bias=bias.astype(np.float32), scoring=scoring, groups=groups, top_groups=top_groups, group_top=2)
+
+
 @pytest.mark.parametrize("E", [1500, 1536, 2000, 2048, 4000])
 def test_shared_memory_at_every_number_of_experts(handles, E):
     """The 64-bit keys of a token and the gradient's rows, where fewer warps share a block."""
