@@ -24,4 +24,16 @@ __device__ __forceinline__ __half route_from_float(float x) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 route_from_float(float x) { return __float2bfloat16_rn(x); }
 
+// Division by a number that the host knows: for n < 2^31 and m = floor(2^(31 + l) / d) + 1 with 2^l >= d,
+// n / d = n * m >> (31 + l).  d = 1 has mul = 0.
+struct Divisor {
+  uint32_t d, mul, shift;
+  __host__ static Divisor of(uint32_t d) {
+    uint32_t l = 0;
+    while ((1ull << l) < d) ++l;
+    return d == 1 ? Divisor{1, 0, 0} : Divisor{d, static_cast<uint32_t>((1ull << (31 + l)) / d + 1), l - 1};
+  }
+  __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return mul == 0u ? n : __umulhi(n, mul) >> shift; }
+};
+
 }  // namespace gmm

@@ -51,7 +51,8 @@ int check_quant8(gmm_ctx *h, Quant8Params &p, const void *x, long long x_stride,
   p.src_rows = src_rows;
   p.width = width;
   p.blocks = (width + gmm::kQ8Block - 1) / gmm::kQ8Block;
-  p.top_k = top_k;
+  p.by_blocks = gmm::Divisor::of(static_cast<uint32_t>(p.blocks));
+  p.by_top_k = gmm::Divisor::of(static_cast<uint32_t>(top_k));
   p.status = reinterpret_cast<uint32_t *>(h->ws);
   return GMM_OK;
 }
@@ -70,13 +71,8 @@ int gmm_quantize_fp8(gmm_handle_t h, void *q, float *scales, const void *x, long
   if (!q || !scales || !aligned16(q) || !aligned_to(scales, 4)) return GMM_ERR_INVALID_ARG;
   p.q = static_cast<uint8_t *>(q);
   p.scales = scales;
-  // Units (a row's block) are numbered in 31 bits: unit / blocks is a multiply and a shift for
-  // unit < 2^31 and mul = floor(2^(31 + l) / blocks) + 1 with 2^l >= blocks.  Longer calls go in slabs.
-  unsigned l = 0;
-  while ((1u << l) < static_cast<unsigned>(p.blocks)) ++l;
-  p.div_shift = 31 + l;
-  p.div_mul = (1ull << p.div_shift) / static_cast<unsigned>(p.blocks) + 1;
-  constexpr int kUnits = gmm::kQ8Threads / gmm::kQ8Lanes * gmm::kQ8Per;   // of a CTA
+  // Units (a row's block) are numbered in 31 bits; longer calls go in slabs.
+  constexpr int kUnits = gmm::kQ8Threads / gmm::kQ8RowLanes;   // of a CTA
   const int slab = static_cast<int>(((1ll << 31) - kUnits) / p.blocks);
   const int align = alignment(x, p.x_pitch);
   DeviceGuard guard(h->device);

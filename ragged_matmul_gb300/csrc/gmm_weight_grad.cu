@@ -127,10 +127,10 @@ extern "C" int gmm_weight_grad_fp8(gmm_handle_t h, void *d_b, const void *d_t, c
   if (p.num_stages < v.min_stages) return GMM_ERR_UNSUPPORTED;   // the offsets leave no room for the ring
   // As many n tiles a band as make the tiles that run side by side about as deep as they are wide.
   const uint32_t band = std::min(8u, p.n_tiles);
-  p.band = gmm::WgDivisor::of(band);
-  p.rest = gmm::WgDivisor::of(std::max(1u, p.n_tiles % band));
-  p.whole = gmm::WgDivisor::of(band * p.k_tiles);
-  p.per_group = gmm::WgDivisor::of(p.k_tiles * p.n_tiles);
+  p.band = gmm::Divisor::of(band);
+  p.rest = gmm::Divisor::of(std::max(1u, p.n_tiles % band));
+  p.whole = gmm::Divisor::of(band * p.k_tiles);
+  p.per_group = gmm::Divisor::of(p.k_tiles * p.n_tiles);
   p.d_scales = static_cast<const uint8_t *>(d_t_scales);
   p.a_scales = static_cast<const uint8_t *>(a_t_scales);
   p.a_offsets = rows > 0 ? a_offsets : nullptr;

@@ -37,6 +37,7 @@
 
 #include <type_traits>
 
+#include "gmm_common.cuh"
 #include "gmm_kernel.cuh"
 
 namespace gmm {
@@ -66,18 +67,6 @@ constexpr size_t kWgFixedBytes = 1024 + kWgEntries * kWgEntryBytes;   // and the
 static_assert(kWgScaleCol + 12 <= kTmemCols, "scales beside the accumulators");
 static_assert(kWgABytes % 1024 == 0 && kWgBBytes % 1024 == 0 && kWgStgBytes<true> % 1024 == 0, "swizzled tiles start at 1024 bytes");
 
-// Division by a number that the host knows: for n < 2^31 and m = floor(2^(31 + l) / d) + 1 with 2^l >= d,
-// n / d = n * m >> (31 + l).  d = 1 has mul = 0.
-struct WgDivisor {
-  uint32_t d, mul, shift;
-  __host__ static WgDivisor of(uint32_t d) {
-    uint32_t l = 0;
-    while ((1ull << l) < d) ++l;
-    return d == 1 ? WgDivisor{1, 0, 0} : WgDivisor{d, static_cast<uint32_t>((1ull << (31 + l)) / d + 1), l - 1};
-  }
-  __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return mul == 0u ? n : __umulhi(n, mul) >> shift; }
-};
-
 struct alignas(128) WeightGradParams {
   CUtensorMap d_map;        // codes of dc {pitch, N}, box {128, 128}, 128-byte swizzle
   CUtensorMap a_map[2];     // codes of a {pitch, K}, box {128, half of a narrow / wide tile}
@@ -98,10 +87,10 @@ struct alignas(128) WeightGradParams {
   uint32_t wide;
   uint32_t width;
   uint32_t n_tiles;
-  WgDivisor band;           // n tiles per band of the tile order (the last band has n_tiles % band, `rest`)
-  WgDivisor rest;
-  WgDivisor whole;          // tiles of a whole band: band * k_tiles
-  WgDivisor per_group;      // n_tiles * k_tiles
+  Divisor band;           // n tiles per band of the tile order (the last band has n_tiles % band, `rest`)
+  Divisor rest;
+  Divisor whole;          // tiles of a whole band: band * k_tiles
+  Divisor per_group;      // n_tiles * k_tiles
   uint32_t total;           // tiles
   unsigned long long wait_limit_ns;
 };
