@@ -698,10 +698,14 @@ _ROUTE_OPTIONS = {}
 
 def _route_options(scoring, renormalise, scale, groups=1, top_groups=1, group_top=1):
     """gmm_route_options by reference; one structure for each combination of settings."""
-    key = (scoring, int(groups), int(top_groups), int(group_top), int(bool(renormalise)), float(scale))   # values, no objects
-    o = _ROUTE_OPTIONS.get(key) if isinstance(scoring, (str, int)) else None
+    key = (scoring, groups, top_groups, group_top, renormalise, scale)
+    if not (type(scale) is float and type(renormalise) is bool and type(group_top) is int and type(top_groups) is int
+            and type(groups) is int and type(scoring) is str):     # kept by value, whatever holds it
+        key = (scoring if isinstance(scoring, (str, int)) else None, int(groups), int(top_groups), int(group_top),
+               bool(renormalise), float(scale))
+    o = _ROUTE_OPTIONS.get(key)
     if o is None:
-        s = SCORINGS.get(scoring, scoring) if isinstance(scoring, (str, int)) else None
+        s = SCORINGS.get(key[0], key[0])
         if s not in (GMM_SCORE_SOFTMAX, GMM_SCORE_SIGMOID):
             raise ValueError(f"unknown scoring {scoring!r}: one of {tuple(SCORINGS)}")
         o = ctypes.byref(GmmRouteOptions(s, *key[1:]))
