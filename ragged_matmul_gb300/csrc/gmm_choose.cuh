@@ -299,6 +299,21 @@ __device__ __forceinline__ double score64(int scoring, float x, float top, doubl
   return scoring == kScoreSoftmax ? exp(static_cast<double>(x) - static_cast<double>(top)) / zd : sigmoid64(static_cast<double>(x));
 }
 
+// Whether the key of (xi, bi) is surely above that of (xj, bj), by their difference: s_i - s_j is s of the larger
+// logit times 1 - exp(-d) (sigmoid: times sigmoid of the smaller one's negative too), d the logits' distance, whose
+// error is relative to the difference and not to the scores.  Softmax: z is off by 3e-7 and V + 5 half steps
+// relative, an exponential by 2.4e-7 and a half step of its argument, the rest by six half steps.  `y`: the keys'
+// magnitude; what 64 bits do not tell apart is not told apart here.  (1685 tokens of
+// 98 fp16, softmax, with a bias: 10.1 -> 3.7 us; near keys went to 64 bits, at a few operations a clock.)
+template <int V>
+__device__ __forceinline__ bool surely_above(int scoring, float xi, float bi, float xj, float bj, float top, float z, float y) {
+  const float hi = fmaxf(xi, xj), lo = fminf(xi, xj), e = -expm1f(lo - hi);
+  const float s = scoring == kScoreSoftmax ? expf(hi - top) / z * e : sigmoid32(hi) * sigmoid32(-lo) * e;
+  const float rel = scoring == kScoreSoftmax ? 1.2e-7f * (V + 30 + (top - hi)) : 2e-6f;
+  const float bd = bi - bj, d = (xi >= xj ? s : -s) + bd;
+  return d > rel * s + 1.2e-7f * fabsf(bd) + 1e-15f * y + 1e-37f;
+}
+
 // Softmax's sum in 64 bits, by the L lanes of a token (every lane of the warp takes part).
 template <class T, int L>
 __device__ __noinline__ double choose_sum64(const T *row, int E, float top) {
@@ -382,8 +397,8 @@ __device__ __noinline__ int choose_exact(const ChooseParams &p, const T *row, fl
 // One token per L lanes, 32 / L tokens a warp.  kScore: a bias, the keys are not the logits themselves.  A whole
 // warp has the shortest way through a token, eight lanes leave fewer of them idle; with a bias up to 16 experts
 // a lane, as a lane works through them one after the other (32768 tokens with a bias, 32 lanes and 8: of 64
-// experts fp32 20.6 and 12.4 us, of 64 in 8 groups 26.6 and 15.2, of 128 bf16 24.3 and 18.6, of 256 fp32 in 8
-// groups 43.6 and 59.6; of 256 bf16 in 8 groups without one 27.4 and 14.1).
+// experts fp32 20.6 and 11.2 us, of 64 in 8 groups 26.6 and 14.8, of 128 bf16 24.3 and 16.2, of 256 fp32 in 8
+// groups 43.2 and 59.6; of 256 bf16 in 8 groups without one 27.4 and 14.1).
 template <class T, int L, int V, bool kVec, bool kScore>
 __global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (L == 8 && V <= 16 ? 6 : (V <= 32 ? 4 : 1))) gmm_route_kernel(const __grid_constant__ ChooseParams p) {
   constexpr bool kPacked = !kScore && sizeof(T) == 2;
@@ -647,7 +662,9 @@ __global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (L == 8 && V <
           const float v = key_value(f.x), vo = key_value(__shfl_down_sync(0xffffffffu, f.x, 1));
           const uint32_t xo = __shfl_down_sync(0xffffffffu, f.z, 1), bo = __shfl_down_sync(0xffffffffu, f.w, 1);
           const bool near = sub + 1 < count && !(v - vo > score_tol + 2.4e-7f * fmaxf(fabsf(v), fabsf(vo))) &&
-                            !(__uint_as_float(xo) == __uint_as_float(f.z) && __uint_as_float(bo) == __uint_as_float(f.w));
+                            !(__uint_as_float(xo) == __uint_as_float(f.z) && __uint_as_float(bo) == __uint_as_float(f.w)) &&
+                            !surely_above<V>(p.scoring, __uint_as_float(f.z), __uint_as_float(f.w), __uint_as_float(xo),
+                                             __uint_as_float(bo), top, z, fabsf(v));
           if (__any_sync(0xffffffffu, near && !bad)) {
             const double zd = softmax ? choose_sum64<T, L>(row, p.num_experts, top) : 0.0;
             const unsigned long long k =
@@ -710,7 +727,9 @@ __global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (L == 8 && V <
               const uint4 o = slots[sub + h * L + 1];
               const float v = key_value(f[h].x), vo = key_value(o.x);
               near |= !(v - vo > score_tol + 2.4e-7f * fmaxf(fabsf(v), fabsf(vo))) &&
-                      !(__uint_as_float(o.z) == __uint_as_float(f[h].z) && __uint_as_float(o.w) == __uint_as_float(f[h].w));
+                      !(__uint_as_float(o.z) == __uint_as_float(f[h].z) && __uint_as_float(o.w) == __uint_as_float(f[h].w)) &&
+                      !surely_above<V>(p.scoring, __uint_as_float(f[h].z), __uint_as_float(f[h].w), __uint_as_float(o.z),
+                                       __uint_as_float(o.w), top, z, fabsf(v));
             }
           if (__any_sync(0xffffffffu, near && !bad)) {
             const double zd = softmax ? choose_sum64<T, L>(row, p.num_experts, top) : 0.0;

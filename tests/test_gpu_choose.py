@@ -132,6 +132,25 @@ def test_many_tokens_with_a_bias_or_groups(handles, E, groups, top_groups, top_k
     assert (ids[40] == -1).all() and (w[40] == 0).all()
 
 
+@pytest.mark.parametrize("T", [70, 2561])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [24, 64, 256])
+def test_biases_that_even_out_scores(handles, E, scoring, T):
+    """Keys near one another whose logits and biases are not, and keys that 64 bits hold equal though the scores differ."""
+    torch = _t()
+    rng = np.random.default_rng([E, T])
+    x = (1.5 * rng.standard_normal(E)).astype(np.float32)
+    e = np.exp(x.astype(np.float64) - x.max())
+    s = e / e.sum() if scoring == "softmax" else 1 / (1 + np.exp(-x.astype(np.float64)))
+    rows = torch.from_numpy(x).cuda() + 2.0 ** -21 * torch.from_numpy(rng.integers(-2, 3, (T, E)).astype(np.float32)).cuda()
+    for step in (0.0, 1e-7, 1e-6, 3e-5):
+        _check(handles(E), rows, 8, bias=(1.0 - s + step * rng.integers(-9, 10, E)).astype(np.float32), scoring=scoring)
+    far = torch.from_numpy((rng.uniform(-60, -50, (T, E))).astype(np.float32)).cuda()
+    if scoring == "softmax":
+        far[:, E // 2] = 0.0
+    _check(handles(E), far, 8, bias=np.ones(E, np.float32), scoring=scoring, renormalise=False)
+
+
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("E,groups,top_groups,top_k", [(64, 1, 1, 8), (100, 1, 1, 5), (128, 1, 1, 8), (40, 8, 5, 8)])
 def test_many_tokens_with_a_few_near_keys(handles, E, groups, top_groups, top_k, scoring):
