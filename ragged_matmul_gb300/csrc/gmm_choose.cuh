@@ -541,8 +541,9 @@ __global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (L == 8 && V <
       float of = far;   // what a group's error grows with: of a sum the terms' magnitudes, which may cancel
       if constexpr (kScore) of = fabsf(g1) + (pair && g2 > -INFINITY ? fabsf(g2) : 0.0f);
       of = __uint_as_float(lanes_max<L>((keep || gk == out) && of < INFINITY ? __float_as_uint(of) : 0u));
-      // Without a bias relative: 1e-6, and of softmax's exponentials half a step of their argument.
-      const float tol = kScore ? 2.0f * (score_tol + 2.4e-7f * of) : a * (1e-6f + 1.3e-7f * of);
+      // Without a bias relative: 1e-6, and of softmax's exponentials half a step of their argument; and a score below
+      // 2^-126 (1.2e-38) may be lost, two of each group.
+      const float tol = kScore ? 2.0f * (score_tol + 2.4e-7f * of) : a * (1e-6f + 1.3e-7f * of) + 5e-38f;
       const bool near = out != 0u && !(a - b > tol) && !bad;
       if (__any_sync(0xffffffffu, near)) {
         double gd;
