@@ -224,8 +224,19 @@ __device__ __forceinline__ void choose_load16(const T *row, const ChoosePlace<kV
   }
 }
 
-// Off by about 4 units in the last place (the quotient by 2); 0 below about -87.
-__device__ __forceinline__ float sigmoid32(float x) { return __fdividef(1.0f, 1.0f + expf(-x)); }
+// Off by about 4 units in the last place (the quotient by 2).  Below -20 the exponential itself (1 + exp(x) is 1 to
+// 2.1e-9), which keeps the scores under 2^-126 that the quotient makes 0.
+__device__ __forceinline__ float sigmoid32(float x) {
+  const float e = expf(x < -20.0f ? x : -x);
+  return x < -20.0f ? e : __fdividef(1.0f, 1.0f + e);
+}
+// A chosen expert's score over a factor that the token's others share, m the largest chosen logit: relative to m's score
+// (softmax, and sigmoids that are exponentials all), else times 2^64, so that small ones keep their bits next to m's.
+__device__ __forceinline__ float relative_score(bool softmax, float x, float m) {
+  if (softmax || m < -20.0f) return expf(x - m);
+  const float e = expf(0.5f * x);
+  return x < -20.0f ? e * (e * 0x1p64f) : sigmoid32(x) * 0x1p64f;
+}
 // For keys, which allow for its error: 2.7e-7 at most (the exponential of 2^-22 relative and 2^-24 a unit of x,
 // times s (1 - s); the sum half a step, the quotient one unit in the last place).
 __device__ __forceinline__ float sigmoid_key(float x) {
@@ -818,13 +829,10 @@ __global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (L == 8 && V <
   if (id < 0) xj = -INFINITY;
   float wj;
   if (p.renormalise) {
-    // Scores relative to the largest chosen logit's: the sum is not below 1 (softmax).  Sigmoids of
-    // logits below -80 are exp(x) to within their last bit, and taken so before they underflow.
     float m = xj;
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (id < 0) wj = 0.0f;
-    else wj = softmax || m < -80.0f ? expf(xj - m) : sigmoid32(xj);
+    wj = id < 0 ? 0.0f : relative_score(softmax, xj, m);
     const float sum = lanes_sum<L>(wj);
     if (id >= 0) wj = wj / sum;
   } else {
@@ -904,8 +912,7 @@ __global__ void __launch_bounds__(32 * kChooseWarps) gmm_route_grad_kernel(const
     float m = id >= 0 ? xj : -INFINITY;
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const bool ratio = p.scoring == kScoreSoftmax || m < -80.0f;
-    const float s = id >= 0 ? (ratio ? expf(xj - m) : sigmoid32(xj)) : 0.0f;
+    const float s = id >= 0 ? relative_score(p.scoring == kScoreSoftmax, xj, m) : 0.0f;
     const float sum = lanes_sum<L>(s);
     const float u = id >= 0 ? s / sum : 0.0f;
     const float mean = lanes_sum<L>(id >= 0 ? u * g : 0.0f);

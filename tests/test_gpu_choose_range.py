@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from tests import choose_util as cu
-from tests.test_gpu_choose import _check, _check_grad, _dtype, handles  # noqa: F401
+from tests.test_gpu_choose import _check, _dtype, _rtol, handles  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +36,43 @@ def test_a_score_that_32_bits_drop(handles):  # noqa: F811
     x = [[-87.0, -87.0, -90.0, -90.0, -86.5, -87.5, -90.0, -90.0]]
     ids, _ = _check(handles(8), _cuda(x, "bf16"), 2, scoring="sigmoid", groups=2, top_groups=1, group_top=2)
     assert ids.tolist() == [[4, 5]]
+
+
+def _check_sigmoid_grad(h, x, ids, dw, renormalise):
+    """As _check_grad, for distinct chosen experts.  Its reference takes 1 - s of a score s near 1, which is off by up to
+    2^-53: of a logit of 29, whose 1 - s is 2.5e-13, more than the bound allows.  Here it is the sigmoid of -x."""
+    from ragged_matmul_gb300 import binding
+    d = _t().full_like(x, float("nan"))
+    binding.gmm_route_grad(h, d, dw, ids, x, scoring="sigmoid", renormalise=renormalise)
+    assert binding.gmm_query_status(h) == binding.GMM_OK
+    xs, at, g = x.double().cpu().numpy(), ids.cpu().numpy(), dw.double().cpu().numpy()
+    xj = np.take_along_axis(xs, at, 1)
+    s, rest = 1.0 / (1.0 + np.exp(-xj)), 1.0 / (1.0 + np.exp(xj))
+    if renormalise:
+        u = s / s.sum(1, keepdims=True)
+        dj, mj = u * (g - (u * g).sum(1, keepdims=True)) * rest, u * (np.abs(g) + (u * np.abs(g)).sum(1, keepdims=True)) * rest
+    else:
+        dj, mj = g * s * rest, np.abs(g) * s * rest
+    want, mag = np.zeros_like(xs), np.zeros_like(xs)
+    np.put_along_axis(want, at, dj, 1)
+    np.put_along_axis(mag, at, mj, 1)
+    info = _t().finfo(x.dtype)
+    bound = mag * 3 * (_rtol(xs, xs.shape[1]) + 2.0 ** -24 * 40)
+    err = np.abs(d.double().cpu().numpy() - want)
+    assert np.all(err <= bound + (np.abs(want) + bound) * info.eps / 2 + info.tiny * info.eps + 1e-37), float((err - bound).max())
+
+
+@pytest.mark.parametrize("T", [40, 2561])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_weights_of_sigmoids_around_the_smallest_normal(handles, dtype, T):  # noqa: F811
+    """Chosen logits on both sides of ln 2^-126 = -87.3: a score that fp32 would drop has up to a thousandth of the weight."""
+    torch = _t()
+    rng = np.random.default_rng([T, 32])
+    x = rng.uniform(-100.0, -86.0, (T, 12))
+    x[:, 3:6] = rng.uniform(-81.0, -60.0, (T, 3))
+    x[::5, 4] = rng.uniform(-30.0, 30.0, len(range(0, T, 5)))
+    x = _cuda(x, dtype)
+    for renormalise in (True, False):
+        ids, _ = _check(handles(12), x, 8, scoring="sigmoid", renormalise=renormalise)
+        dw = torch.from_numpy(rng.standard_normal((T, 8)).astype(np.float32)).cuda()
+        _check_sigmoid_grad(handles(12), x, ids, dw, renormalise)
