@@ -546,16 +546,16 @@ __global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (L == 8 && V <
     }
     bool keep = mine < p.groups && rank < p.top_groups;
     if (kScore || pair) {
-      // The last group kept and the first one left out: near enough to be the other way round?
-      const uint32_t out = lanes_max<L>(keep || mine >= p.groups ? 0u : gk), in = ~lanes_max<L>(keep ? ~gk : 0u);
-      const float a = key_value(in), b = key_value(out);
-      float of = far;   // what a group's error grows with: of a sum the terms' magnitudes, which may cancel
-      if constexpr (kScore) of = fabsf(g1) + (pair && g2 > -INFINITY ? fabsf(g2) : 0.0f);
-      of = __uint_as_float(lanes_max<L>((keep || gk == out) && of < INFINITY ? __float_as_uint(of) : 0u));
-      // Without a bias relative: 1e-6, and of softmax's exponentials half a step of their argument; and a score below
-      // 2^-126 (1.2e-38) may be lost, two of each group.
-      const float tol = kScore ? 2.0f * (score_tol + 2.4e-7f * of) : a * (1e-6f + 1.3e-7f * of) + 5e-38f;
-      const bool near = out != 0u && !(a - b > tol) && !bad;
+      // Is one left out near enough to one kept that they might be the other way round?  `err`: how far a group's sum may
+      // be off, with a bias as its terms are (they may cancel), else relative (3.6e-7 and half a step of the exponentials'
+      // argument; sigmoids 4.8e-7; half a step more as it is added), and by two scores below 2^-126 (1.2e-38), which
+      // fp32 may lose.
+      float err;
+      if constexpr (kScore) err = score_tol + 2.4e-7f * (fabsf(g1) + (pair && g2 > -INFINITY ? fabsf(g2) : 0.0f));
+      else err = gv * (6e-7f + 6.5e-8f * far) + 2.5e-38f;
+      const uint32_t high = lanes_max<L>(keep || gk == 0u ? 0u : order_key(gv + err));    // 0: none left out that has an expert
+      const uint32_t low = ~lanes_max<L>(keep ? ~order_key(gv - err) : 0u);               // 0 for NaN: an infinite bias
+      const bool near = high != 0u && high >= low && !bad;
       if (__any_sync(0xffffffffu, near)) {
         double gd;
         if constexpr (kScore) {

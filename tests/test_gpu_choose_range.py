@@ -76,3 +76,13 @@ def test_weights_of_sigmoids_around_the_smallest_normal(handles, dtype, T):  # n
         ids, _ = _check(handles(12), x, 8, scoring="sigmoid", renormalise=renormalise)
         dw = torch.from_numpy(rng.standard_normal((T, 8)).astype(np.float32)).cuda()
         _check_sigmoid_grad(handles(12), x, ids, dw, renormalise)
+
+
+@pytest.mark.parametrize("T", [3, 2561])
+def test_a_group_left_out_whose_terms_cancel(handles, T):  # noqa: F811
+    """The last group's fp32 sum is 1.5, below the two before it, of which the better one is kept; its exact sum, 1.5003,
+    is the largest.  Its error is far above that of the others."""
+    logit = np.log1p(4e-4 * 2) * np.array([0.0, 0.0, 0.0, 0.0, -9.0, -9.0, 1.0, 0.5])       # scores 0.5 + 2e-4, 0.5 + 1e-4
+    bias = np.array([0.25, 0.2501, 0.25, 0.25005, 0.0, 0.0, 4096.0, -4095.5], np.float32)
+    ids, _ = _check(handles(8), _cuda(np.tile(logit, (T, 1))), 2, bias=bias, scoring="sigmoid", groups=4, top_groups=1, group_top=2)
+    assert (ids.cpu() == _t().tensor([6, 7], dtype=_t().int32)).all()
