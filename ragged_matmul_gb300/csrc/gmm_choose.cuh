@@ -525,8 +525,8 @@ __global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (L == 8 && V <
     const bool pair = p.group_top == 2;
     float far = 0.0f, gv = g1;   // far: how far below the largest logit the group's is
     if (pair) {
-      if constexpr (kScore) {
-        gv = g2 > -INFINITY ? g1 + g2 : g1;
+      if constexpr (kScore) {   // a sum below fp32's lowest value is not that of a group without experts
+        gv = g2 > -INFINITY ? fmaxf(g1 + g2, -3.402823466e38f) : g1;
       } else if (softmax) {   // scores relative to the largest logit's
         float m = g1;
 #pragma unroll

@@ -86,3 +86,21 @@ def test_a_group_left_out_whose_terms_cancel(handles, T):  # noqa: F811
     bias = np.array([0.25, 0.2501, 0.25, 0.25005, 0.0, 0.0, 4096.0, -4095.5], np.float32)
     ids, _ = _check(handles(8), _cuda(np.tile(logit, (T, 1))), 2, bias=bias, scoring="sigmoid", groups=4, top_groups=1, group_top=2)
     assert (ids.cpu() == _t().tensor([6, 7], dtype=_t().int32)).all()
+
+
+@pytest.mark.parametrize("T", [3, 2561])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_group_sums_that_fp32_cannot_hold(handles, scoring, T):  # noqa: F811
+    """Biases of the type's lowest and largest value: a sum of two is a finite 64-bit number, not -infinity (no expert at
+    all) and not equal to another such sum."""
+    low, inf = float(np.finfo(np.float32).min), np.inf
+    x = _cuda(np.random.default_rng([T, 33]).standard_normal((T, 8)))
+    for bias in ([0, 0, -inf, -inf, low, low, -inf, -inf],         # the third group has experts
+                 [0, 0, low, low, low, 0.99 * low, -inf, -inf],
+                 [0, 0, low, low, 0.99 * low, 0.99 * low, 2, 2],
+                 [-low, -0.9 * low, 0, 0, -low, -low, -0.9 * low, -low],
+                 [low, low, low, -inf, -inf, -inf, low, low]):
+        for top_groups in (1, 2, 3):
+            _check(handles(8), x, 2, bias=np.array(bias, np.float32), scoring=scoring, groups=4, top_groups=top_groups, group_top=2)
+            if top_groups > 1:
+                _check(handles(8), x, 4, bias=np.array(bias, np.float32), scoring=scoring, groups=4, top_groups=top_groups, group_top=2)
