@@ -534,7 +534,10 @@ int gmm_run_noalloc(void *c, const void *a, const uint32_t *a_offsets, const voi
  * only the device sees: decreasing offsets and out-of-range expert ids, and a
  * kernel that gave up on a pipeline wait.
  * Synchronise `stream`, then read and clear the device status that the kernels of
- * this handle accumulated since the last query.  Returns GMM_OK,
+ * this handle accumulated since the last query.  It speaks for the work that is ordered
+ * before it on `stream`: where calls of one handle overlap on several streams, join them
+ * first.  What a call on another stream reports meanwhile is in this answer or stays for
+ * the next query.  Returns GMM_OK,
  * GMM_ERR_BAD_INPUT or GMM_ERR_DEVICE_TIMEOUT (timeout wins when both are set),
  * or GMM_ERR_CUDA when the synchronisation or the copy fails (for instance after
  * an earlier asynchronous fault).

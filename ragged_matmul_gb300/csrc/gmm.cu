@@ -38,9 +38,7 @@ constexpr size_t kTileCounterOffset = 64;
 constexpr size_t kDenseRoutingOffset = 128;   // gmm_matmul_int4: a_offsets {0, M} and expert id 0
 constexpr size_t kDenseStatsOffset = 144;     // and its usage stats (written, never read)
 
-}  // namespace
-
-namespace {
+__global__ void gmm_clear_status_kernel(uint32_t *status, uint32_t bits) { atomicAnd(status, ~bits); }
 
 // Token (A) map, 128-byte swizzle.  The row extent and the box height written here
 // are placeholders: each CTA derives one map per box height from it and patches the
@@ -1143,9 +1141,16 @@ int gmm_query_status(gmm_handle_t h, cudaStream_t stream) {
   if (!h) return GMM_ERR_INVALID_ARG;
   DeviceGuard guard(h->device);
   uint32_t status = 0;
-  if (cudaMemcpyAsync(&status, h->ws, sizeof(status), cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
-      cudaMemsetAsync(h->ws, 0, sizeof(status), stream) != cudaSuccess ||
-      cudaStreamSynchronize(stream) != cudaSuccess) {
+  bool ok = cudaMemcpyAsync(&status, h->ws, sizeof(status), cudaMemcpyDeviceToHost, stream) == cudaSuccess &&
+            cudaStreamSynchronize(stream) == cudaSuccess;
+  if (ok && status) {
+    // Only what was read is cleared: a call on another stream may have reported since.  Done when this returns, or
+    // the clearing could take back a report of a later call.
+    void *args[2] = {&h->ws, &status};
+    ok = cudaLaunchKernel(reinterpret_cast<const void *>(gmm_clear_status_kernel), dim3(1), dim3(1), args, 0, stream) == cudaSuccess &&
+         cudaStreamSynchronize(stream) == cudaSuccess;
+  }
+  if (!ok) {
     cudaGetLastError();
     return GMM_ERR_CUDA;
   }
