@@ -306,14 +306,14 @@ __device__ __forceinline__ void set_wait_limit(uint64_t requested) {
 // suspend the thread for up to kSuspendNs (it resumes as soon as the phase
 // completes), so a waiting role does not spin on the issue slots that the dequant,
 // epilogue and MMA-issuing warps of its SM need; the abort flag and the clock are
-// checked after every test.
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *abort) {
+// checked after every test.  more_ns: beyond the limit, for a phase that is many others' work.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *abort, uint64_t more_ns = 0) {
   if (mbar_test_wait(bar, parity)) return true;   // already complete: no potentially blocking test
   if (mbar_try_wait_hint(bar, parity, kSuspendNs)) return true;
   const uint64_t t0 = global_timer_ns();
   for (;;) {
     if (*abort) return false;
-    if (global_timer_ns() - t0 > s_wait_limit_ns) {
+    if (global_timer_ns() - t0 > s_wait_limit_ns + more_ns) {
       *abort = 1;
       return false;
     }

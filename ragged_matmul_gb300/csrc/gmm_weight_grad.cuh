@@ -63,6 +63,7 @@ constexpr uint32_t kWgScaleCol = 2 * kWgAccCols;
 template <bool kBf16>
 constexpr uint32_t kWgStgBytes = 32 * 32 * (kBf16 ? 2 : 4);  // one staging buffer: 32 n x 32 k
 constexpr int kWgMaxStages = 8;
+constexpr uint64_t kWgStageNs = 4000;   // allowed for one stage of a tile (0.3 us measured, of one tile alone)
 constexpr size_t kWgFixedBytes = 1024 + kWgEntries * kWgEntryBytes;   // and the staging buffers
 static_assert(kWgScaleCol + 12 <= kTmemCols, "scales beside the accumulators");
 static_assert(kWgABytes % 1024 == 0 && kWgBBytes % 1024 == 0 && kWgStgBytes<true> % 1024 == 0, "swizzled tiles start at 1024 bytes");
@@ -345,7 +346,8 @@ __global__ void __launch_bounds__(kWgThreads, 1) gmm_weight_grad_fp8_kernel(cons
       const uint32_t taddr = tmem_base + ((quad * 32u) << 16) + acc * kWgAccCols;
       if (!zero) {
         int ok = 1;
-        if (lane == 0) ok = wait_phase(smem_addr(&ctl.acc_full[acc]), acc_phase, abort);
+        // A whole tile's wait, as long as its group.  What stops a stage ends that role's own wait, and this one by `abort`.
+        if (lane == 0) ok = wait_phase(smem_addr(&ctl.acc_full[acc]), acc_phase, abort, x.stages * kWgStageNs);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) {
           if (lane == 0) atomicOr(p.status, kStatusTimeout);
