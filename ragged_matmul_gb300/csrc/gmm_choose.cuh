@@ -405,6 +405,12 @@ __device__ __noinline__ int choose_exact(const ChooseParams &p, const T *row, fl
   return id;
 }
 
+// Slots of a token's gathered keys (key, expert, logit, bias), and those of a CTA in shared memory.
+template <int L, bool kScore>
+constexpr int kChooseTokenSlots = kScore && L < 32 ? 2 * L : L;
+template <class T, int L, bool kScore>
+constexpr int kChooseSlots = !kScore && sizeof(T) == 2 ? 1 : 32 / L * kChooseTokenSlots<L, kScore> * kChooseWarps;
+
 // One token per L lanes, 32 / L tokens a warp.  kScore: a bias, the keys are not the logits themselves.  A whole
 // warp has the shortest way through a token, eight lanes leave fewer of them idle; with a bias up to 16 experts
 // a lane, as a lane works through them one after the other (32768 tokens with a bias, 32 lanes and 8: of 64
@@ -415,8 +421,8 @@ __global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (L == 8 && V <
   constexpr bool kPacked = !kScore && sizeof(T) == 2;
   constexpr bool kKeep = kScore && L == 32;   // logits and biases stay in registers, else they are read again
   extern __shared__ unsigned long long choose_smem[];
-  constexpr int kSlots = kScore && L < 32 ? 2 * L : L;   // of a token's gathered keys: key, expert, logit, bias
-  __shared__ uint4 choose_slots[kPacked ? 1 : 32 / L * kSlots * kChooseWarps];
+  constexpr int kSlots = kChooseTokenSlots<L, kScore>;
+  __shared__ uint4 choose_slots[kChooseSlots<T, L, kScore>];
   const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
   const int sub = lane & (L - 1), seg = lane & ~(L - 1);
   const uint32_t seg_mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << seg;

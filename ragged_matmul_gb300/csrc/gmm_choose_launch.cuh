@@ -10,9 +10,10 @@ namespace gmm {
 namespace host {
 
 // Warps a CTA: fewer where a warp's `smem` bytes (64-bit keys of every expert, rows of the
-// gradient) and the kernel's own shared memory (2 KB) would not fit the default 48 KB.
-inline int choose_warps(size_t smem) {
-  return static_cast<int>(std::max<size_t>(1, std::min<size_t>(gmm::kChooseWarps, 46 * 1024 / std::max<size_t>(1, smem))));
+// gradient) and the kernel's own `own` would not fit the default 48 KB.
+constexpr size_t kChooseSmem = 48 * 1024;
+inline int choose_warps(size_t smem, size_t own) {
+  return static_cast<int>(std::max<size_t>(1, std::min<size_t>(gmm::kChooseWarps, (kChooseSmem - own) / std::max<size_t>(1, smem))));
 }
 
 // The largest share of a token's experts that one of eight lanes takes where there is a bias.
@@ -24,7 +25,12 @@ int launch_choose(gmm::ChooseParams p, bool vec, bool score, bool grad, cudaStre
   const long long warps = (p.num_tokens + 32 / L - 1) / (32 / L);
   const bool dense = p.scoring == GMM_SCORE_SOFTMAX && !p.renormalise;
   const size_t per_warp = grad ? static_cast<size_t>(32) * V * 4 : (score ? static_cast<size_t>(32 / L) * p.num_experts * 8 : 0);
-  const int wc = choose_warps(per_warp);
+  const size_t own = grad ? 0 : 16 * static_cast<size_t>(score ? gmm::kChooseSlots<T, L, true> : gmm::kChooseSlots<T, L, false>);
+  // One warp always fits: the keys of a whole warp's token, or of 32 / L tokens of as many experts as the layout is taken for.
+  static_assert(16 * gmm::kChooseSlots<T, 32, true> + 8 * gmm::kRouteMaxExperts <= kChooseSmem, "a token's keys");
+  static_assert(16 * gmm::kChooseSlots<T, 8, true> + 32 / 8 * 8 * (8 * kScoreShare8) <= kChooseSmem, "four tokens' keys");
+  static_assert(32 * gmm::kChooseMaxPerLane * 4 <= kChooseSmem, "a row of the gradient");
+  const int wc = choose_warps(per_warp, own);
   const unsigned grid = static_cast<unsigned>((warps + wc - 1) / wc), threads = 32u * wc;
   const size_t smem = per_warp * wc;
   auto go = [&](auto vec_c) {
