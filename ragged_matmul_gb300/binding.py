@@ -696,13 +696,21 @@ def gmm_run_fp4(h: Handle, c, a, a_offsets, b, expert_ids, expert_usage_stats, a
 _ROUTE_OPTIONS = {}
 
 
+def _whole(x, name):
+    """x as an int; 2.5 is refused, not cut off."""
+    i = int(x)
+    if i != x:
+        raise ValueError(f"{name} must be a whole number, got {x}")
+    return i
+
+
 def _route_options(scoring, renormalise, scale, groups=1, top_groups=1, group_top=1):
     """gmm_route_options by reference; one structure for each combination of settings."""
     key = (scoring, groups, top_groups, group_top, renormalise, scale)
     if not (type(scale) is float and type(renormalise) is bool and type(group_top) is int and type(top_groups) is int
             and type(groups) is int and type(scoring) is str):     # kept by value, whatever holds it
-        key = (scoring if isinstance(scoring, (str, int)) else None, int(groups), int(top_groups), int(group_top),
-               bool(renormalise), float(scale))
+        key = (scoring if isinstance(scoring, (str, int)) else None, _whole(groups, "expert_groups"),
+               _whole(top_groups, "top_groups"), _whole(group_top, "group_top"), bool(renormalise), float(scale))
     o = _ROUTE_OPTIONS.get(key)
     if o is None:
         s = SCORINGS.get(key[0], key[0])
@@ -802,7 +810,7 @@ def gmm_quantize_fp8(h: Handle, q, scales, x, row_slots=None, top_k: int = 1, po
     px, stride, src_rows, K, ps, rows = _gather(x, row_slots, types, dev)
     pq = _shaped(q, "q", _e4m3_types(), dev, (rows, K))
     psc = _shaped(scales, "scales", _F32, dev, (rows, -(-K // FP8_BLOCK)))
-    rc = load_library().gmm_quantize_fp8(h.ptr, pq, psc, px, stride, src_rows, ps, int(top_k), rows, K, types[x.dtype],
+    rc = load_library().gmm_quantize_fp8(h.ptr, pq, psc, px, stride, src_rows, ps, _whole(top_k, "top_k"), rows, K, types[x.dtype],
                                          int(bool(pow2)), stream_handle(dev, stream))
     if check and rc != GMM_OK:
         raise GmmError(rc, "gmm_quantize_fp8")
@@ -847,7 +855,7 @@ def gmm_quantize_fp8_cols(h: Handle, q_t, t_scales, x, a_offsets, row_slots=None
     if q is not None:
         pq = _shaped(q, "q", _e4m3_types(), dev, (rows, width))
         psc = _shaped(scales, "scales", _F32, dev, (rows, -(-width // FP8_BLOCK)))
-    rc = load_library().gmm_quantize_fp8_cols(h.ptr, pqt, pts, pq, psc, px, stride, src_rows, ps, int(top_k), po, G, rows,
+    rc = load_library().gmm_quantize_fp8_cols(h.ptr, pqt, pts, pq, psc, px, stride, src_rows, ps, _whole(top_k, "top_k"), po, G, rows,
                                               width, types[x.dtype], stream_handle(dev, stream))
     if check and rc != GMM_OK:
         raise GmmError(rc, "gmm_quantize_fp8_cols")
