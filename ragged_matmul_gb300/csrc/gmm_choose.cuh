@@ -419,7 +419,8 @@ constexpr int kChooseSlots = !kScore && sizeof(T) == 2 ? 1 : 32 / L * kChooseTok
 template <class T, int L, int V, bool kVec, bool kScore>
 __global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (L == 8 && V <= 16 ? 6 : (V <= 32 ? 4 : 1))) gmm_route_kernel(const __grid_constant__ ChooseParams p) {
   constexpr bool kPacked = !kScore && sizeof(T) == 2;
-  constexpr bool kKeep = kScore && L == 32;   // logits and biases stay in registers, else they are read again
+  constexpr bool kLong = V > 32;   // a lane's keys fill its registers (with biases and logits beside them its stack passed 2 KB)
+  constexpr bool kKeep = kScore && L == 32 && !kLong;   // logits and biases stay in registers, else they are read again
   extern __shared__ unsigned long long choose_smem[];
   constexpr int kSlots = kChooseTokenSlots<L, kScore>;
   __shared__ uint4 choose_slots[kChooseSlots<T, L, kScore>];
@@ -442,8 +443,8 @@ __global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (L == 8 && V <
   uint32_t raw[kPacked ? V / 2 : 1], key[V];
   if constexpr (kPacked) choose_load16<T, V, kVec>(row, at, raw);
   else choose_load<T, V, kVec>(row, at, x);
-  float bias[kScore ? V : 1];   // beside the logits' loads, not behind them
-  if constexpr (kScore) {
+  float bias[kScore && !kLong ? V : 1];   // beside the logits' loads, not behind them
+  if constexpr (kScore && !kLong) {
     if (kVec && V % 4 == 0 && p.bias_vec) {
 #pragma unroll
       for (int v = 0; v < V; v += 4) {
@@ -499,13 +500,17 @@ __global__ void __launch_bounds__(32 * kChooseWarps, V <= 8 ? 8 : (L == 8 && V <
   float score_tol = 0.0f;
   if constexpr (kScore) {
     score_tol = softmax ? 1.2e-7f * (V + 20) / z : 6e-7f;
+    auto bias_at = [&](int v) {
+      if constexpr (kLong) return at.there(v) ? __ldg(p.bias + at.expert(v)) : 0.0f;
+      else return bias[v];
+    };
     if (softmax) {
       const float rz = 1.0f / z;
 #pragma unroll
-      for (int v = 0; v < V; ++v) key[v] = x[v] > -INFINITY ? order_key(__expf(x[v] - top) * rz + bias[v]) : 0u;
+      for (int v = 0; v < V; ++v) key[v] = x[v] > -INFINITY ? order_key(__expf(x[v] - top) * rz + bias_at(v)) : 0u;
     } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) key[v] = x[v] > -INFINITY ? order_key(sigmoid_key(x[v]) + bias[v]) : 0u;
+      for (int v = 0; v < V; ++v) key[v] = x[v] > -INFINITY ? order_key(sigmoid_key(x[v]) + bias_at(v)) : 0u;
     }
   }
 
