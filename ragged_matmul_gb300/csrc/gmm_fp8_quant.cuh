@@ -419,8 +419,8 @@ __global__ void __launch_bounds__(kQ8Threads, sizeof(T) == 2 ? 4 : 2) gmm_quanti
     }
     a = quant_bits<T>(a);
     const uint32_t code = a >= 0x7f800000u ? 0xffu : pow2_code(a);
-    // A block that is not finite: zero codes, by a mark that no inverse has.
-    inv[tid] = code == 0xffu ? -1.0f : pow2_inverse(code);
+    // A block that is not finite, or zeros of any sign: zero codes, by a mark that no inverse has.
+    inv[tid] = code == 0xffu || a == 0u ? -1.0f : pow2_inverse(code);
     if (c0 + tid < p.width) p.t_scales[static_cast<size_t>(block) * p.width + c0 + tid] = static_cast<uint8_t>(code);
   }
   __syncthreads();
