@@ -33,8 +33,8 @@
 // values.  16-bit logits carry the expert's number in their key's low half, and sorted lists of eight are
 // merged across the lanes.  Of 32-bit keys those that reach a bound are gathered, a lane each, and
 // ranked against one another, which also settles ties.
-// Measured: 32768 tokens of 128 bf16 logits, top-8, 5.7 us (their bytes
-// take 1.5); 256 tokens of 256 fp32 logits with a bias and groups 4.1 us, 5.6 with a token in 64 bits; one token
+// Measured: 32768 tokens of 128 bf16 logits, top-8, 6.0 us (their bytes
+// take 1.5); 256 tokens of 256 fp32 logits with a bias and groups 4.4 us, 5.6 with a token in 64 bits; one token
 // 1.8 us, about an empty launch.
 #pragma once
 
